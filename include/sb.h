@@ -312,6 +312,68 @@ size_t sb_partial_workspace_bytes(const sb_partial_desc *desc, sb_status *status
 sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, int64_t ldo,
                               void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training surface: softmax cross entropy over the whole vocabulary and its
+ * gradient.  The logits are never written to memory.
+ *   lse[b]  = log sum_v exp(z[b][v])
+ *   loss[b] = lse[b] - z[b][targets[b]]
+ *   dz[b][v] = (exp(z[b][v] - lse[b]) - [v == targets[b]]) * dloss[b]
+ *   dx = dz . W^T (bf16 [B][lddx]),  dw = x^T . dz (bf16, lane by lane)
+ *  - A negative target marks an ignored row (padding): its loss is 0, its row
+ *    of dx is 0 wherever W is finite, and it adds nothing to dw, whatever its
+ *    x holds.  Its lse is computed like any other.  A target >= V makes the
+ *    row's loss, its row of dx and all of dw NaN.
+ *  - Logits are fp32 sums of exact bf16 x bf16 products, in an order fixed by
+ *    H (not the order of the projection calls: last bits can differ from
+ *    theirs).  lse is an online sum over 256-column blocks.  The gradient
+ *    computes the logits again, in pieces of the vocabulary, rounds dz to bf16
+ *    (off by at most 2^-8 of its value, as each bf16 result is) and
+ *    accumulates dx and dw in fp32; each is rounded once.  Repeated calls give
+ *    the same bits.
+ *  - Non-finite logits follow IEEE rules: a row with a NaN or +inf logit has a
+ *    NaN lse; -inf logits count as probability 0.
+ * The head descriptor and its limits are the projection calls'; the gradient
+ * also needs 256 shard rows to span less than 4 GiB (SB_ERR_UNSUPPORTED).
+ * H == 0 gives all-zero logits; dx and dw are then empty.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Bytes of device workspace of sb_cross_entropy (grad == 0) or
+ * sb_cross_entropy_grad (grad != 0); 0 for B == 0.  On an invalid descriptor
+ * returns 0 and sets *status (if not NULL).
+ */
+size_t sb_cross_entropy_workspace_bytes(const sb_head_desc *desc, int grad, sb_status *status);
+
+/*
+ *   targets  DEVICE int32 [B]
+ *   loss     DEVICE fp32 [B]
+ *   lse      DEVICE fp32 [B]
+ *   ws       >= sb_cross_entropy_workspace_bytes(desc, 0), 16-byte aligned
+ */
+sb_status sb_cross_entropy(const sb_head_desc *desc, const int32_t *targets, float *loss, float *lse,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/*
+ *   targets  DEVICE int32 [B]
+ *   lse      DEVICE fp32 [B], as sb_cross_entropy returned it
+ *   dloss    DEVICE fp32 [B], the gradient of each row's loss (1 / rows for
+ *            a mean)
+ *   dx       DEVICE bf16 [B][lddx] or NULL; lddx >= H, a multiple of 8;
+ *            16-byte aligned
+ *   dw       HOST array of k DEVICE pointers or NULL; dw[i] is lane i's
+ *            gradient, bf16 [H][lddw], laid out as w[i]; lddw >= every lane's
+ *            width, a multiple of 8; 16-byte aligned
+ *   ws       >= sb_cross_entropy_workspace_bytes(desc, 1), 16-byte aligned
+ * At least one of dx and dw is required.  Both are overwritten, not added to
+ * (B == 0 zeroes dw).  Columns past H in dx and past a lane's width in dw are
+ * left as they were.
+ */
+sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets, const float *lse,
+                                const float *dloss, void *dx, int64_t lddx, void *const *dw,
+                                int64_t lddw, void *ws, size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *sb_status_string(sb_status status);
 

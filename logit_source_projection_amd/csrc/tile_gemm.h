@@ -1,0 +1,358 @@
+// The MFMA tile product of the loss, gradient and 8-bit kernels (gfx950).
+//
+// One workgroup = 8 waves = a 256 x 256 tile of C[m][n] = sum_k A[m][k] B[n][k].
+// Operands come in two layouts, either way without a copy in memory:
+//   * kAlongK:   k contiguous, rows of the operand `ld` apart (X in X.W, both
+//                operands of dZ.W^T, both int8 operands);
+//   * kAcrossK:  rows of the operand contiguous, k steps `ld` apart (W in X.W,
+//                both operands of X^T.dZ).
+// K advances in stages of 128 bytes per row (64 bf16 or 128 int8) through two
+// LDS stages of 64 KB, filled by direct-to-LDS buffer loads of 1 KB.
+//
+// What bounds it: a stage is 64 MFMAs per wave (2 x 8 x 4 blocks of 16 x 16 x
+// 32 bf16), about 2048 cycles with two waves per SIMD, and 24 KB of fragment
+// reads per wave, about 1536 cycles of the CU's LDS port.  They only overlap
+// if a wave's reads run beside its own MFMAs, so each 32-deep half of a stage
+// is computed while the other half's fragments arrive: the reads of half h + 1
+// are issued between the MFMAs of half h.  The one barrier of a stage sits
+// between its halves, where the wave already holds the second half in
+// registers: behind it the stage's slot is free and is refilled two stages
+// ahead, so a load has a whole stage of time.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+namespace sbk {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 256;             // rows and columns of a workgroup's tile
+constexpr int kTileWaves = 8;          // 2 (rows) x 4 (columns) waves of 128 x 64
+constexpr int kTileThreads = kTileWaves * 64;
+constexpr int kStageBytes = 128;       // K bytes of a row per stage
+constexpr int kStageK = 64;            // bf16 K steps per stage
+constexpr int kOperandBytes = kTile * kStageBytes;      // one operand's stage
+constexpr int kTileLdsBytes = 2 * 2 * kOperandBytes;    // two stages of two operands
+constexpr int kRowBlocks = 8;          // 16-row blocks of a wave
+constexpr int kColBlocks = 4;          // 16-column blocks of a wave
+
+enum Layout : int { kAlongK = 0, kAcrossK = 1 };
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes)
+{
+    const uint32_t n = bytes <= 0 ? 0u : (bytes >= 0xFFFFFFFFll ? 0xFFFFFFFFu : (uint32_t)bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n,
+                                             0x00020000);  // raw buffer, 32-bit data format
+}
+
+// Raises a kernel's dynamic-LDS limit on the current device, once per device
+// (devices past 63 set it on every call; concurrent first calls may both).
+inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit))
+        return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess && bit)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// Workgroup order.  Workgroup ids are handed to the 8 XCDs round-robin, so
+// XCD x = id % 8 runs ids x, x + 8, ...  The tiles are numbered in bands of
+// `pm` tile rows, column by column inside a band, and every XCD takes an equal
+// run of consecutive numbers: the 32 tiles it runs at a time (one per CU) form
+// a patch of about pm x (32 / pm) tiles, which share their operands' stages in
+// the XCD's L2, and no XCD has more tiles than another.  A placement hint
+// only: any bijection gives the same results.
+// ---------------------------------------------------------------------------
+struct TileGrid {
+    int mt, nt;  // tiles in m and n
+    int pm;      // tile rows of a band
+};
+
+inline TileGrid tile_grid(int64_t m, int64_t n)
+{
+    TileGrid g;
+    g.mt = (int)((m + kTile - 1) / kTile);
+    g.nt = (int)((n + kTile - 1) / kTile);
+    g.pm = g.mt < 8 ? (g.mt > 0 ? g.mt : 1) : 8;
+    return g;
+}
+
+inline int64_t tile_count(const TileGrid &g) { return (int64_t)g.mt * g.nt; }
+
+// Workgroups of a launch over `tiles` tiles (up to 7 of them without one).
+inline int64_t xcd_ids(int64_t tiles) { return (tiles + 7) / 8 * 8; }
+
+// The tile number of workgroup `id`, or -1.
+__device__ __forceinline__ int xcd_tile(int id, int tiles)
+{
+    const int per = (tiles + 7) / 8, t = (id & 7) * per + (id >> 3);
+    return t < tiles ? t : -1;
+}
+
+__device__ __forceinline__ void tile_of(const TileGrid &g, int number, int &mt, int &nt)
+{
+    const int band = number / (g.pm * g.nt), r = number - band * (g.pm * g.nt);
+    const int h = min(g.pm, g.mt - band * g.pm);
+    mt = band * g.pm + r % h;
+    nt = r / h;
+}
+
+// ---------------------------------------------------------------------------
+// Stage layouts in LDS.
+//   kAlongK:  row r at r * 128, its 16-byte piece p in slot p ^ ((r / 2) & 7):
+//     the 16 rows of a fragment read (ds_read_b128) hit distinct banks.
+//   kAcrossK: k step at k * 512 (256 rows of 2 bytes), its 32-byte unit u (16
+//     rows) in slot u ^ across_swz(k): the 16 k steps of a transposing read
+//     (ds_read_b64_tr_b16) hit distinct banks.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int across_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+
+// This wave's four 1 KB loads of a stage: byte offsets from the stage's base.
+template <int LAYOUT>
+__device__ __forceinline__ void stage_offsets(uint32_t (&vo)[4], int wave, int L, int64_t ld_bytes)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = 4 * wave + i;
+        if (LAYOUT == kAlongK) {
+            const int r = 8 * j + (L >> 3);
+            const int p = (L & 7) ^ ((r >> 1) & 7);
+            vo[i] = (uint32_t)((int64_t)r * ld_bytes + 16 * p);
+        } else {
+            const int k = 2 * j + (L >> 5);
+            const int u = ((L & 31) >> 1) ^ across_swz(k);
+            vo[i] = (uint32_t)((int64_t)k * ld_bytes + 32 * u + 16 * (L & 1));
+        }
+    }
+}
+
+__device__ __forceinline__ void stage_load(uint8_t *lds, __amdgpu_buffer_rsrc_t r,
+                                           const uint32_t (&vo)[4], int wave)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (__attribute__((address_space(3))) void *)(lds + (4 * wave + i) * 1024), 16, vo[i],
+            0, 0, 0);
+}
+
+// Zero the K bytes at and past `kbytes` (< 128) of a kAlongK stage: what lies
+// there in memory is a row's padding or the next row, which may be any bits.
+__device__ __forceinline__ void zero_stage_tail(uint8_t *lds, int kbytes)
+{
+    for (int idx = threadIdx.x; idx < kTile * 8; idx += kTileThreads) {
+        const int r = idx >> 3, p = idx & 7;
+        if (16 * p + 16 <= kbytes)
+            continue;
+        uint8_t *piece = lds + r * kStageBytes + (p ^ ((r >> 1) & 7)) * 16;
+        if (16 * p >= kbytes) {
+            *reinterpret_cast<u32x4 *>(piece) = u32x4{0u, 0u, 0u, 0u};
+        } else {
+            for (int e = kbytes - 16 * p; e < 16; ++e)
+                piece[e] = 0;
+        }
+    }
+}
+
+typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+
+// Four 16-bit values of a column of the 4 x 16 block whose 16-byte row quarters
+// the 16 lanes of a group point at.  The restrict pointer gives the read alias
+// information of its own, without which the compiler makes it wait for every
+// load into LDS that is in flight; run() orders the two itself.
+__device__ __forceinline__ s16x4 read_across(lds_s16x4 __restrict p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
+// Fragment reader of NB 16-row blocks from operand row `row0` on (a multiple
+// of 16 * NB): lane L gets row L % 16 of a block, K bytes 16 * (L / 16) .. of
+// the half's 64.
+template <int LAYOUT, int NB>
+struct FragReader {
+    uint32_t at;  // the lane's byte offset inside a stage, block 0, half 0
+
+    __device__ __forceinline__ void init(int row0, int L)
+    {
+        const int n = L & 15, g = L >> 4;
+        if (LAYOUT == kAlongK)
+            at = (uint32_t)((row0 + n) * kStageBytes + ((g ^ ((n >> 1) & 7)) * 16));
+        else  // k = 8 g + n / 4 (+ 4 for the second read), rows 4 (n % 4) .. + 3 of the block
+            at = (uint32_t)((8 * g + (n >> 2)) * 512 +
+                            (((row0 / 16) ^ across_swz(8 * g + (n >> 2))) * 32) + (n & 3) * 8);
+    }
+    __device__ __forceinline__ u32x4 read(const uint8_t *stage, int half, int block) const
+    {
+        if (LAYOUT == kAlongK)
+            return *reinterpret_cast<const u32x4 *>(stage + (at ^ (uint32_t)(half * 64)) +
+                                                    block * 16 * kStageBytes);
+        // block < NB and row0 / 16 is a multiple of NB: the block number only
+        // flips bits of the swizzled slot
+        const uint8_t *p = stage + (at ^ (uint32_t)(block * 32)) + half * 32 * 512;
+        const s16x4 lo = read_across((lds_s16x4)p);
+        const s16x4 hi = read_across((lds_s16x4)(p + 4 * 512));
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+        return u32x4{a[0], a[1], b[0], b[1]};
+    }
+};
+
+// One 16 x 16 block step: 32 bf16 or 64 int8 K values.  The column operand
+// goes first, so a lane holds four consecutive columns of one row.
+__device__ __forceinline__ void block_mma(f32x4 &c, const u32x4 &row, const u32x4 &col)
+{
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, col),
+                                                __builtin_bit_cast(bf16x8, row), c, 0, 0, 0);
+}
+__device__ __forceinline__ void block_mma(i32x4 &c, const u32x4 &row, const u32x4 &col)
+{
+    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, col),
+                                              __builtin_bit_cast(i32x4, row), c, 0, 0, 0);
+}
+
+constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;
+
+// The accumulators of a wave: acc[rb][cb] holds, for lane L, row 16 rb + L % 16
+// and columns 16 cb + 4 (L / 16) .. + 3 of the wave's 128 x 64 part.
+template <typename Acc>
+struct WaveTile {
+    Acc acc[kRowBlocks][kColBlocks];
+    int wave, L, row0, col0;  // the wave's first row and column inside the tile
+
+    __device__ __forceinline__ void init()
+    {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        L = threadIdx.x & 63;
+        row0 = (wave >> 2) * (16 * kRowBlocks);
+        col0 = (wave & 3) * (16 * kColBlocks);
+#pragma unroll
+        for (int rb = 0; rb < kRowBlocks; ++rb)
+#pragma unroll
+            for (int cb = 0; cb < kColBlocks; ++cb)
+                acc[rb][cb] = Acc{};
+    }
+
+    // Stages 0 .. nst - 1.  src.a(st) / src.b(st) give the buffers of stage st
+    // (their base the stage's first K step; empty from nst on), called once
+    // for each stage in ascending order; src.tail(st) the valid K bytes of
+    // stage st (>= 128 where nothing has to be zeroed): the kAlongK operands
+    // named by ZA / ZB are zeroed past it.
+    template <int LA, int LB, bool ZA, bool ZB, typename Src>
+    __device__ __forceinline__ void run(uint8_t *lds, int nst, int64_t lda_bytes, int64_t ldb_bytes,
+                                        Src &src)
+    {
+        if (nst <= 0)
+            return;
+        uint32_t va[4], vb[4];
+        stage_offsets<LA>(va, wave, L, lda_bytes);
+        stage_offsets<LB>(vb, wave, L, ldb_bytes);
+        FragReader<LA, kRowBlocks> ra;
+        FragReader<LB, kColBlocks> rb_;
+        ra.init(row0, L);
+        rb_.init(col0, L);
+        auto fill = [&](int st, __amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b) {
+            uint8_t *slot = lds + (st & 1) * (2 * kOperandBytes);
+            stage_load(slot, a, va, wave);
+            stage_load(slot + kOperandBytes, b, vb, wave);
+        };
+        auto mend = [&](int st) {  // a stage whose K range ends inside it
+            const int kb = src.tail(st);
+            if (__builtin_expect(kb < kStageBytes, 0)) {
+                uint8_t *slot = lds + (st & 1) * (2 * kOperandBytes);
+                if (ZA)
+                    zero_stage_tail(slot, kb);
+                if (ZB)
+                    zero_stage_tail(slot + kOperandBytes, kb);
+                __syncthreads();
+            }
+        };
+        fill(0, src.a(0), src.b(0));
+        fill(1, src.a(1), src.b(1));             // (empty where there is no stage 1)
+        __builtin_amdgcn_s_waitcnt(0x0f70 | 8);  // vmcnt(8): stage 0 has landed
+        __syncthreads();
+        mend(0);
+        u32x4 fa[2][kRowBlocks], fb[2][kColBlocks];
+        read_half<LA, LB>(fa[0], fb[0], ra, rb_, lds, 0, 0);
+        for (int st = 0; st < nst; ++st) {
+            // first half, beside the reads of the second
+            read_half<LA, LB>(fa[1], fb[1], ra, rb_, lds, st & 1, 1);
+            mma_half(fa[0], fb[0]);
+            interleave<LA, LB, false>();
+            const __amdgpu_buffer_rsrc_t na = src.a(st + 2), nb = src.b(st + 2);
+            // The next stage has landed (its loads are a stage old) and every
+            // wave holds the rest of this one in registers.
+            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+            __syncthreads();
+            if (st + 1 < nst)
+                mend(st + 1);
+            // second half, beside the reads of the next stage's first (past
+            // the last stage: zeros, never used)
+            fill(st, na, nb);
+            read_half<LA, LB>(fa[0], fb[0], ra, rb_, lds, (st + 1) & 1, 0);
+            mma_half(fa[1], fb[1]);
+            interleave<LA, LB, true>();
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __syncthreads();  // LDS is the caller's
+    }
+
+private:
+    template <int LA, int LB>
+    static __device__ __forceinline__ void read_half(u32x4 (&fa)[kRowBlocks], u32x4 (&fb)[kColBlocks],
+                                                     const FragReader<LA, kRowBlocks> &ra,
+                                                     const FragReader<LB, kColBlocks> &rb_,
+                                                     const uint8_t *lds, int slot, int half)
+    {
+        const uint8_t *sa = lds + slot * (2 * kOperandBytes), *sb = sa + kOperandBytes;
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb)
+            fb[cb] = rb_.read(sb, half, cb);
+#pragma unroll
+        for (int rb = 0; rb < kRowBlocks; ++rb)
+            fa[rb] = ra.read(sa, half, rb);
+    }
+    __device__ __forceinline__ void mma_half(const u32x4 (&fa)[kRowBlocks],
+                                             const u32x4 (&fb)[kColBlocks])
+    {
+#pragma unroll
+        for (int rb = 0; rb < kRowBlocks; ++rb)
+#pragma unroll
+            for (int cb = 0; cb < kColBlocks; ++cb)
+                block_mma(acc[rb][cb], fa[rb], fb[cb]);
+    }
+    // Asks the scheduler for the half's LDS reads to be spread over its MFMAs
+    // (FILL: after the refill's loads).
+    template <int LA, int LB, bool FILL>
+    static __device__ __forceinline__ void interleave()
+    {
+        constexpr int reads = kRowBlocks * (LA == kAcrossK ? 2 : 1) + kColBlocks * (LB == kAcrossK ? 2 : 1);
+        constexpr int per = (reads + kRowBlocks - 1) / kRowBlocks;
+        if (FILL)
+            __builtin_amdgcn_sched_group_barrier(kSchedVmem, 8, 0);
+#pragma unroll
+        for (int i = 0; i < kRowBlocks; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kSchedDsRead, per, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedMfma, kColBlocks, 0);
+        }
+    }
+};
+
+}  // namespace
+}  // namespace sbk

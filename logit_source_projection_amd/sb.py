@@ -40,7 +40,8 @@ REDUCE_OPS = {"sum": SB_RED_SUM, "prod": SB_RED_PROD, "min": SB_RED_MIN, "max": 
 EXPORTS = ("sb_workspace_bytes", "sb_project_tokens", "sb_project_tokens_static",
            "sb_project_lane_results",
            "sb_project_logprobs", "sb_full_logits", "sb_partial_workspace_bytes",
-           "sb_partial_complete", "sb_status_string")
+           "sb_partial_complete", "sb_cross_entropy_workspace_bytes", "sb_cross_entropy",
+           "sb_cross_entropy_grad", "sb_status_string")
 
 
 class SbError(RuntimeError):
@@ -100,6 +101,13 @@ def lib():
     L.sb_partial_workspace_bytes.argtypes = [PP, ctypes.POINTER(ctypes.c_int)]
     L.sb_partial_complete.restype = ctypes.c_int
     L.sb_partial_complete.argtypes = [PP, ctypes.c_int, vp, i64, vp, sz, vp]
+    L.sb_cross_entropy_workspace_bytes.restype = sz
+    L.sb_cross_entropy_workspace_bytes.argtypes = [P, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    L.sb_cross_entropy.restype = ctypes.c_int
+    L.sb_cross_entropy.argtypes = [P, vp, vp, vp, vp, sz, vp]
+    L.sb_cross_entropy_grad.restype = ctypes.c_int
+    L.sb_cross_entropy_grad.argtypes = [P, vp, vp, vp, vp, i64, ctypes.POINTER(vp), i64, vp, sz,
+                                        vp]
     L.sb_status_string.restype = ctypes.c_char_p
     L.sb_status_string.argtypes = [ctypes.c_int]
     _lib = L
@@ -216,6 +224,10 @@ class Head:
         if self.from_tensors:
             _operands([self.x], "x")
             _operands(self.w if isinstance(self.w, (list, tuple)) else [self.w], "w")
+
+    def tensors(self):
+        """The operands of a descriptor built from tensors."""
+        return [self.x] + _as_list(self.w) if self.from_tensors else []
 
 
 def sb_workspace_bytes(head, surface):
@@ -400,6 +412,97 @@ def sb_partial_complete(part, op, out, ws=None, stream=None):
     _check(lib().sb_partial_complete(part.ref(), code, _ptr(out), out.stride(0), _ptr(ws),
                                      ws.numel(), _stream(stream)), "sb_partial_complete")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Training surface.  These calls run on the device of their tensors, whatever
+# the current one is; a stream that is not given is that device's current one.
+# ---------------------------------------------------------------------------
+def _one_device(tensors):
+    """The device that holds every tensor of a call."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _as_list(w):
+    return list(w) if isinstance(w, (list, tuple)) else [w]
+
+
+def _run(name, device, stream, nbytes_fn, ws, call):
+    """call(workspace pointer, its size, stream) on `device`."""
+    with torch.cuda.device(device):
+        ws = _workspace(nbytes_fn, ws, device, stream)
+        _check(call(_ptr(ws), ws.numel(), _stream(stream)), name)
+
+
+def sb_cross_entropy_workspace_bytes(head, grad):
+    st = ctypes.c_int(0)
+    n = lib().sb_cross_entropy_workspace_bytes(head.ref(), int(bool(grad)), ctypes.byref(st))
+    if st.value != SB_OK:
+        raise SbError(st.value, "sb_cross_entropy_workspace_bytes")
+    return int(n)
+
+
+def cross_entropy_workspace(head, grad=False, device=None):
+    """A workspace for sb_cross_entropy, or with grad for sb_cross_entropy_grad
+    (its contents on entry do not matter)."""
+    return torch.empty(max(sb_cross_entropy_workspace_bytes(head, grad), 16), dtype=torch.uint8,
+                       device=head.x.device if device is None else device)
+
+
+def sb_cross_entropy(head, targets, loss, lse, ws=None, stream=None):
+    """loss and lse (fp32 [B]) <- softmax cross entropy of every row with its
+    target (int32 [B]; negative = ignored, loss 0).  Returns loss."""
+    head.check()
+    B = head.B
+    _vector(targets, "targets", torch.int32, B)
+    _vector(loss, "loss", torch.float32, B)
+    _vector(lse, "lse", torch.float32, B)
+    _vector(ws, "ws", torch.uint8, 0)
+    dev = _one_device([targets, loss, lse, ws] + head.tensors())
+    _run("sb_cross_entropy", dev, stream, lambda: sb_cross_entropy_workspace_bytes(head, False), ws,
+         lambda p, n, s: lib().sb_cross_entropy(head.ref(), _ptr(targets), _ptr(loss), _ptr(lse), p,
+                                                n, s))
+    return loss
+
+
+def sb_cross_entropy_grad(head, targets, lse, dloss, dx=None, dw=None, ws=None, stream=None):
+    """dx (bf16 [B, H]) and / or dw <- the gradient of sum(dloss * loss).  dw
+    has the head weight's form: one bf16 [H, V] tensor, or a list of one
+    [H, V_i] tensor per lane with a common row stride.  lse is what
+    sb_cross_entropy returned; dloss (fp32 [B]) the gradient of each row's
+    loss.  Returns (dx, dw)."""
+    head.check()
+    B, H, V, off = head.B, head.desc.H, head.V, head.lane_off
+    _vector(targets, "targets", torch.int32, B)
+    _vector(lse, "lse", torch.float32, B)
+    _vector(dloss, "dloss", torch.float32, B)
+    _matrix(dx, "dx", torch.bfloat16, B, H)
+    _vector(ws, "ws", torch.uint8, 0)
+    dws, ptrs, lddw = [], None, 0
+    if isinstance(dw, (list, tuple)):
+        dws = list(dw)
+        if len(dws) != len(off) - 1:
+            raise ValueError(f"dw must hold one tensor per lane, {len(off) - 1}")
+        for i, t in enumerate(dws):
+            _matrix(t, f"dw[{i}]", torch.bfloat16, H, off[i + 1] - off[i])
+        if len({t.stride(0) for t in dws}) > 1:
+            raise ValueError("the tensors of dw must have one row stride")
+        ptrs, lddw = [t.data_ptr() for t in dws], dws[0].stride(0)
+    elif dw is not None:
+        _matrix(dw, "dw", torch.bfloat16, H, V)
+        dws = [dw]
+        ptrs, lddw = [dw.data_ptr() + 2 * o for o in off[:-1]], dw.stride(0)
+    arr = None if ptrs is None else (ctypes.c_void_p * len(ptrs))(*ptrs)
+    dev = _one_device([targets, lse, dloss, dx, ws] + dws + head.tensors())
+    _run("sb_cross_entropy_grad", dev, stream,
+         lambda: sb_cross_entropy_workspace_bytes(head, True), ws,
+         lambda p, n, s: lib().sb_cross_entropy_grad(
+             head.ref(), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx),
+             0 if dx is None else dx.stride(0), arr, lddw, p, n, s))
+    return dx, dw
 
 
 def to_device_bf16(bits, device="cuda"):

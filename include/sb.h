@@ -374,6 +374,97 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
                                 const float *dloss, void *dx, int64_t lddx, void *const *dw,
                                 int64_t lddw, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The head in 8-bit integers: rows quantised with one scale each, weights
+ * held as one channel per vocabulary column with one scale each.
+ *   z[b][v] = (float(sum_h x[b][h] * w[v][h]) * x_scale[b]) * w_scale[v]
+ * The integer sums are exact (H <= 131071), so z is the same whatever the
+ * batch, the lane split or the call: three fp32 roundings (the sum's, and
+ * one for each scale).  sb_int8_project_tokens ranks these fp32 z as the
+ * projection calls rank theirs: NaN above every number, the lowest global
+ * index among equals.
+ *
+ * Codes and scales (of a row of x, or of a column of the head weight):
+ *   scale = max |value| / 127,  code = rint(value / scale)
+ * both in fp32, ties to even, codes in -127 .. 127.  A row or column of zeros
+ * has scale 0; one that holds a NaN or an infinity has the scale NaN or
+ * infinity, which makes its z NaN; the codes of both are 0.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types of an output. */
+typedef enum sb_dtype {
+    SB_FP32 = 0,
+    SB_BF16 = 1
+} sb_dtype;
+
+/*
+ *   B, V, k, lane_off   as in sb_head_desc
+ *   H        hidden size, <= 131071 (SB_ERR_UNSUPPORTED)
+ *   x        DEVICE int8 [B][ldx], 16-byte aligned; -128 is allowed
+ *   ldx      row stride of x, >= H, multiple of 16
+ *   x_scale  DEVICE fp32 [B]
+ *   w        HOST array of k DEVICE pointers; w[i] is lane i's channels,
+ *            int8 [V_i][ldw]: row j is vocab column off_i + j; 16-byte
+ *            aligned.  A single [V][ldw] allocation is passed as w[i] =
+ *            base + off_i * ldw.
+ *   ldw      channel stride, >= H, multiple of 16
+ *   w_scale  HOST array of k DEVICE pointers; w_scale[i] is fp32 [V_i]
+ * 256 rows of x and 256 channels must span less than 4 GiB.  Bytes past H in
+ * a row or channel may hold anything.
+ */
+typedef struct sb_int8_desc {
+    int32_t B, H, V, k;
+    const int32_t *lane_off;
+    const void *x;
+    int64_t ldx;
+    const float *x_scale;
+    const void *const *w;
+    int64_t ldw;
+    const float *const *w_scale;
+} sb_int8_desc;
+
+/*
+ * Codes and scales of B rows.
+ *   x      DEVICE bf16 [B][ldx], 16-byte aligned, ldx >= H, multiple of 8
+ *   q      DEVICE int8 [B][ldq], 16-byte aligned, ldq >= H, multiple of 16;
+ *          bytes past H are left as they were
+ *   scale  DEVICE fp32 [B]
+ */
+sb_status sb_int8_quantize_rows(const void *x, int64_t ldx, int32_t B, int32_t H, void *q, int64_t ldq,
+                                float *scale, void *stream);
+
+/*
+ * Codes and scales of a bf16 head's weight, turned round into channels.  Only
+ * the weight fields of `desc` are read (H, V, k, lane_off, w, ldw).
+ *   q      HOST array of k DEVICE pointers; q[i] is int8 [V_i][ldq], 16-byte
+ *          aligned, ldq >= H, multiple of 16; bytes past H are left as they were
+ *   scale  HOST array of k DEVICE pointers; scale[i] is fp32 [V_i]
+ */
+sb_status sb_int8_quantize_head(const sb_head_desc *desc, void *const *q, int64_t ldq,
+                                float *const *scale, void *stream);
+
+/*
+ * Bytes of device workspace of sb_int8_project_tokens (SB_SURF_TOKENS) or
+ * sb_int8_logits (SB_SURF_FULL_LOGITS; often 0).  On an invalid descriptor or
+ * another surface returns 0 and sets *status (if not NULL).
+ */
+size_t sb_int8_workspace_bytes(const sb_int8_desc *desc, int surface, sb_status *status);
+
+/* ids[b] = lowest global index of max_v z[b][v]  (DEVICE int32 [B]). */
+sb_status sb_int8_project_tokens(const sb_int8_desc *desc, int32_t *ids, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * out[b][v] = z[b][v], rounded once more for SB_BF16.
+ *   dtype  sb_dtype of out (anything else: SB_ERR_SHAPE)
+ *   out    DEVICE [B][ldo], 16-byte aligned; ldo >= V, a multiple of 4 (fp32)
+ *          or 8 (bf16)
+ */
+sb_status sb_int8_logits(const sb_int8_desc *desc, void *out, int dtype, int64_t ldo, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *sb_status_string(sb_status status);
 

@@ -6,7 +6,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsb.so")
-SOURCES = ["kernels.hip", "sb_api.cpp", "loss.hip", "sb_loss.cpp"]
+SOURCES = ["kernels.hip", "sb_api.cpp", "loss.hip", "sb_loss.cpp", "int8.hip",
+           "sb_int8.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

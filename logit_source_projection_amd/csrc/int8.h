@@ -1,0 +1,73 @@
+// Internal launch interface of the 8-bit head kernels (not part of the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace sbk {
+
+// Largest hidden size: 131071 products of -128 * -128 still fit 32 bits.
+constexpr int kInt8MaxH = 131071;
+
+// Batches of up to kInt8SmallRows rows stream the weight once past all of
+// them (int8_rows_kernel); larger ones run 256 x 256 MFMA tiles.
+constexpr int kInt8SmallRows = 64;
+constexpr int kInt8SmallTile = 64;   // channels per workgroup of the streaming kernel
+constexpr int kInt8LargeTile = 256;  // channels per tile of the MFMA kernel
+inline int int8_tile(int B) { return B <= kInt8SmallRows ? kInt8SmallTile : kInt8LargeTile; }
+
+struct Int8Args {
+    const int8_t *w[kMaxLanes];       // lane i's channels, int8 [V_i][ldw]
+    const float *w_scale[kMaxLanes];  // [V_i]
+    int32_t off[kMaxLanes + 1];       // vocab offsets
+    int32_t tile0[kMaxLanes + 1];     // first tile of lane i (int8_tile(B) channels each)
+    int32_t k;
+    const int8_t *x;                  // int8 [B][ldx]
+    const float *x_scale;             // [B]
+    int64_t ldx, ldw;
+    int32_t B, H, V;
+    // the product: fp32 or bf16 [B][ldo]
+    void *out;
+    int64_t ldo;
+    int32_t bf16;
+    // greedy token IDs: one (value, lowest index) pair per row and tile (or per
+    // row and chunk of kInt8Chunk columns of a split product)
+    int2 *pair;                       // [pairs][B]
+    int32_t pairs;
+    int32_t *ids;                     // [B]
+    // K slices of the streaming kernel: slice s holds K steps s * slice_steps ..
+    int32_t slices, slice_steps;      // steps of kInt8StepK
+    int32_t *part;                    // [slices][B][tiles * kInt8SmallTile]
+};
+
+constexpr int kInt8StepK = 64;
+constexpr int kInt8Chunk = 1024;
+
+// K slices of the streaming kernel for `tiles` tiles.
+int int8_slices(int32_t B, int32_t H, int32_t tiles);
+int int8_slice_steps(int32_t H, int slices);
+
+hipError_t launch_int8_quantize_rows(const uint16_t *x, int64_t ldx, int32_t B, int32_t H, int8_t *q,
+                                     int64_t ldq, float *scale, hipStream_t s);
+
+struct Int8QuantizeArgs {
+    const uint16_t *w[kMaxLanes];  // bf16 [H][ldw]
+    int8_t *q[kMaxLanes];          // int8 [V_i][ldq]
+    float *scale[kMaxLanes];       // [V_i]
+    int32_t off[kMaxLanes + 1];
+    int32_t tile0[kMaxLanes + 1];  // first tile of kInt8QuantizeTile channels of lane i
+    int32_t k, H;
+    int64_t ldw, ldq;
+};
+constexpr int kInt8QuantizeTile = 64;
+hipError_t launch_int8_quantize_head(const Int8QuantizeArgs &a, hipStream_t s);
+
+// The scaled product (a.out) or the pairs and IDs (a.ids).
+hipError_t launch_int8(const Int8Args &a, hipStream_t s);
+
+// Work items of the largest launch of a product of B rows on `tiles` tiles.
+int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices);
+
+}  // namespace sbk

@@ -1,0 +1,654 @@
+// The output head in 8-bit integers (gfx950).
+//
+//   x_scale_b = max_h |x_bh| / 127          q_bh = rint(x_bh / x_scale_b)
+//   z_bv = float(sum_h q_bh w_vh) * x_scale_b * w_scale_v
+//
+// Integer sums are exact, so neither the order of a sum nor its split changes
+// a bit; the three fp32 roundings of z are applied once, at the end.
+#include "int8.h"
+
+#include <limits.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "tile_gemm.h"
+
+namespace sbk {
+namespace {
+
+static_assert(kInt8LargeTile == kTile, "a large tile is one MFMA tile wide");
+
+// The order of the argmax: NaN above every number, then larger values, then
+// lower indices (the projection calls' order).
+__device__ __forceinline__ bool better(float v1, int i1, float v2, int i2)
+{
+    const bool n1 = v1 != v1, n2 = v2 != v2;
+    if (n1 || n2)
+        return n1 && (!n2 || i1 < i2);
+    return v1 > v2 || (v1 == v2 && i1 < i2);
+}
+
+__device__ __forceinline__ void take_better(float &v, int &i, float v2, int i2)
+{
+    if (better(v2, i2, v, i)) {
+        v = v2;
+        i = i2;
+    }
+}
+
+__device__ __forceinline__ int tile_lane(const Int8Args &a, int tile)
+{
+    int lane = 0;
+    while (lane + 1 < a.k && a.tile0[lane + 1] <= tile)
+        ++lane;
+    return lane;
+}
+
+__device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+// ---------------------------------------------------------------------------
+// Quantisation of rows: one workgroup per row.  The first kRowUnits 8-value
+// units of every thread stay in registers between the maximum and the codes
+// (rows of up to 16384 values are read once); longer rows are read again.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256, kRowUnits = 8;
+
+// The code of one value: the fp32 quotient rounded to the nearest, ties to even.
+__device__ __forceinline__ int row_code(uint32_t bits, float scale)
+{
+    const float q = rintf(bf16_value(bits) / scale);
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+__device__ __forceinline__ uint2 unit_codes(const u32x4 &v, float scale)
+{
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t bits = e & 1 ? v[e >> 1] >> 16 : v[e >> 1] & 0xFFFFu;
+        w[e >> 2] |= ((uint32_t)row_code(bits, scale) & 0xFFu) << (8 * (e & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// |max| of a unit as bf16 bits: without the sign, larger bits are larger
+// values, infinity above every number and NaN above infinity.
+__device__ __forceinline__ uint32_t unit_max(const u32x4 &v, uint32_t m)
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        m = max(m, v[d] & 0x7FFFu);
+        m = max(m, (v[d] >> 16) & 0x7FFFu);
+    }
+    return m;
+}
+
+// The scale of codes whose largest magnitude has these bf16 bits; 0 and
+// non-finite maxima quantise to codes of 0 (see codes_of_zero).
+__device__ __forceinline__ float code_scale(uint32_t maxbits) { return bf16_value(maxbits) / 127.f; }
+__device__ __forceinline__ bool codes_of_zero(uint32_t maxbits) { return maxbits == 0 || maxbits >= 0x7F80u; }
+
+__global__ __launch_bounds__(kRowThreads) void quantize_rows_kernel(const uint16_t *x, int64_t ldx,
+                                                                    int H, int8_t *q, int64_t ldq,
+                                                                    float *scale)
+{
+    __shared__ uint32_t wave_max[kRowThreads / 64];
+    const int64_t b = blockIdx.x;
+    const uint16_t *row = x + b * ldx;
+    int8_t *out = q + b * ldq;
+    const int units = H / 8;  // whole units; the last H % 8 values are taken one by one
+    u32x4 v[kRowUnits];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kRowUnits; ++i) {
+        const int u = threadIdx.x + i * kRowThreads;
+        v[i] = u < units ? *reinterpret_cast<const u32x4 *>(row + 8 * u) : u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < kRowUnits; ++i)
+        m = unit_max(v[i], m);
+    for (int u = threadIdx.x + kRowUnits * kRowThreads; u < units; u += kRowThreads)
+        m = unit_max(*reinterpret_cast<const u32x4 *>(row + 8 * u), m);
+    const int tail = 8 * units + threadIdx.x;  // < H for at most 7 threads
+    if (tail < H)
+        m = max(m, (uint32_t)row[tail] & 0x7FFFu);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    if ((threadIdx.x & 63) == 0)
+        wave_max[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRowThreads / 64; ++w)
+        m = max(m, wave_max[w]);
+    const float s = code_scale(m);
+    if (threadIdx.x == 0)
+        scale[b] = s;
+    const bool zero = codes_of_zero(m);
+#pragma unroll
+    for (int i = 0; i < kRowUnits; ++i) {
+        const int u = threadIdx.x + i * kRowThreads;
+        if (u < units)
+            *reinterpret_cast<uint2 *>(out + 8 * u) = zero ? make_uint2(0u, 0u) : unit_codes(v[i], s);
+    }
+    for (int u = threadIdx.x + kRowUnits * kRowThreads; u < units; u += kRowThreads)
+        *reinterpret_cast<uint2 *>(out + 8 * u) =
+            zero ? make_uint2(0u, 0u) : unit_codes(*reinterpret_cast<const u32x4 *>(row + 8 * u), s);
+    if (tail < H)
+        out[tail] = zero ? (int8_t)0 : (int8_t)row_code(row[tail], s);
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation of a bf16 head [H][V] into channels [V][H] with one scale each.
+// One workgroup = 64 channels: a first pass over H for the channels' maxima, a
+// second that turns 64 x 64 blocks round through LDS.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void quantize_head_kernel(const Int8QuantizeArgs a)
+{
+    __shared__ uint32_t cmax[4][kInt8QuantizeTile];
+    __shared__ uint16_t turn[64][kInt8QuantizeTile + 2];
+    int lane = 0;
+    while (lane + 1 < a.k && a.tile0[lane + 1] <= (int)blockIdx.x)
+        ++lane;
+    const int c0 = (blockIdx.x - a.tile0[lane]) * kInt8QuantizeTile;
+    const int width = a.off[lane + 1] - a.off[lane];
+    const int c = threadIdx.x & 63, part = threadIdx.x >> 6;
+    const bool ok = c0 + c < width;
+    const uint16_t *w = a.w[lane] + c0 + c;
+    uint32_t m = 0;
+    if (ok)
+        for (int h = part; h < a.H; h += 4)
+            m = max(m, (uint32_t)w[(int64_t)h * a.ldw] & 0x7FFFu);
+    cmax[part][c] = m;
+    __syncthreads();
+    m = max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c]));
+    if (ok && part == 0)
+        a.scale[lane][c0 + c] = code_scale(m);
+    for (int h0 = 0; h0 < a.H; h0 += 64) {
+        __syncthreads();
+        for (int h = part; h < 64; h += 4)
+            turn[h][c] = ok && h0 + h < a.H ? w[(int64_t)(h0 + h) * a.ldw] : (uint16_t)0;
+        __syncthreads();
+        // thread: channel threadIdx.x / 4, 16 hidden values from 16 * (threadIdx.x % 4)
+        const int ch = threadIdx.x >> 2, hq = 16 * (threadIdx.x & 3);
+        if (c0 + ch < width) {
+            const uint32_t cm = max(max(cmax[0][ch], cmax[1][ch]), max(cmax[2][ch], cmax[3][ch]));
+            const float s = code_scale(cm);
+            const bool zero = codes_of_zero(cm);
+            int8_t *out = a.q[lane] + (int64_t)(c0 + ch) * a.ldq + h0 + hq;
+            uint32_t word[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                word[d] = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!zero)
+                        word[d] |= ((uint32_t)row_code(turn[hq + 4 * d + e][ch], s) & 0xFFu) << (8 * e);
+            }
+            if (h0 + hq + 16 <= a.H) {
+                *reinterpret_cast<u32x4 *>(out) = u32x4{word[0], word[1], word[2], word[3]};
+            } else {
+                for (int e = 0; e < 16 && h0 + hq + e < a.H; ++e)
+                    out[e] = (int8_t)(word[e >> 2] >> (8 * (e & 3)));
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue of four consecutive channels of one row.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void scaled(const i32x4 &acc, float xs, const float *ws, int n, float (&z)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        z[e] = e < n ? ((float)acc[e] * xs) * ws[e] : 0.f;
+}
+
+// z to columns gcol .. of row b, the first n of them.
+__device__ __forceinline__ void store_logits(const Int8Args &a, int64_t b, int gcol, const float (&z)[4], int n)
+{
+    if (a.bf16) {
+        uint16_t *p = static_cast<uint16_t *>(a.out) + b * a.ldo + gcol;
+        if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+            bf16x4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = (__bf16)z[e];
+            *reinterpret_cast<uint2 *>(p) = __builtin_bit_cast(uint2, h);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n)
+                    p[e] = __builtin_bit_cast(uint16_t, (__bf16)z[e]);
+        }
+    } else {
+        float *p = static_cast<float *>(a.out) + b * a.ldo + gcol;
+        if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            *reinterpret_cast<f32x4 *>(p) = f32x4{z[0], z[1], z[2], z[3]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n)
+                    p[e] = z[e];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Large batches: 256 x 256 MFMA tiles, both operands along K.
+// ---------------------------------------------------------------------------
+struct Int8Src {
+    const uint8_t *x, *w;
+    int64_t xbytes, wbytes;
+    int H;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
+    {
+        const int64_t at = (int64_t)st * kStageBytes;
+        return buffer_of(x + at, at < H ? xbytes - at : 0);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t b(int st) const
+    {
+        const int64_t at = (int64_t)st * kStageBytes;
+        return buffer_of(w + at, at < H ? wbytes - at : 0);
+    }
+    __device__ __forceinline__ int tail(int st) const { return min(H - st * kStageBytes, kStageBytes); }
+};
+
+template <bool TOKENS>
+__global__ __launch_bounds__(kTileThreads, 1) void int8_tile_kernel(const Int8Args a, const TileGrid grid)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int number = xcd_tile(blockIdx.x, grid.mt * grid.nt);
+    if (number < 0)
+        return;
+    int mt, nt;
+    tile_of(grid, number, mt, nt);
+    const int lane = tile_lane(a, nt);
+    const int c0 = (nt - a.tile0[lane]) * kTile;
+    const int nvalid = min(kTile, a.off[lane + 1] - a.off[lane] - c0);
+    const int m0 = mt * kTile, rows = min(a.B - m0, kTile);
+    const int H = a.H;
+    Int8Src src;
+    src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
+    src.w = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw);
+    src.xbytes = (int64_t)(rows - 1) * a.ldx + ((H + 15) & ~15);
+    src.wbytes = (int64_t)(nvalid - 1) * a.ldw + ((H + 15) & ~15);
+    src.H = H;
+    WaveTile<i32x4> t;
+    t.init();
+    // a ragged H: x zeroed past it makes the products there 0
+    t.run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
+
+    const int n = t.L & 15, g = t.L >> 4;
+    const int gcol0 = a.off[lane] + c0;
+    float2 *part = reinterpret_cast<float2 *>(smem);  // [kTile][4 column waves]
+    float ws[kColBlocks][4];
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = t.col0 + 16 * cb + 4 * g + e;
+            ws[cb][e] = c < nvalid ? a.w_scale[lane][c0 + c] : 0.f;
+        }
+#pragma unroll
+    for (int rb = 0; rb < kRowBlocks; ++rb) {
+        const int r = t.row0 + 16 * rb + n;
+        const float xs = r < rows ? a.x_scale[m0 + r] : 0.f;
+        float bv = -INFINITY;
+        int bi = INT_MAX;
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb) {
+            const int c = t.col0 + 16 * cb + 4 * g;
+            const int left = nvalid - c;
+            float z[4];
+            scaled(t.acc[rb][cb], xs, ws[cb], 4, z);
+            if (TOKENS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left)
+                        take_better(bv, bi, z[e], gcol0 + c + e);
+            } else if (r < rows && left > 0) {
+                store_logits(a, m0 + r, gcol0 + c, z, left);
+            }
+        }
+        if (TOKENS) {
+            take_better(bv, bi, __shfl_xor(bv, 16), __shfl_xor(bi, 16));
+            take_better(bv, bi, __shfl_xor(bv, 32), __shfl_xor(bi, 32));
+            if (g == 0)
+                part[r * 4 + (t.wave & 3)] = make_float2(bv, __int_as_float(bi));
+        }
+    }
+    if (TOKENS) {
+        __syncthreads();
+        const int r = threadIdx.x;
+        if (r < rows) {
+            float v = part[r * 4].x;
+            int i = __float_as_int(part[r * 4].y);
+#pragma unroll
+            for (int w = 1; w < 4; ++w)
+                take_better(v, i, part[r * 4 + w].x, __float_as_int(part[r * 4 + w].y));
+            a.pair[(int64_t)nt * a.B + m0 + r] = make_int2(__float_as_int(v), i);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 64 rows: the weight streams from memory once.  One workgroup = 4 waves
+// = 64 channels of one lane; wave w takes the K steps w, w + 4, ... of its
+// slice (64 values each), every lane loading 16 bytes of a channel straight
+// into MFMA operand registers, and the four partial tiles meet in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kRowsWaves = 4, kRowsThreads = kRowsWaves * 64;
+constexpr int kRowsBlocks = kInt8SmallTile / 16;  // 16-channel blocks per tile
+
+template <int MB, bool TOKENS>
+__global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args a)
+{
+    __shared__ i32x4 red[kRowsWaves][16][kInt8SmallTile / 4 + 1];
+    const int tile = blockIdx.x / a.slices, slice = blockIdx.x - tile * a.slices;
+    const int lane = tile_lane(a, tile);
+    const int c0 = (tile - a.tile0[lane]) * kInt8SmallTile;
+    const int nvalid = min(kInt8SmallTile, a.off[lane + 1] - a.off[lane] - c0);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int L = threadIdx.x & 63, n = L & 15, g = L >> 4;
+    const int H = a.H;
+    const int64_t hb = (H + 15) & ~15;
+    // buffers end with the last row's and channel's last unit; what lies past H
+    // inside a unit is masked out of x
+    const uint8_t *xp = reinterpret_cast<const uint8_t *>(a.x);
+    const uint8_t *wp = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw);
+    const int64_t xbytes = H > 0 ? (int64_t)(a.B - 1) * a.ldx + hb : 0;
+    const int64_t wbytes = H > 0 ? (int64_t)(nvalid - 1) * a.ldw + hb : 0;
+    uint32_t xo[MB], wo[kRowsBlocks];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+        xo[mb] = (uint32_t)((int64_t)(16 * mb + n) * a.ldx + 16 * g);
+#pragma unroll
+    for (int cb = 0; cb < kRowsBlocks; ++cb)
+        wo[cb] = (uint32_t)((int64_t)(16 * cb + n) * a.ldw + 16 * g);
+    i32x4 acc[MB][kRowsBlocks];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int cb = 0; cb < kRowsBlocks; ++cb)
+            acc[mb][cb] = i32x4{0, 0, 0, 0};
+    const int steps = (H + kInt8StepK - 1) / kInt8StepK;
+    const int s0 = slice * a.slice_steps, s1 = min(s0 + a.slice_steps, steps);
+    constexpr int kAhead = 4;  // steps in flight per wave
+    u32x4 fw[kAhead][kRowsBlocks], fx[kAhead][MB];
+    auto load = [&](int j, int st) {
+        const int64_t at = (int64_t)st * kInt8StepK;
+        const __amdgpu_buffer_rsrc_t rw = buffer_of(wp + at, st < s1 ? wbytes - at : 0);
+        const __amdgpu_buffer_rsrc_t rx = buffer_of(xp + at, st < s1 ? xbytes - at : 0);
+#pragma unroll
+        for (int cb = 0; cb < kRowsBlocks; ++cb)
+            fw[j][cb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo[cb], 0, 2));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            fx[j][mb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb], 0, 0));
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        load(j, s0 + wave + j * kRowsWaves);
+    for (int st = s0 + wave; st < s1; st += kAhead * kRowsWaves) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int sj = st + j * kRowsWaves;  // (at or past s1: zeros)
+            u32x4 xa[MB], wb[kRowsBlocks];
+            // values of x at and past H (a row's padding, or the next row)
+            const int left = H - sj * kInt8StepK - 16 * g;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                xa[mb] = fx[j][mb];
+                if (__builtin_expect(sj * kInt8StepK + kInt8StepK > H, 0)) {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int keep = left - 4 * d;  // valid bytes of the word
+                        xa[mb][d] &= keep >= 4 ? 0xFFFFFFFFu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1u);
+                    }
+                }
+            }
+#pragma unroll
+            for (int cb = 0; cb < kRowsBlocks; ++cb)
+                wb[cb] = fw[j][cb];
+            load(j, sj + kAhead * kRowsWaves);
+#pragma unroll
+            for (int cb = 0; cb < kRowsBlocks; ++cb)
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                    block_mma(acc[mb][cb], xa[mb], wb[cb]);
+        }
+    }
+    // thread: row threadIdx.x / 16 of the block, channels 4 * (threadIdx.x % 16) ..
+    const int er = threadIdx.x >> 4, ec = 4 * (threadIdx.x & 15);
+    const int left = nvalid - ec;
+    const int gcol = a.off[lane] + c0 + ec;
+    float ws[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        ws[e] = e < left ? a.w_scale[lane][c0 + ec + e] : 0.f;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        if (16 * mb >= a.B)
+            break;
+        __syncthreads();
+#pragma unroll
+        for (int cb = 0; cb < kRowsBlocks; ++cb)
+            red[wave][n][4 * cb + g] = acc[mb][cb];
+        __syncthreads();
+        i32x4 sum = red[0][er][ec / 4];
+#pragma unroll
+        for (int w = 1; w < kRowsWaves; ++w)
+            sum += red[w][er][ec / 4];
+        const int b = 16 * mb + er;
+        if (a.slices > 1) {
+            if (b < a.B) {
+                const int64_t ld = (int64_t)a.tile0[a.k] * kInt8SmallTile;
+                *reinterpret_cast<i32x4 *>(a.part + ((int64_t)slice * a.B + b) * ld +
+                                           (int64_t)tile * kInt8SmallTile + ec) = sum;
+            }
+            continue;
+        }
+        float z[4];
+        scaled(sum, b < a.B ? a.x_scale[b] : 0.f, ws, 4, z);
+        if (!TOKENS) {
+            if (b < a.B && left > 0)
+                store_logits(a, b, gcol, z, left);
+            continue;
+        }
+        float bv = -INFINITY;
+        int bi = INT_MAX;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left)
+                take_better(bv, bi, z[e], gcol + e);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1)
+            take_better(bv, bi, __shfl_xor(bv, d), __shfl_xor(bi, d));
+        if (ec == 0 && b < a.B)
+            a.pair[(int64_t)tile * a.B + b] = make_int2(__float_as_int(bv), bi);
+    }
+}
+
+// The slices of a split product added up: one workgroup = kInt8Chunk columns
+// (16 tiles) of one row.
+template <bool TOKENS>
+__global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args a)
+{
+    __shared__ float wv[4];
+    __shared__ int wi[4];
+    const int b = blockIdx.y;
+    const int col = blockIdx.x * kInt8Chunk + 4 * threadIdx.x;  // among the tiles' columns
+    const int64_t ld = (int64_t)a.tile0[a.k] * kInt8SmallTile;
+    float bv = -INFINITY;
+    int bi = INT_MAX;
+    if (col < ld) {
+        const int tile = col / kInt8SmallTile;
+        const int lane = tile_lane(a, tile);
+        const int c = (tile - a.tile0[lane]) * kInt8SmallTile + col % kInt8SmallTile;
+        const int left = a.off[lane + 1] - a.off[lane] - c;
+        if (left > 0) {
+            const int32_t *p = a.part + (int64_t)b * ld + col;
+            i32x4 sum = *reinterpret_cast<const i32x4 *>(p);
+            for (int s = 1; s < a.slices; ++s)
+                sum += *reinterpret_cast<const i32x4 *>(p + (int64_t)s * a.B * ld);
+            float ws[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ws[e] = e < left ? a.w_scale[lane][c + e] : 0.f;
+            scaled(sum, a.x_scale[b], ws, 4, z);
+            const int gcol = a.off[lane] + c;
+            if (!TOKENS)
+                store_logits(a, b, gcol, z, left);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (TOKENS && e < left)
+                    take_better(bv, bi, z[e], gcol + e);
+        }
+    }
+    if (TOKENS) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            take_better(bv, bi, __shfl_xor(bv, d), __shfl_xor(bi, d));
+        if ((threadIdx.x & 63) == 0) {
+            wv[threadIdx.x >> 6] = bv;
+            wi[threadIdx.x >> 6] = bi;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 4; ++w)
+                take_better(bv, bi, wv[w], wi[w]);
+            a.pair[(int64_t)blockIdx.x * a.B + b] = make_int2(__float_as_int(bv), bi);
+        }
+    }
+}
+
+// One workgroup per row folds its pairs.
+__global__ __launch_bounds__(256) void int8_ids_kernel(const Int8Args a)
+{
+    __shared__ float wv[4];
+    __shared__ int wi[4];
+    const int64_t b = blockIdx.x;
+    float bv = -INFINITY;
+    int bi = INT_MAX;
+    for (int t = threadIdx.x; t < a.pairs; t += 256) {
+        const int2 p = a.pair[(int64_t)t * a.B + b];
+        take_better(bv, bi, __int_as_float(p.x), p.y);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        take_better(bv, bi, __shfl_xor(bv, d), __shfl_xor(bi, d));
+    if ((threadIdx.x & 63) == 0) {
+        wv[threadIdx.x >> 6] = bv;
+        wi[threadIdx.x >> 6] = bi;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 4; ++w)
+            take_better(bv, bi, wv[w], wi[w]);
+        a.ids[b] = bi;
+    }
+}
+
+template <int MB>
+hipError_t launch_rows(const Int8Args &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((int64_t)a.tile0[a.k] * a.slices));
+    if (a.ids)
+        hipLaunchKernelGGL((int8_rows_kernel<MB, true>), grid, dim3(kRowsThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((int8_rows_kernel<MB, false>), grid, dim3(kRowsThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool TOKENS>
+hipError_t launch_tiles(const Int8Args &a, hipStream_t s)
+{
+    const TileGrid g = tile_grid(a.B, (int64_t)a.tile0[a.k] * kTile);
+    static std::atomic<uint64_t> lds_done{0};
+    const hipError_t e = allow_lds((const void *)int8_tile_kernel<TOKENS>, kTileLdsBytes, lds_done);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(int8_tile_kernel<TOKENS>, dim3((unsigned)xcd_ids(tile_count(g))),
+                       dim3(kTileThreads), kTileLdsBytes, s, a, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int int8_slices(int32_t B, int32_t H, int32_t tiles)
+{
+    if (B > kInt8SmallRows || tiles <= 0)
+        return 1;
+    // about 1024 workgroups (four to a CU), of at least 16 K steps each
+    const int steps = (H + kInt8StepK - 1) / kInt8StepK;
+    int s = std::min((1024 + tiles - 1) / tiles, steps / 16);
+    s = std::max(1, std::min(s, 16));
+    if (tiles >= 512)
+        s = 1;
+    const int per = int8_slice_steps(H, s);
+    return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
+}
+
+int int8_slice_steps(int32_t H, int slices)
+{
+    const int steps = (H + kInt8StepK - 1) / kInt8StepK;
+    return ((steps + slices - 1) / slices + kRowsWaves - 1) / kRowsWaves * kRowsWaves;
+}
+
+hipError_t launch_int8_quantize_rows(const uint16_t *x, int64_t ldx, int32_t B, int32_t H, int8_t *q,
+                                     int64_t ldq, float *scale, hipStream_t s)
+{
+    if (B <= 0)
+        return hipSuccess;
+    hipLaunchKernelGGL(quantize_rows_kernel, dim3(B), dim3(kRowThreads), 0, s, x, ldx, H, q, ldq, scale);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_quantize_head(const Int8QuantizeArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL(quantize_head_kernel, dim3((unsigned)a.tile0[a.k]), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8(const Int8Args &a, hipStream_t s)
+{
+    hipError_t e;
+    if (a.B > kInt8SmallRows)
+        e = a.ids ? launch_tiles<true>(a, s) : launch_tiles<false>(a, s);
+    else if (a.B <= 16)
+        e = launch_rows<1>(a, s);
+    else if (a.B <= 32)
+        e = launch_rows<2>(a, s);
+    else
+        e = launch_rows<4>(a, s);
+    if (e != hipSuccess)
+        return e;
+    if (a.slices > 1) {
+        const dim3 grid((unsigned)(((int64_t)a.tile0[a.k] * kInt8SmallTile + kInt8Chunk - 1) / kInt8Chunk), a.B);
+        if (a.ids)
+            hipLaunchKernelGGL(int8_join_kernel<true>, grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL(int8_join_kernel<false>, grid, dim3(256), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    if (a.ids) {
+        hipLaunchKernelGGL(int8_ids_kernel, dim3(a.B), dim3(256), 0, s, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices)
+{
+    const int64_t rows = (int64_t)B * 256;  // one workgroup per row
+    if (B <= kInt8SmallRows)
+        return std::max(rows, tiles * slices * kRowsThreads);
+    const int64_t mt = (B + kTile - 1) / kTile;
+    return std::max(rows, (mt * tiles + 8) * kTileThreads);
+}
+
+}  // namespace sbk

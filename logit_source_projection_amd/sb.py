@@ -31,6 +31,9 @@ SB_SURF_FULL_LOGITS = 3
 
 SB_MAX_LANES = 64
 
+SB_FP32 = 0
+SB_BF16 = 1
+
 SB_RED_SUM = 0
 SB_RED_PROD = 1
 SB_RED_MIN = 2
@@ -41,7 +44,9 @@ EXPORTS = ("sb_workspace_bytes", "sb_project_tokens", "sb_project_tokens_static"
            "sb_project_lane_results",
            "sb_project_logprobs", "sb_full_logits", "sb_partial_workspace_bytes",
            "sb_partial_complete", "sb_cross_entropy_workspace_bytes", "sb_cross_entropy",
-           "sb_cross_entropy_grad", "sb_status_string")
+           "sb_cross_entropy_grad", "sb_int8_quantize_rows", "sb_int8_quantize_head",
+           "sb_int8_workspace_bytes", "sb_int8_project_tokens", "sb_int8_logits",
+           "sb_status_string")
 
 
 class SbError(RuntimeError):
@@ -66,6 +71,17 @@ class sb_partial_desc(ctypes.Structure):
         ("lane_k", ctypes.POINTER(ctypes.c_int32)),
         ("x", ctypes.POINTER(ctypes.c_void_p)), ("ldx", ctypes.c_int64),
         ("w", ctypes.POINTER(ctypes.c_void_p)), ("ldw", ctypes.c_int64),
+    ]
+
+
+class sb_int8_desc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("V", ctypes.c_int32), ("k", ctypes.c_int32),
+        ("lane_off", ctypes.POINTER(ctypes.c_int32)),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.POINTER(ctypes.c_void_p)), ("ldw", ctypes.c_int64),
+        ("w_scale", ctypes.POINTER(ctypes.c_void_p)),
     ]
 
 
@@ -108,6 +124,17 @@ def lib():
     L.sb_cross_entropy_grad.restype = ctypes.c_int
     L.sb_cross_entropy_grad.argtypes = [P, vp, vp, vp, vp, i64, ctypes.POINTER(vp), i64, vp, sz,
                                         vp]
+    PI, pvp, i32 = ctypes.POINTER(sb_int8_desc), ctypes.POINTER(vp), ctypes.c_int32
+    L.sb_int8_quantize_rows.restype = ctypes.c_int
+    L.sb_int8_quantize_rows.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp]
+    L.sb_int8_quantize_head.restype = ctypes.c_int
+    L.sb_int8_quantize_head.argtypes = [P, pvp, i64, pvp, vp]
+    L.sb_int8_workspace_bytes.restype = sz
+    L.sb_int8_workspace_bytes.argtypes = [PI, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    L.sb_int8_project_tokens.restype = ctypes.c_int
+    L.sb_int8_project_tokens.argtypes = [PI, vp, vp, sz, vp]
+    L.sb_int8_logits.restype = ctypes.c_int
+    L.sb_int8_logits.argtypes = [PI, vp, ctypes.c_int, i64, vp, sz, vp]
     L.sb_status_string.restype = ctypes.c_char_p
     L.sb_status_string.argtypes = [ctypes.c_int]
     _lib = L
@@ -503,6 +530,169 @@ def sb_cross_entropy_grad(head, targets, lse, dloss, dx=None, dw=None, ws=None, 
              head.ref(), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx),
              0 if dx is None else dx.stride(0), arr, lddw, p, n, s))
     return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# The head in 8-bit integers.
+# ---------------------------------------------------------------------------
+class Int8Head:
+    """Descriptor of an 8-bit head: row codes x [B, H] (int8) with scales
+    x_scale [B], and the channels of every lane with their scales.
+
+    ``w`` is either one [V, H] int8 tensor with w_scale [V], or lists of k
+    tensors, lane i of shape [V_i, H] (one common row stride) and [V_i].
+    ``lane_off`` holds the k+1 vocab offsets.  Row strides are multiples of
+    16.  Raw values can be overridden to exercise the ABI's validation."""
+
+    def __init__(self, x, x_scale, w, w_scale, lane_off, *, B=None, H=None, V=None, ldx=None,
+                 ldw=None, x_ptr=None, x_scale_ptr=None, w_ptrs=None, w_scale_ptrs=None):
+        self.x, self.x_scale, self.w, self.w_scale = x, x_scale, w, w_scale
+        self.from_tensors = x_ptr is None and w_ptrs is None
+        off = [int(o) for o in lane_off]
+        self.lane_off = off
+        k = len(off) - 1
+        self._off = (ctypes.c_int32 * max(1, k + 1))(*off)
+        if w_ptrs is not None:
+            wp, sp, stride = list(w_ptrs), list(w_scale_ptrs), 0
+        elif isinstance(w, (list, tuple)):
+            if len(w) != k or len(w_scale) != k:
+                raise ValueError(f"w and w_scale must hold one tensor per lane, {k}")
+            wp, sp = [t.data_ptr() for t in w], [t.data_ptr() for t in w_scale]
+            stride = w[0].stride(0)
+        else:
+            stride = w.stride(0)
+            wp = [w.data_ptr() + stride * o for o in off[:-1]]
+            sp = [w_scale.data_ptr() + 4 * o for o in off[:-1]]
+        self._w = (ctypes.c_void_p * max(1, len(wp)))(*wp)
+        self._ws = (ctypes.c_void_p * max(1, len(sp)))(*sp)
+        self.desc = sb_int8_desc(
+            B=x.shape[0] if B is None else B,
+            H=x.shape[1] if H is None else H,
+            V=off[-1] if V is None else V,
+            k=k, lane_off=self._off,
+            x=x.data_ptr() if x_ptr is None else x_ptr,
+            ldx=x.stride(0) if ldx is None else ldx,
+            x_scale=x_scale.data_ptr() if x_scale_ptr is None else x_scale_ptr,
+            w=self._w, ldw=stride if ldw is None else ldw, w_scale=self._ws)
+
+    @property
+    def B(self):
+        return self.desc.B
+
+    @property
+    def V(self):
+        return self.desc.V
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+    def check(self):
+        if not self.from_tensors:
+            return
+        d, off = self.desc, self.lane_off
+        _matrix(self.x, "x", torch.int8, d.B, d.H)
+        _vector(self.x_scale, "x_scale", torch.float32, d.B)
+        if isinstance(self.w, (list, tuple)):
+            for i, (t, s) in enumerate(zip(self.w, self.w_scale)):
+                n = off[i + 1] - off[i]
+                _matrix(t, f"w[{i}]", torch.int8, n, d.H)
+                _vector(s, f"w_scale[{i}]", torch.float32, n)
+            if len({t.stride(0) for t in self.w}) > 1:
+                raise ValueError("the tensors of w must have one row stride")
+        else:
+            _matrix(self.w, "w", torch.int8, d.V, d.H)
+            _vector(self.w_scale, "w_scale", torch.float32, d.V)
+
+    def tensors(self):
+        if not self.from_tensors:
+            return []
+        return [self.x, self.x_scale] + _as_list(self.w) + _as_list(self.w_scale)
+
+
+def sb_int8_quantize_rows(x, q, scale, stream=None):
+    """q (int8 [B, H]) and scale (fp32 [B]) <- the codes of the rows of x
+    (bf16 [B, H]).  Returns (q, scale)."""
+    _operands([x], "x")
+    B, H = x.shape
+    _matrix(q, "q", torch.int8, B, H)
+    _vector(scale, "scale", torch.float32, B)
+    with torch.cuda.device(_one_device([x, q, scale])):
+        _check(lib().sb_int8_quantize_rows(_ptr(x), x.stride(0), B, H, _ptr(q), q.stride(0),
+                                           _ptr(scale), _stream(stream)), "sb_int8_quantize_rows")
+    return q, scale
+
+
+def sb_int8_quantize_head(head, q, scale, stream=None):
+    """q and scale <- the codes of a bf16 head's weight, one channel per vocab
+    column: int8 [V, H] and fp32 [V], or lists of one [V_i, H] and one [V_i]
+    tensor per lane (one common row stride).  Returns (q, scale)."""
+    head.check()
+    off, H = head.lane_off, head.desc.H
+    k = len(off) - 1
+    if isinstance(q, (list, tuple)):
+        if len(q) != k or len(scale) != k:
+            raise ValueError(f"q and scale must hold one tensor per lane, {k}")
+        for i, (t, s) in enumerate(zip(q, scale)):
+            _matrix(t, f"q[{i}]", torch.int8, off[i + 1] - off[i], H)
+            _vector(s, f"scale[{i}]", torch.float32, off[i + 1] - off[i])
+        if len({t.stride(0) for t in q}) > 1:
+            raise ValueError("the tensors of q must have one row stride")
+        qp, sp, ldq = [t.data_ptr() for t in q], [t.data_ptr() for t in scale], q[0].stride(0)
+    else:
+        _matrix(q, "q", torch.int8, head.V, H)
+        _vector(scale, "scale", torch.float32, head.V)
+        ldq = q.stride(0)
+        qp = [q.data_ptr() + ldq * o for o in off[:-1]]
+        sp = [scale.data_ptr() + 4 * o for o in off[:-1]]
+    weights = _as_list(head.w) if head.from_tensors else []
+    with torch.cuda.device(_one_device(_as_list(q) + _as_list(scale) + weights)):
+        _check(lib().sb_int8_quantize_head(head.ref(), (ctypes.c_void_p * k)(*qp), ldq,
+                                           (ctypes.c_void_p * k)(*sp), _stream(stream)),
+               "sb_int8_quantize_head")
+    return q, scale
+
+
+def sb_int8_workspace_bytes(head, surface):
+    st = ctypes.c_int(0)
+    n = lib().sb_int8_workspace_bytes(head.ref(), int(surface), ctypes.byref(st))
+    if st.value != SB_OK:
+        raise SbError(st.value, "sb_int8_workspace_bytes")
+    return int(n)
+
+
+def int8_workspace(head, surface, device=None):
+    """A workspace for `surface` (its contents on entry do not matter)."""
+    return torch.empty(max(sb_int8_workspace_bytes(head, surface), 16), dtype=torch.uint8,
+                       device=head.x.device if device is None else device)
+
+
+def sb_int8_project_tokens(head, ids, ws=None, stream=None):
+    """Greedy token IDs (int32 [B]) of the 8-bit head.  Returns ids."""
+    head.check()
+    _vector(ids, "ids", torch.int32, head.B)
+    _vector(ws, "ws", torch.uint8, 0)
+    dev = _one_device([ids, ws] + head.tensors())
+    _run("sb_int8_project_tokens", dev, stream,
+         lambda: sb_int8_workspace_bytes(head, SB_SURF_TOKENS), ws,
+         lambda p, n, s: lib().sb_int8_project_tokens(head.ref(), _ptr(ids), p, n, s))
+    return ids
+
+
+def sb_int8_logits(head, out, ws=None, stream=None):
+    """out (fp32 or bf16 [B, V], row stride out.stride(0)) <- the scaled
+    product.  Returns out."""
+    head.check()
+    if isinstance(out, torch.Tensor) and out.dtype == torch.bfloat16:
+        _matrix(out, "out", torch.bfloat16, head.B, head.V)
+    else:
+        _matrix(out, "out", torch.float32, head.B, head.V)
+    _vector(ws, "ws", torch.uint8, 0)
+    dev = _one_device([out, ws] + head.tensors())
+    dtype = SB_BF16 if out.dtype == torch.bfloat16 else SB_FP32
+    _run("sb_int8_logits", dev, stream,
+         lambda: sb_int8_workspace_bytes(head, SB_SURF_FULL_LOGITS), ws,
+         lambda p, n, s: lib().sb_int8_logits(head.ref(), _ptr(out), dtype, out.stride(0), p, n, s))
+    return out
 
 
 def to_device_bf16(bits, device="cuda"):

@@ -65,7 +65,7 @@ struct LogitsSrc {
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
     {
         const int64_t at = (int64_t)st * kStageBytes;
-        return buffer_of(x + at, xbytes - at);
+        return buffer_of(x + at, st * kStageK < H ? xbytes - at : 0);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t b(int st) const
     {
@@ -232,7 +232,7 @@ struct DxSrc {
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
     {
         const int64_t at = (int64_t)st * kStageBytes;
-        return buffer_of(dz + at, dzbytes - at);
+        return buffer_of(dz + at, st < (nb_end - nb_first) * (kTile / kStageK) ? dzbytes - at : 0);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t b(int st)
     {

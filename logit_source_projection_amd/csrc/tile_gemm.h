@@ -6,8 +6,9 @@
 //                operands of dZ.W^T, both int8 operands);
 //   * kAcrossK:  rows of the operand contiguous, k steps `ld` apart (W in X.W,
 //                both operands of X^T.dZ).
-// K advances in stages of 128 bytes per row (64 bf16 or 128 int8) through two
-// LDS stages of 64 KB, filled by direct-to-LDS buffer loads of 1 KB.
+// K advances in stages of 128 bytes per row (64 bf16 or 128 int8) through LDS
+// rings of three stages of A and two of B (32 KB each), filled by
+// direct-to-LDS buffer loads of 1 KB.
 //
 // What bounds it: a stage is 64 MFMAs per wave (2 x 8 x 4 blocks of 16 x 16 x
 // 32 bf16), about 2048 cycles with two waves per SIMD, and 24 KB of fragment
@@ -16,8 +17,12 @@
 // is computed while the other half's fragments arrive: the reads of half h + 1
 // are issued between the MFMAs of half h.  The one barrier of a stage sits
 // between its halves, where the wave already holds the second half in
-// registers: behind it the stage's slot is free and is refilled two stages
-// ahead, so a load has a whole stage of time.
+// registers: behind it B's slot is free and is refilled two stages ahead, while
+// A's third slot takes A's loads in the first half.  So four of a stage's eight
+// loads per wave are issued in each half, spread over its MFMAs (eight in a
+// row after the barrier hold the wave's MFMAs up while the CU's one address
+// unit takes the 64 loads of its waves), and a load has at least most of a
+// stage of time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -41,7 +46,7 @@ constexpr int kTileThreads = kTileWaves * 64;
 constexpr int kStageBytes = 128;       // K bytes of a row per stage
 constexpr int kStageK = 64;            // bf16 K steps per stage
 constexpr int kOperandBytes = kTile * kStageBytes;      // one operand's stage
-constexpr int kTileLdsBytes = 2 * 2 * kOperandBytes;    // two stages of two operands
+constexpr int kTileLdsBytes = 5 * kOperandBytes;        // three stages of A, two of B: all 160 KB
 constexpr int kRowBlocks = 8;          // 16-row blocks of a wave
 constexpr int kColBlocks = 4;          // 16-column blocks of a wave
 
@@ -229,6 +234,22 @@ __device__ __forceinline__ void block_mma(i32x4 &c, const u32x4 &row, const u32x
 
 constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;
 
+// A workgroup barrier that no memory operation is moved across.  Unlike
+// __syncthreads() it does not wait for loads into LDS that are still in flight.
+__device__ __forceinline__ void block_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// This wave's LDS operations are done.
+__device__ __forceinline__ void wait_lds()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+}
+
 // The accumulators of a wave: acc[rb][cb] holds, for lane L, row 16 rb + L % 16
 // and columns 16 cb + 4 (L / 16) .. + 3 of the wave's 128 x 64 part.
 template <typename Acc>
@@ -267,47 +288,56 @@ struct WaveTile {
         FragReader<LB, kColBlocks> rb_;
         ra.init(row0, L);
         rb_.init(col0, L);
-        auto fill = [&](int st, __amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b) {
-            uint8_t *slot = lds + (st & 1) * (2 * kOperandBytes);
-            stage_load(slot, a, va, wave);
-            stage_load(slot + kOperandBytes, b, vb, wave);
-        };
-        auto mend = [&](int st) {  // a stage whose K range ends inside it
+        // A's ring of three slots, then B's of two
+        uint8_t *const ringb = lds + 3 * kOperandBytes;
+        auto slot_b = [&](int st) { return ringb + (st & 1) * kOperandBytes; };
+        auto mend = [&](int st, uint8_t *sa) {  // a stage whose K range ends inside it
             const int kb = src.tail(st);
             if (__builtin_expect(kb < kStageBytes, 0)) {
-                uint8_t *slot = lds + (st & 1) * (2 * kOperandBytes);
                 if (ZA)
-                    zero_stage_tail(slot, kb);
+                    zero_stage_tail(sa, kb);
                 if (ZB)
-                    zero_stage_tail(slot + kOperandBytes, kb);
-                __syncthreads();
+                    zero_stage_tail(slot_b(st), kb);
+                wait_lds();
+                block_barrier();
             }
         };
-        fill(0, src.a(0), src.b(0));
-        fill(1, src.a(1), src.b(1));             // (empty where there is no stage 1)
+        stage_load(lds, src.a(0), va, wave);
+        stage_load(slot_b(0), src.b(0), vb, wave);
+        stage_load(lds + kOperandBytes, src.a(1), va, wave);  // (empty where there is no stage 1)
+        stage_load(slot_b(1), src.b(1), vb, wave);
         __builtin_amdgcn_s_waitcnt(0x0f70 | 8);  // vmcnt(8): stage 0 has landed
-        __syncthreads();
-        mend(0);
+        block_barrier();
+        mend(0, lds);
+        uint8_t *a0 = lds, *a1 = lds + kOperandBytes, *a2 = lds + 2 * kOperandBytes;  // stages st, st + 1, st + 2
         u32x4 fa[2][kRowBlocks], fb[2][kColBlocks];
-        read_half<LA, LB>(fa[0], fb[0], ra, rb_, lds, 0, 0);
+        read_half<LA, LB>(fa[0], fb[0], ra, rb_, a0, slot_b(0), 0);
+        __amdgpu_buffer_rsrc_t next_a = src.a(2);
         for (int st = 0; st < nst; ++st) {
-            // first half, beside the reads of the second
-            read_half<LA, LB>(fa[1], fb[1], ra, rb_, lds, st & 1, 1);
+            // first half, beside A's loads of stage st + 2 and the reads of
+            // the second half
+            stage_load(a2, next_a, va, wave);
+            read_half<LA, LB>(fa[1], fb[1], ra, rb_, a0, slot_b(st), 1);
             mma_half(fa[0], fb[0]);
-            interleave<LA, LB, false>();
-            const __amdgpu_buffer_rsrc_t na = src.a(st + 2), nb = src.b(st + 2);
-            // The next stage has landed (its loads are a stage old) and every
-            // wave holds the rest of this one in registers.
-            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
-            __syncthreads();
+            interleave<LA, LB>();
+            const __amdgpu_buffer_rsrc_t next_b = src.b(st + 2);
+            next_a = src.a(st + 3);
+            // Stage st + 1 has landed (only A's four loads of stage st + 2 are
+            // later) and every wave holds the rest of this stage in registers.
+            __builtin_amdgcn_s_waitcnt(0x0070 | 4);  // vmcnt(4), lgkmcnt(0)
+            block_barrier();
             if (st + 1 < nst)
-                mend(st + 1);
-            // second half, beside the reads of the next stage's first (past
-            // the last stage: zeros, never used)
-            fill(st, na, nb);
-            read_half<LA, LB>(fa[0], fb[0], ra, rb_, lds, (st + 1) & 1, 0);
+                mend(st + 1, a1);
+            // second half, beside B's loads of stage st + 2 and the reads of
+            // the next stage's first half (past the last stage: never used)
+            stage_load(slot_b(st), next_b, vb, wave);
+            read_half<LA, LB>(fa[0], fb[0], ra, rb_, a1, slot_b(st + 1), 0);
             mma_half(fa[1], fb[1]);
-            interleave<LA, LB, true>();
+            interleave<LA, LB>();
+            uint8_t *const free_slot = a0;
+            a0 = a1;
+            a1 = a2;
+            a2 = free_slot;
         }
         __builtin_amdgcn_s_waitcnt(0x0070);
         __syncthreads();  // LDS is the caller's
@@ -318,9 +348,8 @@ private:
     static __device__ __forceinline__ void read_half(u32x4 (&fa)[kRowBlocks], u32x4 (&fb)[kColBlocks],
                                                      const FragReader<LA, kRowBlocks> &ra,
                                                      const FragReader<LB, kColBlocks> &rb_,
-                                                     const uint8_t *lds, int slot, int half)
+                                                     const uint8_t *sa, const uint8_t *sb, int half)
     {
-        const uint8_t *sa = lds + slot * (2 * kOperandBytes), *sb = sa + kOperandBytes;
 #pragma unroll
         for (int cb = 0; cb < kColBlocks; ++cb)
             fb[cb] = rb_.read(sb, half, cb);
@@ -337,17 +366,17 @@ private:
             for (int cb = 0; cb < kColBlocks; ++cb)
                 block_mma(acc[rb][cb], fa[rb], fb[cb]);
     }
-    // Asks the scheduler for the half's LDS reads to be spread over its MFMAs
-    // (FILL: after the refill's loads).
-    template <int LA, int LB, bool FILL>
+    // Asks the scheduler to spread a half's four loads and its LDS reads over
+    // its MFMAs.
+    template <int LA, int LB>
     static __device__ __forceinline__ void interleave()
     {
         constexpr int reads = kRowBlocks * (LA == kAcrossK ? 2 : 1) + kColBlocks * (LB == kAcrossK ? 2 : 1);
         constexpr int per = (reads + kRowBlocks - 1) / kRowBlocks;
-        if (FILL)
-            __builtin_amdgcn_sched_group_barrier(kSchedVmem, 8, 0);
 #pragma unroll
         for (int i = 0; i < kRowBlocks; ++i) {
+            if (i < 4)
+                __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
             __builtin_amdgcn_sched_group_barrier(kSchedDsRead, per, 0);
             __builtin_amdgcn_sched_group_barrier(kSchedMfma, kColBlocks, 0);
         }

@@ -411,8 +411,9 @@ typedef enum sb_dtype {
  *            base + off_i * ldw.
  *   ldw      channel stride, >= H, multiple of 16
  *   w_scale  HOST array of k DEVICE pointers; w_scale[i] is fp32 [V_i]
- * 256 rows of x and 256 channels must span less than 4 GiB.  Bytes past H in
- * a row or channel may hold anything.
+ * 256 rows of x and 256 channels must span less than 4 GiB, and B is below
+ * 2^22 (SB_ERR_UNSUPPORTED).  Bytes past H in a row or channel may hold
+ * anything.
  */
 typedef struct sb_int8_desc {
     int32_t B, H, V, k;

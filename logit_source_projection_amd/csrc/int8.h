@@ -34,7 +34,7 @@ struct Int8Args {
     int32_t bf16;
     // greedy token IDs: one (value, lowest index) pair per row and tile (or per
     // row and chunk of kInt8Chunk columns of a split product)
-    int2 *pair;                       // [pairs][B]
+    int2 *pair;                       // [B][pairs]
     int32_t pairs;
     int32_t *ids;                     // [B]
     // K slices of the streaming kernel: slice s holds K steps s * slice_steps ..
@@ -42,7 +42,7 @@ struct Int8Args {
     int32_t *part;                    // [slices][B][tiles * kInt8SmallTile]
 };
 
-constexpr int kInt8StepK = 64;
+constexpr int kInt8StepK = 128;  // a cache line of every channel
 constexpr int kInt8Chunk = 1024;
 
 // K slices of the streaming kernel for `tiles` tiles.

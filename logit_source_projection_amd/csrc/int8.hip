@@ -50,9 +50,11 @@ __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_fl
 // ---------------------------------------------------------------------------
 // Quantisation of rows: one workgroup per row.  The first kRowUnits 8-value
 // units of every thread stay in registers between the maximum and the codes
-// (rows of up to 16384 values are read once); longer rows are read again.
+// (rows of up to 32768 values are read once); longer rows are read again.
 // ---------------------------------------------------------------------------
-constexpr int kRowThreads = 256, kRowUnits = 8;
+constexpr int kRowUnits = 4;
+// Threads per row: enough that a unit or two per thread covers the row.
+inline int row_threads(int H) { return H <= 2048 ? 256 : 1024; }
 
 // The code of one value: the fp32 quotient rounded to the nearest, ties to even.
 __device__ __forceinline__ int row_code(uint32_t bits, float scale)
@@ -89,6 +91,7 @@ __device__ __forceinline__ uint32_t unit_max(const u32x4 &v, uint32_t m)
 __device__ __forceinline__ float code_scale(uint32_t maxbits) { return bf16_value(maxbits) / 127.f; }
 __device__ __forceinline__ bool codes_of_zero(uint32_t maxbits) { return maxbits == 0 || maxbits >= 0x7F80u; }
 
+template <int kRowThreads>
 __global__ __launch_bounds__(kRowThreads) void quantize_rows_kernel(const uint16_t *x, int64_t ldx,
                                                                     int H, int8_t *q, int64_t ldq,
                                                                     float *scale)
@@ -329,7 +332,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void int8_tile_kernel(const Int8Ar
 #pragma unroll
             for (int w = 1; w < 4; ++w)
                 take_better(v, i, part[r * 4 + w].x, __float_as_int(part[r * 4 + w].y));
-            a.pair[(int64_t)nt * a.B + m0 + r] = make_int2(__float_as_int(v), i);
+            a.pair[(int64_t)(m0 + r) * a.pairs + nt] = make_int2(__float_as_int(v), i);
         }
     }
 }
@@ -337,16 +340,32 @@ __global__ __launch_bounds__(kTileThreads, 1) void int8_tile_kernel(const Int8Ar
 // ---------------------------------------------------------------------------
 // Up to 64 rows: the weight streams from memory once.  One workgroup = 4 waves
 // = 64 channels of one lane; wave w takes the K steps w, w + 4, ... of its
-// slice (64 values each), every lane loading 16 bytes of a channel straight
-// into MFMA operand registers, and the four partial tiles meet in LDS.
+// slice (128 bytes each), and the four partial tiles meet in LDS.
+//
+// Bound by the weight's bytes.  MFMA wants 16 bytes of 16 channels per load,
+// half a cache line of each: loaded straight into registers, the second half
+// of every line was fetched again (non-temporal: 198 us at 16 rows, H 5120, V
+// 151936) or cost L1 look-ups (158 us).  So every wave fills a private LDS ring
+// of kSlots steps with direct-to-LDS loads of 8 whole lines and reads its
+// fragments from there; nothing is shared before the end, so there is no
+// barrier in the loop, only the wave's own load counter.
 // ---------------------------------------------------------------------------
 constexpr int kRowsWaves = 4, kRowsThreads = kRowsWaves * 64;
 constexpr int kRowsBlocks = kInt8SmallTile / 16;  // 16-channel blocks per tile
+constexpr int kRowsSlots = 2;
+constexpr int kRowsSlotBytes = kInt8SmallTile * kInt8StepK;
+constexpr int kRowsLoads = kRowsSlotBytes / 1024;
+constexpr int kRowsLdsBytes = kRowsWaves * kRowsSlots * kRowsSlotBytes;
+constexpr int kRedStride = kInt8SmallTile / 4 + 1;  // quads per row of a partial tile, one of padding
+static_assert(kRowsWaves * 16 * kRedStride * 16 <= kRowsLdsBytes, "the partial tiles reuse the ring");
+
+// s_waitcnt vmcnt(n), nothing else.
+constexpr int vmcnt_only(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 
 template <int MB, bool TOKENS>
 __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args a)
 {
-    __shared__ i32x4 red[kRowsWaves][16][kInt8SmallTile / 4 + 1];
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tile = blockIdx.x / a.slices, slice = blockIdx.x - tile * a.slices;
     const int lane = tile_lane(a, tile);
     const int c0 = (tile - a.tile0[lane]) * kInt8SmallTile;
@@ -361,13 +380,19 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
     const uint8_t *wp = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw);
     const int64_t xbytes = H > 0 ? (int64_t)(a.B - 1) * a.ldx + hb : 0;
     const int64_t wbytes = H > 0 ? (int64_t)(nvalid - 1) * a.ldw + hb : 0;
-    uint32_t xo[MB], wo[kRowsBlocks];
+    uint32_t xo[MB], wo[kRowsLoads];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
         xo[mb] = (uint32_t)((int64_t)(16 * mb + n) * a.ldx + 16 * g);
+    // load i brings channels 8 i .. 8 i + 7; piece p of channel c sits in slot
+    // p ^ ((c / 2) & 7) of its line
 #pragma unroll
-    for (int cb = 0; cb < kRowsBlocks; ++cb)
-        wo[cb] = (uint32_t)((int64_t)(16 * cb + n) * a.ldw + 16 * g);
+    for (int i = 0; i < kRowsLoads; ++i) {
+        const int c = 8 * i + (L >> 3);
+        wo[i] = (uint32_t)((int64_t)c * a.ldw + 16 * ((L & 7) ^ ((c >> 1) & 7)));
+    }
+    uint8_t *const ring = smem + wave * (kRowsSlots * kRowsSlotBytes);
+    const uint32_t fo = (uint32_t)(n * kInt8StepK + ((g ^ ((n >> 1) & 7)) * 16));
     i32x4 acc[MB][kRowsBlocks];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
@@ -376,53 +401,77 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
             acc[mb][cb] = i32x4{0, 0, 0, 0};
     const int steps = (H + kInt8StepK - 1) / kInt8StepK;
     const int s0 = slice * a.slice_steps, s1 = min(s0 + a.slice_steps, steps);
-    constexpr int kAhead = 4;  // steps in flight per wave
-    u32x4 fw[kAhead][kRowsBlocks], fx[kAhead][MB];
+    u32x4 fx[kRowsSlots][2][MB];
+    // (at or past s1: zeros)
     auto load = [&](int j, int st) {
         const int64_t at = (int64_t)st * kInt8StepK;
         const __amdgpu_buffer_rsrc_t rw = buffer_of(wp + at, st < s1 ? wbytes - at : 0);
         const __amdgpu_buffer_rsrc_t rx = buffer_of(xp + at, st < s1 ? xbytes - at : 0);
 #pragma unroll
-        for (int cb = 0; cb < kRowsBlocks; ++cb)
-            fw[j][cb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo[cb], 0, 2));
+        for (int i = 0; i < kRowsLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rw, (__attribute__((address_space(3))) void *)(ring + j * kRowsSlotBytes + i * 1024), 16,
+                wo[i], 0, 0, 2);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-            fx[j][mb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb], 0, 0));
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                fx[j][i][mb] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb], 64 * i, 0));
     };
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
+    for (int j = 0; j < kRowsSlots; ++j)
         load(j, s0 + wave + j * kRowsWaves);
-    for (int st = s0 + wave; st < s1; st += kAhead * kRowsWaves) {
+    for (int st = s0 + wave; st < s1; st += kRowsSlots * kRowsWaves) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int sj = st + j * kRowsWaves;  // (at or past s1: zeros)
-            u32x4 xa[MB], wb[kRowsBlocks];
-            // values of x at and past H (a row's padding, or the next row)
-            const int left = H - sj * kInt8StepK - 16 * g;
+        for (int j = 0; j < kRowsSlots; ++j) {
+            const int sj = st + j * kRowsWaves;
+            // this slot's loads are done: only the later slots' are in flight
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(vmcnt_only((kRowsSlots - 1) * (kRowsLoads + 2 * MB)));
+            asm volatile("" ::: "memory");
+            u32x4 xa[2][MB], wb[2][kRowsBlocks];
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                xa[mb] = fx[j][mb];
-                if (__builtin_expect(sj * kInt8StepK + kInt8StepK > H, 0)) {
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const int keep = left - 4 * d;  // valid bytes of the word
-                        xa[mb][d] &= keep >= 4 ? 0xFFFFFFFFu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1u);
+                for (int cb = 0; cb < kRowsBlocks; ++cb)
+                    wb[i][cb] = *reinterpret_cast<const u32x4 *>(
+                        ring + j * kRowsSlotBytes + (fo ^ (uint32_t)(64 * i)) + cb * 16 * kInt8StepK);
+                // values of x at and past H (a row's padding, or the next row)
+                const int left = H - sj * kInt8StepK - 64 * i - 16 * g;
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    xa[i][mb] = fx[j][i][mb];
+                    if (__builtin_expect(sj * kInt8StepK + kInt8StepK > H, 0)) {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const int keep = left - 4 * d;  // valid bytes of the word
+                            xa[i][mb][d] &= keep >= 4 ? 0xFFFFFFFFu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1u);
+                        }
                     }
                 }
             }
+            // the fragments are in registers before the slot is filled again
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+            load(j, sj + kRowsSlots * kRowsWaves);
 #pragma unroll
-            for (int cb = 0; cb < kRowsBlocks; ++cb)
-                wb[cb] = fw[j][cb];
-            load(j, sj + kAhead * kRowsWaves);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int cb = 0; cb < kRowsBlocks; ++cb)
+                for (int cb = 0; cb < kRowsBlocks; ++cb)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    block_mma(acc[mb][cb], xa[mb], wb[cb]);
+                    for (int mb = 0; mb < MB; ++mb)
+                        acc[mb][cb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                            __builtin_bit_cast(i32x4, wb[i][cb]), __builtin_bit_cast(i32x4, xa[i][mb]),
+                            acc[mb][cb], 0, 0, 0);
         }
     }
-    // thread: row threadIdx.x / 16 of the block, channels 4 * (threadIdx.x % 16) ..
-    const int er = threadIdx.x >> 4, ec = 4 * (threadIdx.x & 15);
+    // the ring's last (empty) loads are done in every wave: LDS is free
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    i32x4 *const red = reinterpret_cast<i32x4 *>(smem);  // [wave][16 rows][kRedStride]
+    // thread: row threadIdx.x / kQuads of the block, four channels
+    constexpr int kQuads = kInt8SmallTile / 4;
+    const int er = threadIdx.x / kQuads, ec = 4 * (threadIdx.x % kQuads);
     const int left = nvalid - ec;
     const int gcol = a.off[lane] + c0 + ec;
     float ws[4];
@@ -436,12 +485,14 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
         __syncthreads();
 #pragma unroll
         for (int cb = 0; cb < kRowsBlocks; ++cb)
-            red[wave][n][4 * cb + g] = acc[mb][cb];
+            red[(wave * 16 + n) * kRedStride + 4 * cb + g] = acc[mb][cb];
         __syncthreads();
-        i32x4 sum = red[0][er][ec / 4];
+        if (er >= 16)
+            continue;
+        i32x4 sum = red[er * kRedStride + ec / 4];
 #pragma unroll
         for (int w = 1; w < kRowsWaves; ++w)
-            sum += red[w][er][ec / 4];
+            sum += red[(w * 16 + er) * kRedStride + ec / 4];
         const int b = 16 * mb + er;
         if (a.slices > 1) {
             if (b < a.B) {
@@ -465,10 +516,10 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
             if (e < left)
                 take_better(bv, bi, z[e], gcol + e);
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1)
+        for (int d = 1; d < kQuads; d <<= 1)
             take_better(bv, bi, __shfl_xor(bv, d), __shfl_xor(bi, d));
         if (ec == 0 && b < a.B)
-            a.pair[(int64_t)tile * a.B + b] = make_int2(__float_as_int(bv), bi);
+            a.pair[(int64_t)b * a.pairs + tile] = make_int2(__float_as_int(bv), bi);
     }
 }
 
@@ -492,6 +543,7 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args a)
         if (left > 0) {
             const int32_t *p = a.part + (int64_t)b * ld + col;
             i32x4 sum = *reinterpret_cast<const i32x4 *>(p);
+#pragma unroll 4
             for (int s = 1; s < a.slices; ++s)
                 sum += *reinterpret_cast<const i32x4 *>(p + (int64_t)s * a.B * ld);
             float ws[4], z[4];
@@ -520,21 +572,22 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args a)
         if (threadIdx.x == 0) {
             for (int w = 1; w < 4; ++w)
                 take_better(bv, bi, wv[w], wi[w]);
-            a.pair[(int64_t)blockIdx.x * a.B + b] = make_int2(__float_as_int(bv), bi);
+            a.pair[(int64_t)b * a.pairs + blockIdx.x] = make_int2(__float_as_int(bv), bi);
         }
     }
 }
 
 // One workgroup per row folds its pairs.
-__global__ __launch_bounds__(256) void int8_ids_kernel(const Int8Args a)
+constexpr int kIdsThreads = 1024;
+__global__ __launch_bounds__(kIdsThreads) void int8_ids_kernel(const Int8Args a)
 {
-    __shared__ float wv[4];
-    __shared__ int wi[4];
+    __shared__ float wv[kIdsThreads / 64];
+    __shared__ int wi[kIdsThreads / 64];
     const int64_t b = blockIdx.x;
     float bv = -INFINITY;
     int bi = INT_MAX;
-    for (int t = threadIdx.x; t < a.pairs; t += 256) {
-        const int2 p = a.pair[(int64_t)t * a.B + b];
+    for (int t = threadIdx.x; t < a.pairs; t += kIdsThreads) {
+        const int2 p = a.pair[b * a.pairs + t];
         take_better(bv, bi, __int_as_float(p.x), p.y);
     }
 #pragma unroll
@@ -546,20 +599,21 @@ __global__ __launch_bounds__(256) void int8_ids_kernel(const Int8Args a)
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 4; ++w)
+        for (int w = 1; w < kIdsThreads / 64; ++w)
             take_better(bv, bi, wv[w], wi[w]);
         a.ids[b] = bi;
     }
 }
 
-template <int MB>
+template <int MB, bool TOKENS>
 hipError_t launch_rows(const Int8Args &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)a.tile0[a.k] * a.slices));
-    if (a.ids)
-        hipLaunchKernelGGL((int8_rows_kernel<MB, true>), grid, dim3(kRowsThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((int8_rows_kernel<MB, false>), grid, dim3(kRowsThreads), 0, s, a);
+    static std::atomic<uint64_t> lds_done{0};
+    const hipError_t e = allow_lds((const void *)int8_rows_kernel<MB, TOKENS>, kRowsLdsBytes, lds_done);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((int8_rows_kernel<MB, TOKENS>), dim3((unsigned)((int64_t)a.tile0[a.k] * a.slices)),
+                       dim3(kRowsThreads), kRowsLdsBytes, s, a);
     return hipGetLastError();
 }
 
@@ -582,12 +636,11 @@ int int8_slices(int32_t B, int32_t H, int32_t tiles)
 {
     if (B > kInt8SmallRows || tiles <= 0)
         return 1;
-    // about 1024 workgroups (four to a CU), of at least 16 K steps each
+    // Two workgroups run on a CU: slices fill those 512 places once, with at
+    // least 8 K steps each (the 64-row product of H 17408 and V 5120, 80 tiles:
+    // 47.0 us in 12 slices, two rounds, 39.0 us in 6).
     const int steps = (H + kInt8StepK - 1) / kInt8StepK;
-    int s = std::min((1024 + tiles - 1) / tiles, steps / 16);
-    s = std::max(1, std::min(s, 16));
-    if (tiles >= 512)
-        s = 1;
+    const int s = std::max(1, std::min(512 / tiles, steps / 8));
     const int per = int8_slice_steps(H, s);
     return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
 }
@@ -603,7 +656,10 @@ hipError_t launch_int8_quantize_rows(const uint16_t *x, int64_t ldx, int32_t B, 
 {
     if (B <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(quantize_rows_kernel, dim3(B), dim3(kRowThreads), 0, s, x, ldx, H, q, ldq, scale);
+    if (row_threads(H) == 256)
+        hipLaunchKernelGGL(quantize_rows_kernel<256>, dim3(B), dim3(256), 0, s, x, ldx, H, q, ldq, scale);
+    else
+        hipLaunchKernelGGL(quantize_rows_kernel<1024>, dim3(B), dim3(1024), 0, s, x, ldx, H, q, ldq, scale);
     return hipGetLastError();
 }
 
@@ -619,11 +675,11 @@ hipError_t launch_int8(const Int8Args &a, hipStream_t s)
     if (a.B > kInt8SmallRows)
         e = a.ids ? launch_tiles<true>(a, s) : launch_tiles<false>(a, s);
     else if (a.B <= 16)
-        e = launch_rows<1>(a, s);
+        e = a.ids ? launch_rows<1, true>(a, s) : launch_rows<1, false>(a, s);
     else if (a.B <= 32)
-        e = launch_rows<2>(a, s);
+        e = a.ids ? launch_rows<2, true>(a, s) : launch_rows<2, false>(a, s);
     else
-        e = launch_rows<4>(a, s);
+        e = a.ids ? launch_rows<4, true>(a, s) : launch_rows<4, false>(a, s);
     if (e != hipSuccess)
         return e;
     if (a.slices > 1) {
@@ -636,7 +692,7 @@ hipError_t launch_int8(const Int8Args &a, hipStream_t s)
             return e;
     }
     if (a.ids) {
-        hipLaunchKernelGGL(int8_ids_kernel, dim3(a.B), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(int8_ids_kernel, dim3(a.B), dim3(kIdsThreads), 0, s, a);
         e = hipGetLastError();
     }
     return e;
@@ -644,7 +700,7 @@ hipError_t launch_int8(const Int8Args &a, hipStream_t s)
 
 int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices)
 {
-    const int64_t rows = (int64_t)B * 256;  // one workgroup per row
+    const int64_t rows = (int64_t)B * kIdsThreads;  // one workgroup per row
     if (B <= kInt8SmallRows)
         return std::max(rows, tiles * slices * kRowsThreads);
     const int64_t mt = (B + kTile - 1) / kTile;

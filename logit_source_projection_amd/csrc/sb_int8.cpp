@@ -166,7 +166,7 @@ sb_status sb_int8_quantize_rows(const void *x, int64_t ldx, int32_t B, int32_t H
     if (!aligned(scale, 4) ||
         (H > 0 && (!aligned(x, 16) || !aligned(q, 16) || ldx % 8 != 0 || ldq % 16 != 0)))
         return SB_ERR_ALIGN;
-    if ((int64_t)B * 256 >= kItems || H > sbk::kInt8MaxH)
+    if ((int64_t)B * 1024 >= kItems || H > sbk::kInt8MaxH)
         return SB_ERR_UNSUPPORTED;
     return sbk::launch_int8_quantize_rows(static_cast<const uint16_t *>(x), ldx, B, H,
                                           static_cast<int8_t *>(q), ldq, scale,

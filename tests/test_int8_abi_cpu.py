@@ -61,7 +61,7 @@ def test_descriptor():
             (dict(H=131072, ldx=131072, ldw=131072), sb.SB_ERR_UNSUPPORTED),
             (dict(ldx=1 << 24), sb.SB_ERR_UNSUPPORTED), (dict(ldw=1 << 24), sb.SB_ERR_UNSUPPORTED),
             (dict(V=(1 << 30) + 1, off=(0, 8, (1 << 30) + 1)), sb.SB_ERR_UNSUPPORTED),
-            (dict(B=1 << 24), sb.SB_ERR_UNSUPPORTED)):
+            (dict(B=1 << 22), sb.SB_ERR_UNSUPPORTED)):
         assert status(head8(**kw)) == want, kw
     assert status(head8(H=131071, ldx=131072, ldw=131072)) == sb.SB_OK
     assert status(head8(ldx=(1 << 24) - 16, ldw=(1 << 24) - 16)) == sb.SB_OK
@@ -104,7 +104,7 @@ def test_row_quantiser_arguments():
                      (dict(x=FAKE + 2), sb.SB_ERR_ALIGN), (dict(ldx=516), sb.SB_ERR_ALIGN),
                      (dict(q=FAKE + 8), sb.SB_ERR_ALIGN), (dict(ldq=520), sb.SB_ERR_ALIGN),
                      (dict(scale=FAKE + 2), sb.SB_ERR_ALIGN),
-                     (dict(B=1 << 24), sb.SB_ERR_UNSUPPORTED),
+                     (dict(B=1 << 22), sb.SB_ERR_UNSUPPORTED),
                      (dict(H=131072, ldx=131072, ldq=131072), sb.SB_ERR_UNSUPPORTED)):
         assert rows(**kw) == want, kw
     assert rows(x=None, q=None, scale=None, B=0) == sb.SB_OK

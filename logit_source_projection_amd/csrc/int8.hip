@@ -359,9 +359,6 @@ constexpr int kRowsLdsBytes = kRowsWaves * kRowsSlots * kRowsSlotBytes;
 constexpr int kRedStride = kInt8SmallTile / 4 + 1;  // quads per row of a partial tile, one of padding
 static_assert(kRowsWaves * 16 * kRedStride * 16 <= kRowsLdsBytes, "the partial tiles reuse the ring");
 
-// s_waitcnt vmcnt(n), nothing else.
-constexpr int vmcnt_only(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
-
 template <int MB, bool TOKENS>
 __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args a)
 {
@@ -409,9 +406,7 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
         const __amdgpu_buffer_rsrc_t rx = buffer_of(xp + at, st < s1 ? xbytes - at : 0);
 #pragma unroll
         for (int i = 0; i < kRowsLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rw, (__attribute__((address_space(3))) void *)(ring + j * kRowsSlotBytes + i * 1024), 16,
-                wo[i], 0, 0, 2);
+            load_to_lds<2>(ring + j * kRowsSlotBytes + i * 1024, rw, wo[i]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll

@@ -29,14 +29,21 @@ struct LossArgs {
     int64_t ldx, ldw;
     int32_t B, H, V;
     int32_t nb0, nblk;       // the blocks of this launch
+    // Batches of up to kLossSmallRows rows: K slices of the logits, slice s
+    // holding the K steps s * slice_steps .. of kLossStepK, and their sums
+    int32_t slices, slice_steps;
+    float *zp;               // fp32 [slices][B][blocks * kVocabBlock], with two slices or more
     // loss
-    float2 *mse;             // [blocks][B] {block maximum, sum exp(z - maximum)}
+    float2 *mse;             // {maximum, sum exp(z - maximum)}: [blocks][B], or with up to
+                             // kLossSmallRows rows [B][parts]
+    int32_t parts;
     float *zt;               // [B] the target's logit
     float *loss, *lse;       // [B]
     // gradient
     const float *lse_in;     // [B]
     const float *dloss;      // [B]
-    uint16_t *dz;            // bf16 [B][ldz], columns of blocks nb0 ..
+    uint16_t *dz;            // bf16 [dz_parts(B)][B][ldz], whose sum is dz, columns of
+                             // blocks nb0 ..
     int64_t ldz;
     const uint16_t *xm;      // bf16 [B][ldxm]: x with the ignored rows zeroed
     int64_t ldxm;
@@ -47,6 +54,25 @@ struct LossArgs {
     int32_t splits;          // K splits of dx
     int32_t first;           // the first launch on dxp stores, later ones add
 };
+
+// Batches of up to kLossSmallRows rows stream the weight once past all of them;
+// larger ones run 256 x 256 MFMA tiles.
+constexpr int kLossSmallRows = 64;
+constexpr int kLossStepK = 32;        // K rows per MFMA step
+constexpr int kLossSmallTile = 128;   // columns per workgroup of the streaming kernel
+constexpr int kLossChunk = 1024;      // columns per workgroup that adds slices up
+// bf16 parts that dz is held in.  Its rounding is as large as that of the bf16
+// results, and in sums over many rows the two add up as independent errors; in
+// sums of few terms a lone dz's rounding would be the whole result's, so up to
+// 32 rows a second part holds what the first leaves.
+constexpr int dz_parts(int B) { return B <= 32 ? 2 : 1; }
+inline int loss_parts(int nblk, int slices)
+{
+    return slices > 1 ? (nblk * kVocabBlock + kLossChunk - 1) / kLossChunk
+                      : nblk * (kVocabBlock / kLossSmallTile);
+}
+int loss_slices(int32_t B, int32_t H, int32_t nblk);
+int loss_slice_steps(int32_t H, int slices);
 
 // Per-block results of the logits of blocks nb0 .. nb0 + nblk - 1.
 hipError_t launch_loss_blocks(const LossArgs &a, hipStream_t s);
@@ -59,6 +85,8 @@ hipError_t launch_mask_rows(const LossArgs &a, uint16_t *xm, hipStream_t s);
 hipError_t launch_dlogits(const LossArgs &a, hipStream_t s);
 // dw of blocks nb0 ... and the blocks' part of dx.
 hipError_t launch_grad(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s);
+// The same for up to kLossSmallRows rows (all blocks in one launch; reads x, not xm).
+hipError_t launch_grad_rows(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s);
 // dx = sum of the splits' partial sums.
 hipError_t launch_dx_finish(const LossArgs &a, hipStream_t s);
 

@@ -57,6 +57,8 @@ __device__ __forceinline__ void store_bf16x4(uint16_t *p, const float (&v)[4], i
     }
 }
 
+enum LogitsUse { kUseLoss, kUseGrad };
+
 // Z tile = rows of X times a block of W.
 struct LogitsSrc {
     const uint8_t *x, *w;
@@ -75,7 +77,7 @@ struct LogitsSrc {
     __device__ __forceinline__ int tail(int st) const { return min((H - st * kStageK) * 2, kStageBytes); }
 };
 
-enum LogitsUse { kUseLoss, kUseGrad };
+
 
 template <int USE>
 __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs a, const TileGrid grid)
@@ -196,6 +198,291 @@ __global__ __launch_bounds__(kCombineWaves * 64) void loss_combine_kernel(const 
         return;
     for (int w = 1; w < kCombineWaves; ++w)
         merge_ms(m, s, part[w][L].x, part[w][L].y);
+    const float l = m + __logf(s);
+    const int t = a.targets[b];
+    a.lse[b] = l;
+    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : l - a.zt[b]);
+}
+
+// ---------------------------------------------------------------------------
+// Up to 64 rows: the weight streams from memory once past all of them.  One
+// workgroup = 4 waves = 128 columns; wave w takes the K steps w, w + 4, ... of
+// its slice (32 rows of W each).  A lane loads 8 rows x 8 columns (16 lanes
+// read 256 contiguous bytes of a row) and turns them round in registers: MFMA c
+// of a step covers the columns 8 n + c, n = 0 .. 15.  The four partial tiles
+// are added in wave order through LDS; K slices, where the tiles alone cannot
+// fill the card, are added in slice order by join_kernel.
+// ---------------------------------------------------------------------------
+constexpr int kRowsWaves = 4, kRowsThreads = kRowsWaves * 64;
+
+template <int MB>
+struct RowFrags {
+    u32x4 w[8], x[MB];
+};
+
+// loss: {maximum, sum of exponentials} of n values (the 16 lanes of a row
+// hold its columns) and the target's logit.
+__device__ __forceinline__ float2 part_of(const float *y, int n, int lanes)
+{
+    float m = -INFINITY;
+    for (int e = 0; e < n; ++e)
+        m = fmaxf(m, y[e]);
+    for (int d = 1; d < lanes; d <<= 1)
+        m = fmaxf(m, __shfl_xor(m, d));
+    const float at = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+    for (int e = 0; e < n; ++e)
+        s += __expf(y[e] - at);
+    for (int d = 1; d < lanes; d <<= 1)
+        s += __shfl_xor(s, d);
+    return make_float2(m, s);
+}
+
+// dz of one logit: what its row needs, read once per row.
+struct RowGrad {
+    float lse, scale;
+    int target;
+    __device__ __forceinline__ RowGrad(const LossArgs &a, int64_t b)
+    {
+        target = a.targets[b];
+        lse = a.lse_in[b];
+        // a target past the vocabulary has no gradient: NaN, not a guess
+        scale = target >= a.V ? NAN : a.dloss[b];
+    }
+    __device__ __forceinline__ float dz(float z, int col) const
+    {
+        const float p = __expf(z - lse) - (col == target ? 1.f : 0.f);
+        return target < 0 ? 0.f : p * scale;
+    }
+};
+
+// dz in bf16, and where lo is not NULL the rest of it too: as the sum of two
+// bf16 numbers it is off by at most 2^-16.
+template <int N>
+__device__ __forceinline__ void store_split(uint16_t *hi, uint16_t *lo, const float (&v)[N])
+{
+    typedef __bf16 vec __attribute__((ext_vector_type(N)));
+    vec h, l;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        h[e] = (__bf16)v[e];
+        l[e] = (__bf16)(v[e] - (float)h[e]);
+    }
+    *reinterpret_cast<vec *>(hi) = h;
+    if (lo)
+        *reinterpret_cast<vec *>(lo) = l;
+}
+
+template <int MB, int USE>
+__global__ __launch_bounds__(kRowsThreads, MB == 4 ? 2 : (MB == 2 ? 3 : 4)) void logits_rows_kernel(const LossArgs a)
+{
+    __shared__ float red[kRowsWaves][16][kLossSmallTile + 4];
+    const int tile = blockIdx.x / a.slices, slice = blockIdx.x - tile * a.slices;
+    const int nb = tile / (kVocabBlock / kLossSmallTile);
+    const int lane = block_lane(a.vocab, nb);
+    const int c0 = (nb - a.vocab.blk0[lane]) * kVocabBlock + tile % (kVocabBlock / kLossSmallTile) * kLossSmallTile;
+    const int nvalid = max(0, min(kLossSmallTile, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int L = threadIdx.x & 63, n = L & 15, g = L >> 4;
+    const int H = a.H;
+    const uint16_t *wbase = a.vocab.w[lane] + c0;
+    const int64_t wbytes = H > 0 && nvalid > 0 ? ((int64_t)(H - 1) * a.ldw + ((nvalid + 7) & ~7)) * 2 : 0;
+    const int64_t xbytes = H > 0 ? ((int64_t)(a.B - 1) * a.ldx + ((H + 7) & ~7)) * 2 : 0;
+    uint32_t wo[8], xo[MB];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        wo[r] = (uint32_t)(((int64_t)(8 * g + r) * a.ldw + 8 * n) * 2);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+        xo[mb] = (uint32_t)(((int64_t)(16 * mb + n) * a.ldx + 8 * g) * 2);
+    f32x4 acc[MB][8];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            acc[mb][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int steps = (H + kLossStepK - 1) / kLossStepK;
+    const int s0 = slice * a.slice_steps, s1 = min(s0 + a.slice_steps, steps);
+    auto load = [&](RowFrags<MB> &f, int st) {  // (at or past s1: zeros)
+        const int64_t wat = (int64_t)st * kLossStepK * a.ldw * 2, xat = (int64_t)st * kLossStepK * 2;
+        const __amdgpu_buffer_rsrc_t rw =
+            buffer_of(reinterpret_cast<const uint8_t *>(wbase) + wat, st < s1 ? wbytes - wat : 0);
+        const __amdgpu_buffer_rsrc_t rx =
+            buffer_of(reinterpret_cast<const uint8_t *>(a.x) + xat, st < s1 ? xbytes - xat : 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)  // non-temporal: each weight byte is read once
+            f.w[r] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo[r], 0, 2));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            f.x[mb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb], 0, 0));
+    };
+    auto mma = [&](RowFrags<MB> &f, int st) {
+        if (__builtin_expect(st * kLossStepK + kLossStepK > H, 0)) {
+            // values of x at and past H: a row's padding, or the next row
+            const int left = H - st * kLossStepK - 8 * g;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    f.x[mb][d] &= (left > 2 * d ? 0x0000FFFFu : 0u) | (left > 2 * d + 1 ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            u32x4 col;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                col[q] = __builtin_amdgcn_perm(f.w[2 * q + 1][c >> 1], f.w[2 * q][c >> 1],
+                                               c & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                acc[mb][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, f.x[mb]), __builtin_bit_cast(bf16x8, col), acc[mb][c], 0, 0, 0);
+        }
+    };
+    RowFrags<MB> fa, fb;
+    load(fa, s0 + wave);
+    for (int st = s0 + wave; st < s1; st += 2 * kRowsWaves) {
+        load(fb, st + kRowsWaves);
+        mma(fa, st);
+        load(fa, st + 2 * kRowsWaves);
+        mma(fb, st + kRowsWaves);
+    }
+
+    // thread: row threadIdx.x / 16 of a block, columns 8 * (threadIdx.x % 16) ..
+    const int er = threadIdx.x >> 4, ec = 8 * (threadIdx.x & 15);
+    const int gcol = a.vocab.off[lane] + c0 + ec;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        if (16 * mb >= a.B)
+            break;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            *reinterpret_cast<f32x4 *>(&red[wave][4 * g + r][8 * n]) =
+                f32x4{acc[mb][0][r], acc[mb][1][r], acc[mb][2][r], acc[mb][3][r]};
+            *reinterpret_cast<f32x4 *>(&red[wave][4 * g + r][8 * n + 4]) =
+                f32x4{acc[mb][4][r], acc[mb][5][r], acc[mb][6][r], acc[mb][7][r]};
+        }
+        __syncthreads();
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][er][ec + e]);
+#pragma unroll
+            for (int w = 1; w < kRowsWaves; ++w)
+                s += *reinterpret_cast<const f32x4 *>(&red[w][er][ec + e]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[e + i] = s[i];
+        }
+        const int b = 16 * mb + er;
+        if (a.slices > 1) {
+            if (b < a.B) {
+                float *p = a.zp + ((int64_t)slice * a.B + b) * ((int64_t)a.nblk * kVocabBlock) +
+                           (int64_t)tile * kLossSmallTile + ec;
+                *reinterpret_cast<f32x4 *>(p) = f32x4{y[0], y[1], y[2], y[3]};
+                *reinterpret_cast<f32x4 *>(p + 4) = f32x4{y[4], y[5], y[6], y[7]};
+            }
+            continue;
+        }
+        if (USE == kUseLoss) {
+            const int tgt = b < a.B ? a.targets[b] : -1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (ec + e >= nvalid)
+                    y[e] = -INFINITY;
+                else if (gcol + e == tgt)
+                    a.zt[b] = y[e];
+            }
+            const float2 p = part_of(y, 8, 16);
+            if (ec == 0 && b < a.B)
+                a.mse[(int64_t)b * a.parts + tile] = p;
+        } else if (b < a.B) {
+            const RowGrad row(a, b);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = ec + e < nvalid ? row.dz(y[e], gcol + e) : 0.f;
+            uint16_t *p = a.dz + (int64_t)b * a.ldz + (int64_t)tile * kLossSmallTile + ec;
+            store_split(p, dz_parts(a.B) > 1 ? p + (int64_t)a.B * a.ldz : nullptr, v);
+        }
+    }
+}
+
+// The slices of the logits added up: one workgroup = kLossChunk columns of a row.
+template <int USE>
+__global__ __launch_bounds__(256) void join_kernel(const LossArgs a)
+{
+    __shared__ float2 part[4];
+    const int b = blockIdx.y;
+    const int64_t ld = (int64_t)a.nblk * kVocabBlock;
+    const int64_t col = (int64_t)blockIdx.x * kLossChunk + 4 * threadIdx.x;
+    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (col < ld) {
+        const int nb = (int)(col / kVocabBlock);
+        const int lane = block_lane(a.vocab, nb);
+        const int c = (nb - a.vocab.blk0[lane]) * kVocabBlock + (int)(col % kVocabBlock);
+        const int left = a.vocab.off[lane + 1] - a.vocab.off[lane] - c;
+        const int gcol = a.vocab.off[lane] + c;
+        const float *p = a.zp + (int64_t)b * ld + col;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll 4
+        for (int i = 1; i < a.slices; ++i)
+            s += *reinterpret_cast<const f32x4 *>(p + (int64_t)i * a.B * ld);
+        if (USE == kUseLoss) {
+            const int tgt = a.targets[b];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) {
+                    y[e] = s[e];
+                    if (gcol + e == tgt)
+                        a.zt[b] = s[e];
+                }
+        } else {
+            const RowGrad row(a, b);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = e < left ? row.dz(s[e], gcol + e) : 0.f;
+            uint16_t *q = a.dz + (int64_t)b * a.ldz + col;
+            store_split(q, dz_parts(a.B) > 1 ? q + (int64_t)a.B * a.ldz : nullptr, v);
+        }
+    }
+    if (USE == kUseLoss) {
+        float2 p = part_of(y, 4, 64);
+        if ((threadIdx.x & 63) == 0)
+            part[threadIdx.x >> 6] = p;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 4; ++w)
+                merge_ms(p.x, p.y, part[w].x, part[w].y);
+            a.mse[(int64_t)b * a.parts + blockIdx.x] = p;
+        }
+    }
+}
+
+// Few rows: one workgroup per row, its parts spread over the threads.
+__global__ __launch_bounds__(256) void loss_rows_combine_kernel(const LossArgs a)
+{
+    __shared__ float2 part[4];
+    const int b = blockIdx.x;
+    float m = -INFINITY, s = 0.f;
+    for (int i = threadIdx.x; i < a.parts; i += 256) {
+        const float2 p = a.mse[(int64_t)b * a.parts + i];
+        merge_ms(m, s, p.x, p.y);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
+        merge_ms(m, s, m2, s2);
+    }
+    if ((threadIdx.x & 63) == 0)
+        part[threadIdx.x >> 6] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x != 0)
+        return;
+    for (int w = 1; w < 4; ++w)
+        merge_ms(m, s, part[w].x, part[w].y);
     const float l = m + __logf(s);
     const int t = a.targets[b];
     a.lse[b] = l;
@@ -364,19 +651,305 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_kernel(const LossArgs a,
     }
 }
 
-// Four columns per thread; the splits are added in ascending order.
+// ---------------------------------------------------------------------------
+// Up to 64 rows: dX and dW in one pass over the weight, which both are bound
+// by (W is read, dW written).  A workgroup has 64 rows h of W and a run of
+// 64-column steps, which its waves take in turn, so that the lines of W and dW
+// that straddle two steps (row strides need not be multiples of a line) are
+// read and written by neighbours at the same time.  At 16 rows, H 5120, V 37984
+// (rows of 593.5 lines) the whole gradient took 365 us with 256 rows and one
+// step at a time per workgroup, 330 us with two steps, 296 us with four.
+// A wave streams its tiles of W and of dz through a private LDS ring of whole
+// lines and shares nothing.  dz's tile is [rows][64 columns]: rows b of its
+// high part, then (up to 32 rows) of its low part.
+//   dX[b][h] += sum_v W[h][v] dz[b][v]   (k = columns, along both)
+//   dW[h][v]  = sum_b x[b][h] dz[b][v]   (k = dz rows, read across)
+// ---------------------------------------------------------------------------
+constexpr int kFewH = 64, kFewSlots = 2, kFewStep = 64;
+constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;
+constexpr int kFewWBytes = kFewH * kFewStep * 2;  // a step's tile of W
+
+template <int MB>
+struct FewShape {
+    static constexpr int kBp = 16 * MB;                        // rows b, padded
+    static constexpr int kRows = dz_parts(kBp) * kBp;          // dz rows: 32, 64 or 64
+    static constexpr int kSlot = kFewWBytes + kRows * kFewStep * 2;
+    static constexpr int kLds = kFewWaves * kFewSlots * kSlot;
+};
+
+// A step's columns: its lane, the first column there and how many.
+struct Cols {
+    int lane, c, n;
+};
+
+template <int MB>
+__global__ __launch_bounds__(kFewThreads, 1) void grad_rows_kernel(const LossArgs a, const int htiles,
+                                                                                const int per, const int want_dx,
+                                                                                const int want_dw)
+{
+    // the shape as local constants (usable in device code as values)
+    constexpr int kBp = FewShape<MB>::kBp, kRows = FewShape<MB>::kRows, kSlot = FewShape<MB>::kSlot;
+    constexpr int kParts = kRows / kBp;
+    constexpr int kKc = kRows / 32;          // 32-row K steps of dW
+    constexpr int kXc = MB == 4 ? 2 : 1;     // of which x has this many of its own
+    constexpr int kZ = kRows / 8;            // loads of dz per step (8 rows each)
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int split = blockIdx.x / htiles, hw = (blockIdx.x - split * htiles) * kFewH;
+    const int steps = a.nblk * (kVocabBlock / kFewStep);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int L = threadIdx.x & 63, n = L & 15, g = L >> 4;
+    // the wave's steps: s0, s0 + kFewWaves, ... below s1
+    const int s0 = min(split * per, steps) + wave, s1 = min((split + 1) * per, steps);
+    const int hrows = min(kFewH, a.H - hw);
+    uint8_t *const ring = smem + wave * (kFewSlots * kSlot);
+
+    // x's fragments: lane holds x[b][h] of h = 16 hb + n, b = 8 g .. 8 g + 7 of
+    // each 32 dz rows; ignored rows, and rows past B or H, are zeros
+    u32x4 xf[4][kXc];
+    if (want_dw) {
+        const __amdgpu_buffer_rsrc_t rt = buffer_of(a.targets, (int64_t)a.B * 4);
+        const __amdgpu_buffer_rsrc_t rx =
+            buffer_of(a.x, ((int64_t)(a.B - 1) * a.ldx + ((a.H + 7) & ~7)) * 2);
+        int tgt[kXc][8];
+#pragma unroll
+        for (int kc = 0; kc < kXc; ++kc)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                tgt[kc][j] = (int)__builtin_amdgcn_raw_buffer_load_b32(
+                    rt, 4 * ((32 * kc + 8 * g + j) % kBp), 0, 0);
+#pragma unroll
+        for (int kc = 0; kc < kXc; ++kc)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int b = (32 * kc + 8 * g + j) % kBp;
+#pragma unroll
+                for (int hb = 0; hb < 4; ++hb) {
+                    const int h = hw + 16 * hb + n;
+                    // past the buffer's end where the value is to be zero
+                    const uint32_t at = b < a.B && tgt[kc][j] >= 0 && h < a.H
+                                            ? (uint32_t)(((int64_t)b * a.ldx + h) * 2) : 0xFFFFFFF0u;
+                    const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rx, at, 0, 0);
+                    if (j & 1)
+                        xf[hb][kc][j >> 1] |= v << 16;
+                    else
+                        xf[hb][kc][j >> 1] = v;
+                }
+            }
+    }
+
+    uint32_t wo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * i + (L >> 3);
+        wo[i] = (uint32_t)((int64_t)r * a.ldw * 2 + 16 * ((L & 7) ^ ((r >> 1) & 7)));
+    }
+    uint32_t zo[kZ];
+#pragma unroll
+    for (int i = 0; i < kZ; ++i) {
+        const int r = 8 * i + (L >> 3);
+        zo[i] = (uint32_t)((int64_t)(r % kBp) * a.ldz * 2 + 16 * ((L & 7) ^ ((r >> 1) & 7)));
+    }
+    int lane = block_lane(a.vocab, min(s0, steps - 1) / (kVocabBlock / kFewStep));
+    int lane_end = a.vocab.blk0[lane + 1];
+    auto cols_of = [&](int st) {
+        const int nb = st / (kVocabBlock / kFewStep);
+        while (nb >= lane_end) {
+            ++lane;
+            lane_end = a.vocab.blk0[lane + 1];
+        }
+        const int c = (nb - a.vocab.blk0[lane]) * kVocabBlock + st % (kVocabBlock / kFewStep) * kFewStep;
+        return Cols{lane, c, max(0, min(kFewStep, a.vocab.off[lane + 1] - a.vocab.off[lane] - c))};
+    };
+    const int64_t zplane = (int64_t)a.B * a.ldz;
+    const int64_t zbytes = ((int64_t)(a.B - 1) * a.ldz + kFewStep) * 2;
+    auto load = [&](int slot, int st) -> Cols {  // (at or past s1: zeros)
+        Cols k = {lane, 0, 0};
+        if (st < s1)
+            k = cols_of(st);
+        uint8_t *const to = ring + slot * kSlot;
+        if (want_dx) {
+            const __amdgpu_buffer_rsrc_t rw =
+                buffer_of(a.vocab.w[k.lane] + (int64_t)hw * a.ldw + k.c,
+                          k.n > 0 ? ((int64_t)(hrows - 1) * a.ldw + ((k.n + 7) & ~7)) * 2 : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                load_to_lds(to + i * 1024, rw, wo[i]);
+        }
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+            const __amdgpu_buffer_rsrc_t rz =
+                buffer_of(a.dz + part * zplane + (int64_t)st * kFewStep, st < s1 ? zbytes : 0);
+#pragma unroll
+            for (int i = part * (kZ / kParts); i < (part + 1) * (kZ / kParts); ++i)
+                load_to_lds(to + kFewWBytes + i * 1024, rz, zo[i]);
+        }
+        return k;
+    };
+
+    f32x4 dxa[4][MB];
+#pragma unroll
+    for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            dxa[hb][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t fo = (uint32_t)(n * 128 + ((g ^ ((n >> 1) & 7)) * 16));  // row n, piece g
+    Cols cur = load(0, s0), next = load(1, s0 + kFewWaves);
+    // The wave's last memory operations are the next step's loads (kZ of dz, 8
+    // of W) and then kW stores of dw, where the last step stored whole tiles;
+    // a ragged one may have stored more or fewer, and counts as none.
+    constexpr int kW = 8;
+    bool stored = false;
+    int slot = 0;
+    for (int st = s0; st < s1; st += kFewWaves, slot ^= 1) {
+        // this step's tiles have landed (the next step's loads stay in flight)
+        asm volatile("" ::: "memory");
+        if (want_dx) {
+            if (stored)
+                __builtin_amdgcn_s_waitcnt(vmcnt_only(kZ + 8 + kW));
+            else
+                __builtin_amdgcn_s_waitcnt(vmcnt_only(kZ + 8));
+        } else if (stored) {
+            __builtin_amdgcn_s_waitcnt(vmcnt_only(kZ + kW));
+        } else {
+            __builtin_amdgcn_s_waitcnt(vmcnt_only(kZ));
+        }
+        asm volatile("" ::: "memory");
+        const uint8_t *wt = ring + slot * kSlot, *zt = wt + kFewWBytes;
+        f32x4 dwa[4][4];
+#pragma unroll
+        for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+            for (int vb = 0; vb < 4; ++vb)
+                dwa[hb][vb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (want_dx) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 wf[4];
+#pragma unroll
+                for (int hb = 0; hb < 4; ++hb) {
+                    wf[hb] = *reinterpret_cast<const u32x4 *>(wt + (fo ^ (uint32_t)(64 * ks)) + hb * 16 * 128);
+                    if (__builtin_expect(cur.n < kFewStep, 0)) {
+                        // columns past the lane: its padding, or another row
+                        const int left = cur.n - 32 * ks - 8 * g;
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            wf[hb][d] &= (left > 2 * d ? 0x0000FFFFu : 0u) | (left > 2 * d + 1 ? 0xFFFF0000u : 0u);
+                    }
+                }
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) {
+                        const u32x4 zf = *reinterpret_cast<const u32x4 *>(
+                            zt + (fo ^ (uint32_t)(64 * ks)) + (part * kBp + 16 * mb) * 128);
+#pragma unroll
+                        for (int hb = 0; hb < 4; ++hb)
+                            dxa[hb][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, wf[hb]), __builtin_bit_cast(bf16x8, zf),
+                                dxa[hb][mb], 0, 0, 0);
+                    }
+            }
+        }
+        if (want_dw) {
+#pragma unroll
+            for (int kc = 0; kc < kKc; ++kc)
+#pragma unroll
+                for (int vb = 0; vb < 4; ++vb) {
+                    // dz across: row 32 kc + 8 g + i / 4 (+ 4), columns 32 (vb / 2)
+                    // + 8 (i % 4) + 4 (vb % 2) .. + 3: the MFMAs vb and vb + 1 leave
+                    // 8 consecutive columns in a lane
+                    const int r = 32 * kc + 8 * g + (n >> 2);
+                    const int q = 4 * (vb >> 1) + (n & 3);
+                    const uint8_t *p0 = zt + r * 128 + ((q ^ ((r >> 1) & 7)) * 16) + 8 * (vb & 1);
+                    const uint8_t *p1 = zt + (r + 4) * 128 + ((q ^ (((r + 4) >> 1) & 7)) * 16) + 8 * (vb & 1);
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                    const u32x2 lo = __builtin_bit_cast(u32x2, read_across((lds_s16x4)p0));
+                    const u32x2 hi = __builtin_bit_cast(u32x2, read_across((lds_s16x4)p1));
+                    const u32x4 zf = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+                    for (int hb = 0; hb < 4; ++hb)
+                        dwa[hb][vb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, zf), __builtin_bit_cast(bf16x8, xf[hb][kc % kXc]),
+                            dwa[hb][vb], 0, 0, 0);
+                }
+        }
+        wait_lds();  // the tiles are read: their slot can be filled again
+        const Cols done = cur;
+        cur = next;
+        next = load(slot, st + 2 * kFewWaves);
+        asm volatile("" ::: "memory");  // the stores below stay behind these loads
+        stored = want_dw && done.n == kFewStep && hrows == kFewH;
+        if (want_dw) {
+#pragma unroll
+            for (int hb = 0; hb < 4; ++hb) {
+                const int h = hw + 16 * hb + n;
+                if (h >= a.H)
+                    continue;
+                uint16_t *row = a.vocab.dw[done.lane] + (int64_t)h * a.lddw + done.c;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int c = 32 * half + 8 * g;
+                    bf16x8 v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = (__bf16)dwa[hb][2 * half + (e >> 2)][e & 3];
+                    if (c + 8 <= done.n) {
+                        *reinterpret_cast<bf16x8 *>(row + c) = v;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < done.n)
+                                row[c + e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
+                    }
+                }
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // the ring's last (empty) loads
+    if (want_dx)
+#pragma unroll
+        for (int hb = 0; hb < 4; ++hb) {
+            const int h = hw + 16 * hb + 4 * g;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const int b = 16 * mb + n;
+                if (b < a.B && h < a.H)
+                    *reinterpret_cast<f32x4 *>(a.dxp + ((int64_t)(split * kFewWaves + wave) * a.B + b) * a.ldxp + h) =
+                        dxa[hb][mb];
+            }
+        }
+}
+
+// Four columns per thread; PARTS threads share a sum (splits p, p + PARTS, ..
+// in ascending order each, then the parts in order).
+template <int PARTS>
 __global__ __launch_bounds__(256) void dx_finish_kernel(const LossArgs a)
 {
+    __shared__ f32x4 sums[PARTS][256 / PARTS];
     const int64_t quads = a.ldxp / 4;
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int q = threadIdx.x % (256 / PARTS), part = threadIdx.x / (256 / PARTS);
+    const int64_t at = (int64_t)blockIdx.x * (256 / PARTS) + q;
     const int64_t b = at / quads;
     const int c = (int)(at - b * quads) * 4;
-    if (b >= a.B || c >= a.H)
+    const bool ok = b < a.B;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (ok) {
+        const float *p = a.dxp + b * a.ldxp + c;
+#pragma unroll 4
+        for (int i = part; i < a.splits; i += PARTS)
+            s += *reinterpret_cast<const f32x4 *>(p + (int64_t)i * a.B * a.ldxp);
+    }
+    if (PARTS > 1) {
+        sums[part][q] = s;
+        __syncthreads();
+        if (part > 0)
+            return;
+#pragma unroll
+        for (int i = 1; i < PARTS; ++i)
+            s += sums[i][q];
+    }
+    if (!ok)
         return;
-    const float *p = a.dxp + b * a.ldxp + c;
-    f32x4 s = *reinterpret_cast<const f32x4 *>(p);
-    for (int i = 1; i < a.splits; ++i)
-        s += *reinterpret_cast<const f32x4 *>(p + (int64_t)i * a.B * a.ldxp);
     const float v[4] = {s[0], s[1], s[2], s[3]};
     store_bf16x4(a.dx + b * a.lddx + c, v, a.H - c);
 }
@@ -394,14 +967,62 @@ hipError_t launch_logits(const LossArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int USE>
+hipError_t launch_logits_rows(const LossArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((int64_t)a.nblk * (kVocabBlock / kLossSmallTile) * a.slices));
+    if (a.B <= 16)
+        hipLaunchKernelGGL((logits_rows_kernel<1, USE>), grid, dim3(kRowsThreads), 0, s, a);
+    else if (a.B <= 32)
+        hipLaunchKernelGGL((logits_rows_kernel<2, USE>), grid, dim3(kRowsThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((logits_rows_kernel<4, USE>), grid, dim3(kRowsThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.slices == 1)
+        return e;
+    hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.nblk, a.slices), a.B), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Steps of a workgroup where `splits` of them share the blocks.
+inline int few_steps(int nblk, int splits)
+{
+    const int steps = nblk * (kVocabBlock / kFewStep);
+    return ((steps + splits - 1) / splits + kFewWaves - 1) / kFewWaves * kFewWaves;
+}
+
+template <int MB>
+hipError_t launch_few(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s)
+{
+    static std::atomic<uint64_t> lds_done{0};
+    const hipError_t e = allow_lds((const void *)grad_rows_kernel<MB>, FewShape<MB>::kLds, lds_done);
+    if (e != hipSuccess)
+        return e;
+    const int htiles = (a.H + kFewH - 1) / kFewH;
+    const int splits = a.splits / kFewWaves;
+    hipLaunchKernelGGL(grad_rows_kernel<MB>, dim3((unsigned)((int64_t)htiles * splits)), dim3(kFewThreads),
+                       FewShape<MB>::kLds, s, a, htiles, few_steps(a.nblk, splits), (int)want_dx, (int)want_dw);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_loss_blocks(const LossArgs &a, hipStream_t s) { return launch_logits<kUseLoss>(a, s); }
+hipError_t launch_loss_blocks(const LossArgs &a, hipStream_t s)
+{
+    return a.B <= kLossSmallRows ? launch_logits_rows<kUseLoss>(a, s) : launch_logits<kUseLoss>(a, s);
+}
 
-hipError_t launch_dlogits(const LossArgs &a, hipStream_t s) { return launch_logits<kUseGrad>(a, s); }
+hipError_t launch_dlogits(const LossArgs &a, hipStream_t s)
+{
+    return a.B <= kLossSmallRows ? launch_logits_rows<kUseGrad>(a, s) : launch_logits<kUseGrad>(a, s);
+}
 
 hipError_t launch_loss_combine(const LossArgs &a, hipStream_t s)
 {
+    if (a.B <= kLossSmallRows) {
+        hipLaunchKernelGGL(loss_rows_combine_kernel, dim3(a.B), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(loss_combine_kernel, dim3((unsigned)(((int64_t)a.B + 63) / 64)),
                        dim3(kCombineWaves * 64), 0, s, a);
     return hipGetLastError();
@@ -432,17 +1053,55 @@ hipError_t launch_grad(const LossArgs &a, bool want_dx, bool want_dw, hipStream_
     return hipGetLastError();
 }
 
+hipError_t launch_grad_rows(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s)
+{
+    if (a.B <= 16)
+        return launch_few<1>(a, want_dx, want_dw, s);
+    if (a.B <= 32)
+        return launch_few<2>(a, want_dx, want_dw, s);
+    return launch_few<4>(a, want_dx, want_dw, s);
+}
+
 hipError_t launch_dx_finish(const LossArgs &a, hipStream_t s)
 {
     const int64_t items = (int64_t)a.B * (a.ldxp / 4);
     if (items <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(dx_finish_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a);
+    if (a.B <= kLossSmallRows)
+        hipLaunchKernelGGL(dx_finish_kernel<8>, dim3((unsigned)((items + 31) / 32)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(dx_finish_kernel<1>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+int loss_slices(int32_t B, int32_t H, int32_t nblk)
+{
+    const int tiles = nblk * (kVocabBlock / kLossSmallTile);
+    if (B > kLossSmallRows || tiles <= 0)
+        return 1;
+    const int steps = (H + kLossStepK - 1) / kLossStepK;
+    const int s = std::max(1, std::min(1024 / tiles, steps / 16));
+    const int per = loss_slice_steps(H, s);
+    return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
+}
+
+int loss_slice_steps(int32_t H, int slices)
+{
+    const int steps = (H + kLossStepK - 1) / kLossStepK;
+    return ((steps + slices - 1) / slices + kRowsWaves - 1) / kRowsWaves * kRowsWaves;
 }
 
 int dx_splits(int32_t B, int32_t H, int32_t nblk)
 {
+    if (B <= kLossSmallRows) {
+        // one workgroup of the streaming kernel to a CU (its LDS allows no
+        // more); each of its waves has a partial sum of its own
+        const int htiles = std::max(1, (H + kFewH - 1) / kFewH);
+        const int steps = nblk * (kVocabBlock / kFewStep);
+        const int s = std::max(1, std::min(256 / htiles, steps / kFewWaves));
+        const int per = few_steps(nblk, s);
+        return (steps + per - 1) / per * kFewWaves;
+    }
     const int64_t tiles = (int64_t)((B + kTile - 1) / kTile) * ((H + kTile - 1) / kTile);
     if (tiles <= 0)
         return 1;
@@ -458,6 +1117,11 @@ int64_t loss_launch_items(int32_t B, int32_t H, int32_t nblk, int32_t splits)
     const int64_t grad = tile_count(tile_grid(B, H)) * splits +
                          tile_count(tile_grid(H, (int64_t)nblk * kTile));
     int64_t items = (std::max(logits, grad) + 16) * kTileThreads;
+    if (B <= kLossSmallRows) {
+        const int64_t rows = (int64_t)nblk * (kVocabBlock / kLossSmallTile) * loss_slices(B, H, nblk);
+        const int64_t few = ((int64_t)H + kFewH - 1) / kFewH * (splits / kFewWaves);
+        items = std::max(std::max(rows * kRowsThreads, few * kFewThreads), (int64_t)loss_parts(nblk, 2) * 256);
+    }
     items = std::max(items, ((int64_t)B + 63) / 64 * 64 * kCombineWaves);
     return std::max(items, ((int64_t)B * (((int64_t)H + 7) / 8 * 8) / 4 + 255) / 256 * 256);
 }

@@ -33,7 +33,8 @@ constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 struct Layout {
     int blocks = 0, piece = 0, splits = 1;
     bool direct = false;  // dx written without partial sums
-    size_t mse = 0, zt = 0, dz = 0, xm = 0, dxp = 0, total = 0;
+    int slices = 1;       // K slices of the logits (few rows)
+    size_t zp = 0, mse = 0, zt = 0, dz = 0, xm = 0, dxp = 0, total = 0;
     int64_t ldz = 0, ldxm = 0, ldxp = 0;
 };
 
@@ -47,12 +48,33 @@ Layout layout(const sb_head_desc *d, bool grad)
     }
     const size_t B = (size_t)d->B;
     size_t at = 0;
+    const bool few = d->B <= sbk::kLossSmallRows;
+    if (few) {
+        L.slices = sbk::loss_slices(d->B, d->H, L.blocks);
+        if (L.slices > 1) {
+            L.zp = at;
+            at = up(at + (size_t)L.slices * B * L.blocks * sbk::kVocabBlock * sizeof(float), kRegionAlign);
+        }
+    }
     if (!grad) {
         L.mse = at;
-        at = up(at + B * L.blocks * sizeof(float2), kRegionAlign);
+        at = up(at + B * (few ? sbk::loss_parts(L.blocks, L.slices) : L.blocks) * sizeof(float2),
+                kRegionAlign);
         L.zt = at;
         at = up(at + B * sizeof(float), kRegionAlign);
         L.total = at;
+        return L;
+    }
+    if (few) {
+        // all of dz; dx in partial sums
+        L.piece = L.blocks;
+        L.splits = sbk::dx_splits(d->B, d->H, L.blocks);
+        L.ldz = (int64_t)L.blocks * sbk::kVocabBlock;
+        L.ldxp = ((int64_t)d->H + 3) & ~(int64_t)3;
+        L.dz = at;
+        at = up(at + sbk::dz_parts(d->B) * B * (size_t)L.ldz * 2, kRegionAlign);
+        L.dxp = at;
+        L.total = up(at + (size_t)L.splits * B * (size_t)L.ldxp * sizeof(float), kRegionAlign);
         return L;
     }
     const int64_t most = kPieceBytes / ((int64_t)d->B * sbk::kVocabBlock * 2);
@@ -140,6 +162,15 @@ void fill(const sb_head_desc *d, const int32_t *targets, sbk::LossArgs &a)
     a.splits = 1;
 }
 
+// The K slices of a call of few rows.
+void set_slices(const sb_head_desc *d, const Layout &L, void *ws, sbk::LossArgs &a)
+{
+    a.slices = L.slices;
+    a.slice_steps = sbk::loss_slice_steps(d->H, L.slices);
+    if (L.slices > 1)
+        a.zp = region<float>(ws, L.zp);
+}
+
 }  // namespace
 
 extern "C" {
@@ -167,7 +198,9 @@ sb_status sb_cross_entropy(const sb_head_desc *desc, const int32_t *targets, flo
         return st;
     sbk::LossArgs a;
     fill(desc, targets, a);
+    set_slices(desc, L, ws, a);
     a.mse = region<float2>(ws, L.mse);
+    a.parts = sbk::loss_parts(L.blocks, L.slices);
     a.zt = region<float>(ws, L.zt);
     a.loss = loss;
     a.lse = lse;
@@ -225,6 +258,16 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
     if (desc->B == 0)  // dw of no rows is zero
         return sbk::launch_grad(a, false, true, s) == hipSuccess ? SB_OK : SB_ERR_HIP;
     a.dz = region<uint16_t>(ws, L.dz);
+    if (desc->B <= sbk::kLossSmallRows) {
+        set_slices(desc, L, ws, a);
+        a.dxp = region<float>(ws, L.dxp);
+        a.ldxp = L.ldxp;
+        if (sbk::launch_dlogits(a, s) != hipSuccess ||
+            sbk::launch_grad_rows(a, dx != nullptr, dw != nullptr, s) != hipSuccess ||
+            (dx && sbk::launch_dx_finish(a, s) != hipSuccess))
+            return SB_ERR_HIP;
+        return SB_OK;
+    }
     a.xm = region<uint16_t>(ws, L.xm);
     if (!L.direct) {
         a.dxp = region<float>(ws, L.dxp);

@@ -148,14 +148,20 @@ __device__ __forceinline__ void stage_offsets(uint32_t (&vo)[4], int wave, int L
     }
 }
 
+// 64 lanes' 16 bytes at offsets vo into 1 KB of LDS.
+template <int POLICY = 0>
+__device__ __forceinline__ void load_to_lds(uint8_t *lds, __amdgpu_buffer_rsrc_t r, uint32_t vo)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, vo, 0, 0,
+                                             POLICY);
+}
+
 __device__ __forceinline__ void stage_load(uint8_t *lds, __amdgpu_buffer_rsrc_t r,
                                            const uint32_t (&vo)[4], int wave)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (__attribute__((address_space(3))) void *)(lds + (4 * wave + i) * 1024), 16, vo[i],
-            0, 0, 0);
+        load_to_lds(lds + (4 * wave + i) * 1024, r, vo[i]);
 }
 
 // Zero the K bytes at and past `kbytes` (< 128) of a kAlongK stage: what lies
@@ -233,6 +239,10 @@ __device__ __forceinline__ void block_mma(i32x4 &c, const u32x4 &row, const u32x
 }
 
 constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;
+
+// The operand of s_waitcnt that waits for all but the wave's last n (< 64)
+// vector memory operations, and for nothing else.
+constexpr int vmcnt_only(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 
 // A workgroup barrier that no memory operation is moved across.  Unlike
 // __syncthreads() it does not wait for loads into LDS that are still in flight.

@@ -7,6 +7,7 @@ allocates the workspace through torch when none is given, and raises
 the call's stream and recorded as used by it.  There is no fallback: if libsb.so is
 missing, loading fails with an error.
 """
+import contextlib
 import ctypes
 import os
 
@@ -447,19 +448,31 @@ def sb_partial_complete(part, op, out, ws=None, stream=None):
 # ---------------------------------------------------------------------------
 def _one_device(tensors):
     """The device that holds every tensor of a call."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-    return devices.pop()
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+    return device
 
 
 def _as_list(w):
     return list(w) if isinstance(w, (list, tuple)) else [w]
 
 
+def _on(device):
+    """`device` made current for the block (no-op where it already is)."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 def _run(name, device, stream, nbytes_fn, ws, call):
     """call(workspace pointer, its size, stream) on `device`."""
-    with torch.cuda.device(device):
+    with _on(device):
         ws = _workspace(nbytes_fn, ws, device, stream)
         _check(call(_ptr(ws), ws.numel(), _stream(stream)), name)
 
@@ -616,7 +629,7 @@ def sb_int8_quantize_rows(x, q, scale, stream=None):
     B, H = x.shape
     _matrix(q, "q", torch.int8, B, H)
     _vector(scale, "scale", torch.float32, B)
-    with torch.cuda.device(_one_device([x, q, scale])):
+    with _on(_one_device([x, q, scale])):
         _check(lib().sb_int8_quantize_rows(_ptr(x), x.stride(0), B, H, _ptr(q), q.stride(0),
                                            _ptr(scale), _stream(stream)), "sb_int8_quantize_rows")
     return q, scale
@@ -645,7 +658,7 @@ def sb_int8_quantize_head(head, q, scale, stream=None):
         qp = [q.data_ptr() + ldq * o for o in off[:-1]]
         sp = [scale.data_ptr() + 4 * o for o in off[:-1]]
     weights = _as_list(head.w) if head.from_tensors else []
-    with torch.cuda.device(_one_device(_as_list(q) + _as_list(scale) + weights)):
+    with _on(_one_device(_as_list(q) + _as_list(scale) + weights)):
         _check(lib().sb_int8_quantize_head(head.ref(), (ctypes.c_void_p * k)(*qp), ldq,
                                            (ctypes.c_void_p * k)(*sp), _stream(stream)),
                "sb_int8_quantize_head")

@@ -29,11 +29,20 @@ def grad(h, t=FAKE, lse=FAKE, d=FAKE, dx=FAKE, lddx=512, dw=(FAKE, FAKE), lddw=4
 
 
 def test_workspace_sizes():
-    h = fake_head()                     # B=16, H=512, V=4096: 8 + 8 blocks of 256 columns
-    assert sb.sb_cross_entropy_workspace_bytes(h, False) == 16 * 16 * 8 + 256
-    # dz of all blocks, the masked rows, and dx partial sums in 16 K splits
-    assert sb.sb_cross_entropy_workspace_bytes(h, True) == \
-        16 * 4096 * 2 + 16 * 512 * 2 + 16 * 16 * 512 * 4
+    # 16 rows, H=512, V=4096 in two lanes of 8 blocks of 256 columns: 32 tiles
+    # of 128 columns and one K slice (its 16 steps are not split): a result per row and tile
+    h = fake_head()
+    assert sb.sb_cross_entropy_workspace_bytes(h, False) == 16 * 32 * 8 + 256
+    # with 64 steps, four slices of the logits and one result per 1024 columns
+    deep = fake_head(H=2048, ldx=2048)
+    assert sb.sb_cross_entropy_workspace_bytes(deep, False) == 4 * 16 * 4096 * 4 + 16 * 4 * 8 + 256
+    # dz in two parts, dx in 64 partial sums (one per 64 columns)
+    assert sb.sb_cross_entropy_workspace_bytes(h, True) == 2 * 16 * 4096 * 2 + 64 * 16 * 512 * 4
+    # MFMA tiles: a result per row and block; dz, the masked rows and dx in 16 sums
+    mid = fake_head(B=100)
+    assert sb.sb_cross_entropy_workspace_bytes(mid, False) == 100 * 16 * 8 + 512
+    assert sb.sb_cross_entropy_workspace_bytes(mid, True) == \
+        100 * 4096 * 2 + 100 * 512 * 2 + 16 * 100 * 512 * 4
     for g in (False, True):
         assert sb.sb_cross_entropy_workspace_bytes(fake_head(B=0), g) == 0
     # a large batch: dz in pieces of at most 256 MiB, and no logits anywhere

@@ -42,6 +42,12 @@ struct Int8Args {
     int32_t *part;                    // [slices][B][tiles * kInt8SmallTile]
 };
 
+// Whether the MFMA kernel runs small tiles (`tiles` of kInt8LargeTile channels):
+// 0.8 of the big ones' time up to 128 rows, 0.7 to 0.8 on 56 to 112 tiles, 1.2
+// where big tiles fill the card.
+constexpr int kInt8TileSmallRows = 128, kInt8SmallTiles = 128;
+bool int8_small(int32_t B, int32_t tiles);
+
 constexpr int kInt8StepK = 128;  // a cache line of every channel
 constexpr int kInt8Chunk = 1024;
 

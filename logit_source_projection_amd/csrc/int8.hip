@@ -17,7 +17,7 @@
 namespace sbk {
 namespace {
 
-static_assert(kInt8LargeTile == kTile, "a large tile is one MFMA tile wide");
+static_assert(kInt8LargeTile == BigTile::kN && kInt8LargeTile % SmallTile::kN == 0, "no tile spans two lanes");
 
 // The order of the argmax: NaN above every number, then larger values, then
 // lower indices (the projection calls' order).
@@ -259,50 +259,53 @@ struct Int8Src {
     __device__ __forceinline__ int tail(int st) const { return min(H - st * kStageBytes, kStageBytes); }
 };
 
-template <bool TOKENS>
-__global__ __launch_bounds__(kTileThreads, 1) void int8_tile_kernel(const Int8Args a, const TileGrid grid)
+template <class C, bool TOKENS>
+__global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const Int8Args a, const TileGrid grid)
 {
+    constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int number = xcd_tile(blockIdx.x, grid.mt * grid.nt);
     if (number < 0)
         return;
     int mt, nt;
     tile_of(grid, number, mt, nt);
-    const int lane = tile_lane(a, nt);
-    const int c0 = (nt - a.tile0[lane]) * kTile;
-    const int nvalid = min(kTile, a.off[lane + 1] - a.off[lane] - c0);
-    const int m0 = mt * kTile, rows = min(a.B - m0, kTile);
+    const int block = nt / (kInt8LargeTile / kN);
+    const int lane = tile_lane(a, block);
+    // first channel inside the lane (a block's later tiles can lie past it)
+    const int c0 = (block - a.tile0[lane]) * kInt8LargeTile + nt % (kInt8LargeTile / kN) * kN;
+    const int nvalid = max(0, min(kN, a.off[lane + 1] - a.off[lane] - c0));
+    const int m0 = mt * kM, rows = min(a.B - m0, kM);
     const int H = a.H;
     Int8Src src;
     src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
     src.w = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw);
     src.xbytes = (int64_t)(rows - 1) * a.ldx + ((H + 15) & ~15);
-    src.wbytes = (int64_t)(nvalid - 1) * a.ldw + ((H + 15) & ~15);
+    src.wbytes = nvalid > 0 ? (int64_t)(nvalid - 1) * a.ldw + ((H + 15) & ~15) : 0;
     src.H = H;
-    WaveTile<i32x4> t;
+    WaveTile<C, i32x4> t;
     t.init();
     // a ragged H: x zeroed past it makes the products there 0
-    t.run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
+    t.template run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
 
     const int n = t.L & 15, g = t.L >> 4;
     const int gcol0 = a.off[lane] + c0;
-    float2 *part = reinterpret_cast<float2 *>(smem);  // [kTile][4 column waves]
-    float ws[kColBlocks][4];
+    float2 *part = reinterpret_cast<float2 *>(smem);  // [kM][column waves]
+    float ws[kCB][4];
 #pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb)
+    for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int c = t.col0 + 16 * cb + 4 * g + e;
             ws[cb][e] = c < nvalid ? a.w_scale[lane][c0 + c] : 0.f;
         }
 #pragma unroll
-    for (int rb = 0; rb < kRowBlocks; ++rb) {
+    for (int rb = 0; rb < kRB; ++rb) {
         const int r = t.row0 + 16 * rb + n;
         const float xs = r < rows ? a.x_scale[m0 + r] : 0.f;
         float bv = -INFINITY;
         int bi = INT_MAX;
 #pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb) {
+        for (int cb = 0; cb < kCB; ++cb) {
             const int c = t.col0 + 16 * cb + 4 * g;
             const int left = nvalid - c;
             float z[4];
@@ -320,18 +323,18 @@ __global__ __launch_bounds__(kTileThreads, 1) void int8_tile_kernel(const Int8Ar
             take_better(bv, bi, __shfl_xor(bv, 16), __shfl_xor(bi, 16));
             take_better(bv, bi, __shfl_xor(bv, 32), __shfl_xor(bi, 32));
             if (g == 0)
-                part[r * 4 + (t.wave & 3)] = make_float2(bv, __int_as_float(bi));
+                part[r * kWN + t.wave % kWN] = make_float2(bv, __int_as_float(bi));
         }
     }
     if (TOKENS) {
         __syncthreads();
         const int r = threadIdx.x;
         if (r < rows) {
-            float v = part[r * 4].x;
-            int i = __float_as_int(part[r * 4].y);
+            float v = part[r * kWN].x;
+            int i = __float_as_int(part[r * kWN].y);
 #pragma unroll
-            for (int w = 1; w < 4; ++w)
-                take_better(v, i, part[r * 4 + w].x, __float_as_int(part[r * 4 + w].y));
+            for (int w = 1; w < kWN; ++w)
+                take_better(v, i, part[r * kWN + w].x, __float_as_int(part[r * kWN + w].y));
             a.pair[(int64_t)(m0 + r) * a.pairs + nt] = make_int2(__float_as_int(v), i);
         }
     }
@@ -612,17 +615,24 @@ hipError_t launch_rows(const Int8Args &a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <class C, bool TOKENS>
+hipError_t launch_tiles_as(const Int8Args &a, hipStream_t s)
+{
+    const TileGrid g = tile_grid<C>(a.B, (int64_t)a.tile0[a.k] * kInt8LargeTile);
+    static std::atomic<uint64_t> lds_done{0};
+    const hipError_t e = allow_lds((const void *)int8_tile_kernel<C, TOKENS>, C::kLds, lds_done);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((int8_tile_kernel<C, TOKENS>), dim3((unsigned)xcd_ids(tile_count(g))), dim3(C::kThreads),
+                       C::kLds, s, a, g);
+    return hipGetLastError();
+}
+
 template <bool TOKENS>
 hipError_t launch_tiles(const Int8Args &a, hipStream_t s)
 {
-    const TileGrid g = tile_grid(a.B, (int64_t)a.tile0[a.k] * kTile);
-    static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds((const void *)int8_tile_kernel<TOKENS>, kTileLdsBytes, lds_done);
-    if (e != hipSuccess)
-        return e;
-    hipLaunchKernelGGL(int8_tile_kernel<TOKENS>, dim3((unsigned)xcd_ids(tile_count(g))),
-                       dim3(kTileThreads), kTileLdsBytes, s, a, g);
-    return hipGetLastError();
+    return int8_small(a.B, a.tile0[a.k]) ? launch_tiles_as<SmallTile, TOKENS>(a, s)
+                                         : launch_tiles_as<BigTile, TOKENS>(a, s);
 }
 
 }  // namespace
@@ -638,6 +648,12 @@ int int8_slices(int32_t B, int32_t H, int32_t tiles)
     const int s = std::max(1, std::min(512 / tiles, steps / 8));
     const int per = int8_slice_steps(H, s);
     return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
+}
+
+bool int8_small(int32_t B, int32_t tiles)
+{
+    return B <= kInt8TileSmallRows ||
+           tile_count(tile_grid<BigTile>(B, (int64_t)tiles * kInt8LargeTile)) <= kInt8SmallTiles;
 }
 
 int int8_slice_steps(int32_t H, int slices)
@@ -698,8 +714,8 @@ int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices)
     const int64_t rows = (int64_t)B * kIdsThreads;  // one workgroup per row
     if (B <= kInt8SmallRows)
         return std::max(rows, tiles * slices * kRowsThreads);
-    const int64_t mt = (B + kTile - 1) / kTile;
-    return std::max(rows, (mt * tiles + 8) * kTileThreads);
+    // the small tiles' launch holds twice the work items of the big ones'
+    return std::max(rows, (tile_count(tile_grid<SmallTile>(B, tiles * kInt8LargeTile)) + 8) * SmallTile::kThreads);
 }
 
 }  // namespace sbk

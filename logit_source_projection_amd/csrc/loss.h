@@ -34,9 +34,9 @@ struct LossArgs {
     int32_t slices, slice_steps;
     float *zp;               // fp32 [slices][B][blocks * kVocabBlock], with two slices or more
     // loss
-    float2 *mse;             // {maximum, sum exp(z - maximum)}: [blocks][B], or with up to
+    float2 *mse;             // {maximum, sum exp(z - maximum)}: [parts][B], or with up to
                              // kLossSmallRows rows [B][parts]
-    int32_t parts;
+    int32_t parts;           // runs of columns that the row's sum is made of
     float *zt;               // [B] the target's logit
     float *loss, *lse;       // [B]
     // gradient
@@ -66,8 +66,20 @@ constexpr int kLossChunk = 1024;      // columns per workgroup that adds slices 
 // sums of few terms a lone dz's rounding would be the whole result's, so up to
 // 32 rows a second part holds what the first leaves.
 constexpr int dz_parts(int B) { return B <= 32 ? 2 : 1; }
-inline int loss_parts(int nblk, int slices)
+// Whether the logits of nblk blocks, and the gradient's two products, run small
+// tiles (batches of more than kLossSmallRows rows).  Small tiles read each
+// operand twice as often and ran 20 to 30 % longer where big ones fill the card,
+// but took 0.66 to 0.91 of their time on fewer tiles than half the CUs (56 to
+// 112 tiles; 198 tiles: 1.5), and 0.8 to 0.98 up to 128 rows, where a big tile
+// is half empty.  The gradient has many short products: 0.62 to 0.86 up to
+// 448 (tiles of dw) x (256-row blocks), 1.15 at 1792.
+constexpr int kSmallRows = 128, kSmallLogitsTiles = 128, kSmallGradTiles = 1024;
+bool small_logits(int32_t B, int32_t nblk);
+bool small_grad(int32_t B, int32_t H, int32_t nblk);
+inline int loss_parts(int B, int nblk, int slices)
 {
+    if (B > kLossSmallRows)
+        return small_logits(B, nblk) ? 2 * nblk : nblk;
     return slices > 1 ? (nblk * kVocabBlock + kLossChunk - 1) / kLossChunk
                       : nblk * (kVocabBlock / kLossSmallTile);
 }

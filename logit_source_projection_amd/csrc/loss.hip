@@ -20,7 +20,7 @@
 namespace sbk {
 namespace {
 
-static_assert(kVocabBlock == kTile, "a vocabulary block is one tile wide");
+static_assert(kVocabBlock == BigTile::kN && kVocabBlock % SmallTile::kN == 0, "no tile spans two blocks");
 
 __device__ __forceinline__ int block_lane(const VocabTable &t, int nb)
 {
@@ -79,21 +79,23 @@ struct LogitsSrc {
 
 
 
-template <int USE>
-__global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs a, const TileGrid grid)
+template <class C, int USE>
+__global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const LossArgs a, const TileGrid grid)
 {
+    constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int number = xcd_tile(blockIdx.x, grid.mt * grid.nt);
     if (number < 0)
         return;
     int mt, nt;
     tile_of(grid, number, mt, nt);
-    const int nb = a.nb0 + nt;
+    const int nb = a.nb0 + nt / (kVocabBlock / kN);
     const int lane = block_lane(a.vocab, nb);
-    const int c0 = (nb - a.vocab.blk0[lane]) * kTile;  // first column inside the lane
-    const int nvalid = min(kTile, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0);
-    const int m0 = mt * kTile;
-    const int rows = min(a.B - m0, kTile);
+    // first column inside the lane (a block's later tiles can lie past it)
+    const int c0 = (nb - a.vocab.blk0[lane]) * kVocabBlock + nt % (kVocabBlock / kN) * kN;
+    const int nvalid = max(0, min(kN, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0));
+    const int m0 = mt * kM;
+    const int rows = min(a.B - m0, kM);
     const int H = a.H;
 
     LogitsSrc src;
@@ -101,24 +103,24 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs 
     src.w = reinterpret_cast<const uint8_t *>(a.vocab.w[lane] + c0);
     src.ldw_bytes = a.ldw * 2;
     src.xbytes = ((int64_t)(rows - 1) * a.ldx + ((H + 7) & ~7)) * 2;
-    src.wbytes = ((int64_t)(H - 1) * a.ldw + ((nvalid + 7) & ~7)) * 2;
+    src.wbytes = nvalid > 0 ? ((int64_t)(H - 1) * a.ldw + ((nvalid + 7) & ~7)) * 2 : 0;
     src.H = H;
-    WaveTile<f32x4> t;
+    WaveTile<C, f32x4> t;
     t.init();
-    t.run<kAlongK, kAcrossK, true, false>(smem, (H + kStageK - 1) / kStageK, a.ldx * 2, a.ldw * 2,
+    t.template run<kAlongK, kAcrossK, true, false>(smem, (H + kStageK - 1) / kStageK, a.ldx * 2, a.ldw * 2,
                                           src);
 
     const int n = t.L & 15, g = t.L >> 4;
     const int gcol0 = a.vocab.off[lane] + c0;
     if (USE == kUseLoss) {
-        float2 *part = reinterpret_cast<float2 *>(smem);  // [kTile][4 column waves]
+        float2 *part = reinterpret_cast<float2 *>(smem);  // [kM][column waves]
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb) {
+        for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
             const int tgt = r < rows ? a.targets[m0 + r] - gcol0 : -1;  // target's column in the tile
             float m = -INFINITY;
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb)
+            for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = t.col0 + 16 * cb + 4 * g + e;
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs 
             const float at = m == -INFINITY ? 0.f : m;
             float s = 0.f;
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb)
+            for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (t.col0 + 16 * cb + 4 * g + e < nvalid)
@@ -141,20 +143,20 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs 
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (g == 0)
-                part[r * 4 + (t.wave & 3)] = make_float2(m, s);
+                part[r * kWN + t.wave % kWN] = make_float2(m, s);
         }
         __syncthreads();
         const int r = threadIdx.x;
         if (r < rows) {
-            float2 p = part[r * 4];
+            float2 p = part[r * kWN];
 #pragma unroll
-            for (int w = 1; w < 4; ++w)
-                merge_ms(p.x, p.y, part[r * 4 + w].x, part[r * 4 + w].y);
-            a.mse[(int64_t)nb * a.B + m0 + r] = p;
+            for (int w = 1; w < kWN; ++w)
+                merge_ms(p.x, p.y, part[r * kWN + w].x, part[r * kWN + w].y);
+            a.mse[(int64_t)nt * a.B + m0 + r] = p;
         }
     } else {
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb) {
+        for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
             if (r >= rows)
                 continue;
@@ -162,9 +164,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs 
             const float l = a.lse_in[m0 + r];
             // a target past the vocabulary has no gradient: NaN, not a guess
             const float scale = tgt >= a.V ? NAN : a.dloss[m0 + r];
-            uint16_t *out = a.dz + (int64_t)(m0 + r) * a.ldz + (int64_t)nt * kTile;
+            uint16_t *out = a.dz + (int64_t)(m0 + r) * a.ldz + (int64_t)nt * kN;
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb) {
+            for (int cb = 0; cb < kCB; ++cb) {
                 const int c = t.col0 + 16 * cb + 4 * g;
                 float v[4];
 #pragma unroll
@@ -178,7 +180,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_kernel(const LossArgs 
     }
 }
 
-// One row per lane; wave w merges blocks w, w + 16, ... in ascending order and
+// One row per lane; wave w merges parts w, w + 16, ... in ascending order and
 // the waves are merged in wave order.
 constexpr int kCombineWaves = 16;
 __global__ __launch_bounds__(kCombineWaves * 64) void loss_combine_kernel(const LossArgs a)
@@ -188,8 +190,8 @@ __global__ __launch_bounds__(kCombineWaves * 64) void loss_combine_kernel(const 
     const int64_t b = (int64_t)blockIdx.x * 64 + L;
     float m = -INFINITY, s = 0.f;
     if (b < a.B)
-        for (int nb = wave; nb < a.nblk; nb += kCombineWaves) {
-            const float2 p = a.mse[(int64_t)nb * a.B + b];
+        for (int i = wave; i < a.parts; i += kCombineWaves) {
+            const float2 p = a.mse[(int64_t)i * a.B + b];
             merge_ms(m, s, p.x, p.y);
         }
     part[wave][L] = make_float2(m, s);
@@ -519,18 +521,18 @@ struct DxSrc {
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
     {
         const int64_t at = (int64_t)st * kStageBytes;
-        return buffer_of(dz + at, st < (nb_end - nb_first) * (kTile / kStageK) ? dzbytes - at : 0);
+        return buffer_of(dz + at, st < (nb_end - nb_first) * (kVocabBlock / kStageK) ? dzbytes - at : 0);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t b(int st)
     {
-        const int nb = nb_first + st / (kTile / kStageK);
+        const int nb = nb_first + st / (kVocabBlock / kStageK);
         if (nb >= nb_end)
             return buffer_of(args.vocab.w[lane], 0);
         while (nb >= lane_end) {
             ++lane;
             lane_end = args.vocab.blk0[lane + 1];
         }
-        const int c = (nb - args.vocab.blk0[lane]) * kTile + st % (kTile / kStageK) * kStageK;
+        const int c = (nb - args.vocab.blk0[lane]) * kVocabBlock + st % (kVocabBlock / kStageK) * kStageK;
         const int width = args.vocab.off[lane + 1] - args.vocab.off[lane];
         const int cols = max(0, min(kStageK, width - c));
         (st & 1 ? tail1 : tail0) = cols * 2;
@@ -562,12 +564,14 @@ struct DwSrc {
 // K (the piece's columns), dW many with a short one (the rows), and each has
 // half the work, so the dX tiles go first and the dW tiles fill the CUs that
 // are left over.
-__global__ __launch_bounds__(kTileThreads, 1) void grad_kernel(const LossArgs a, const TileGrid gx,
-                                                               const int dx_ids, const TileGrid gw)
+template <class C>
+__global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const LossArgs a, const TileGrid gx,
+                                                                      const int dx_ids, const TileGrid gw)
 {
+    constexpr int kM = C::kM, kN = C::kN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    WaveTile<f32x4> t;
+    WaveTile<C, f32x4> t;
     int mt, nt;
     if ((int)blockIdx.x < dx_ids) {
         const int tiles = gx.mt * gx.nt;
@@ -578,27 +582,27 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_kernel(const LossArgs a,
         tile_of(gx, number - split * tiles, mt, nt);
         const int per = (a.nblk + a.splits - 1) / a.splits;
         const int b0 = min(split * per, a.nblk), b1 = min(b0 + per, a.nblk);
-        const int m0 = mt * kTile, rows = min(a.B - m0, kTile);
+        const int m0 = mt * kM, rows = min(a.B - m0, kM);
         DxSrc src(a);
-        src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)m0 * a.ldz + (int64_t)b0 * kTile);
-        src.dzbytes = ((int64_t)(rows - 1) * a.ldz + (int64_t)(b1 - b0) * kTile) * 2;
+        src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)m0 * a.ldz + (int64_t)b0 * kVocabBlock);
+        src.dzbytes = ((int64_t)(rows - 1) * a.ldz + (int64_t)(b1 - b0) * kVocabBlock) * 2;
         src.nb_first = a.nb0 + b0;
         src.nb_end = a.nb0 + b1;
-        src.h0 = nt * kTile;
-        src.hrows = min(a.H - src.h0, kTile);
+        src.h0 = nt * kN;
+        src.hrows = min(a.H - src.h0, kN);
         src.lane = block_lane(a.vocab, src.nb_first);
         src.lane_end = a.vocab.blk0[src.lane + 1];
         src.tail0 = src.tail1 = kStageBytes;
         t.init();
-        t.run<kAlongK, kAlongK, false, true>(smem, (b1 - b0) * (kTile / kStageK), a.ldz * 2,
+        t.template run<kAlongK, kAlongK, false, true>(smem, (b1 - b0) * (kVocabBlock / kStageK), a.ldz * 2,
                                              a.ldw * 2, src);
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb) {
+        for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
             if (r >= rows)
                 continue;
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb) {
+            for (int cb = 0; cb < kCB; ++cb) {
                 const int c = src.h0 + t.col0 + 16 * cb + 4 * g;
                 if (c >= a.H)
                     continue;
@@ -619,29 +623,31 @@ __global__ __launch_bounds__(kTileThreads, 1) void grad_kernel(const LossArgs a,
     if (number < 0)
         return;
     tile_of(gw, number, mt, nt);
-    const int nb = a.nb0 + nt;
+    const int nb = a.nb0 + nt / (kVocabBlock / kN);
     const int lane = block_lane(a.vocab, nb);
-    const int c0 = (nb - a.vocab.blk0[lane]) * kTile;
-    const int nvalid = min(kTile, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0);
-    const int h0 = mt * kTile, hrows = min(a.H - h0, kTile);
+    const int c0 = (nb - a.vocab.blk0[lane]) * kVocabBlock + nt % (kVocabBlock / kN) * kN;
+    const int nvalid = min(kN, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0);
+    if (nvalid <= 0)
+        return;
+    const int h0 = mt * kM, hrows = min(a.H - h0, kM);
     DwSrc src;
     src.x = reinterpret_cast<const uint8_t *>(a.xm + h0);
-    src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)nt * kTile);
+    src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)nt * kN);
     src.ldx_bytes = a.ldxm * 2;
     src.ldz_bytes = a.ldz * 2;
     src.xbytes = ((int64_t)(a.B - 1) * a.ldxm + ((hrows + 7) & ~7)) * 2;
-    src.zbytes = ((int64_t)(a.B - 1) * a.ldz + kTile) * 2;
+    src.zbytes = ((int64_t)(a.B - 1) * a.ldz + kN) * 2;
     t.init();
-    t.run<kAcrossK, kAcrossK, false, false>(smem, (a.B + kStageK - 1) / kStageK, a.ldxm * 2,
+    t.template run<kAcrossK, kAcrossK, false, false>(smem, (a.B + kStageK - 1) / kStageK, a.ldxm * 2,
                                             a.ldz * 2, src);
 #pragma unroll
-    for (int rb = 0; rb < kRowBlocks; ++rb) {
+    for (int rb = 0; rb < kRB; ++rb) {
         const int r = t.row0 + 16 * rb + n;
         if (r >= hrows)
             continue;
         uint16_t *out = a.vocab.dw[lane] + (int64_t)(h0 + r) * a.lddw + c0;
 #pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb) {
+        for (int cb = 0; cb < kCB; ++cb) {
             const int c = t.col0 + 16 * cb + 4 * g;
             const float v[4] = {t.acc[rb][cb][0], t.acc[rb][cb][1], t.acc[rb][cb][2],
                                 t.acc[rb][cb][3]};
@@ -954,16 +960,39 @@ __global__ __launch_bounds__(256) void dx_finish_kernel(const LossArgs a)
     store_bf16x4(a.dx + b * a.lddx + c, v, a.H - c);
 }
 
+template <class C, int USE>
+hipError_t launch_logits_tiles(const LossArgs &a, hipStream_t s)
+{
+    const TileGrid g = tile_grid<C>(a.B, (int64_t)a.nblk * kVocabBlock);
+    static std::atomic<uint64_t> lds_done{0};
+    const hipError_t e = allow_lds((const void *)logits_kernel<C, USE>, C::kLds, lds_done);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((logits_kernel<C, USE>), dim3((unsigned)xcd_ids(tile_count(g))), dim3(C::kThreads),
+                       C::kLds, s, a, g);
+    return hipGetLastError();
+}
+
 template <int USE>
 hipError_t launch_logits(const LossArgs &a, hipStream_t s)
 {
-    const TileGrid g = tile_grid(a.B, (int64_t)a.nblk * kTile);
+    return small_logits(a.B, a.nblk) ? launch_logits_tiles<SmallTile, USE>(a, s)
+                                     : launch_logits_tiles<BigTile, USE>(a, s);
+}
+
+template <class C>
+hipError_t launch_grad_tiles(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s)
+{
+    const TileGrid gx = tile_grid<C>(a.B, a.H), gw = tile_grid<C>(a.H, (int64_t)a.nblk * kVocabBlock);
+    const int64_t dx_ids = want_dx ? xcd_ids(tile_count(gx) * a.splits) : 0;
+    const int64_t ids = dx_ids + (want_dw ? xcd_ids(tile_count(gw)) : 0);
+    if (ids <= 0)
+        return hipSuccess;
     static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds((const void *)logits_kernel<USE>, kTileLdsBytes, lds_done);
+    const hipError_t e = allow_lds((const void *)grad_kernel<C>, C::kLds, lds_done);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(logits_kernel<USE>, dim3((unsigned)xcd_ids(tile_count(g))),
-                       dim3(kTileThreads), kTileLdsBytes, s, a, g);
+    hipLaunchKernelGGL(grad_kernel<C>, dim3((unsigned)ids), dim3(C::kThreads), C::kLds, s, a, gx, (int)dx_ids, gw);
     return hipGetLastError();
 }
 
@@ -980,7 +1009,7 @@ hipError_t launch_logits_rows(const LossArgs &a, hipStream_t s)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slices == 1)
         return e;
-    hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.nblk, a.slices), a.B), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.B, a.nblk, a.slices), a.B), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1039,18 +1068,8 @@ hipError_t launch_mask_rows(const LossArgs &a, uint16_t *xm, hipStream_t s)
 
 hipError_t launch_grad(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s)
 {
-    const TileGrid gx = tile_grid(a.B, a.H), gw = tile_grid(a.H, (int64_t)a.nblk * kTile);
-    const int64_t dx_ids = want_dx ? xcd_ids(tile_count(gx) * a.splits) : 0;
-    const int64_t ids = dx_ids + (want_dw ? xcd_ids(tile_count(gw)) : 0);
-    if (ids <= 0)
-        return hipSuccess;
-    static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds((const void *)grad_kernel, kTileLdsBytes, lds_done);
-    if (e != hipSuccess)
-        return e;
-    hipLaunchKernelGGL(grad_kernel, dim3((unsigned)ids), dim3(kTileThreads), kTileLdsBytes, s, a, gx,
-                       (int)dx_ids, gw);
-    return hipGetLastError();
+    return small_grad(a.B, a.H, a.nblk) ? launch_grad_tiles<SmallTile>(a, want_dx, want_dw, s)
+                                        : launch_grad_tiles<BigTile>(a, want_dx, want_dw, s);
 }
 
 hipError_t launch_grad_rows(const LossArgs &a, bool want_dx, bool want_dw, hipStream_t s)
@@ -1091,6 +1110,18 @@ int loss_slice_steps(int32_t H, int slices)
     return ((steps + slices - 1) / slices + kRowsWaves - 1) / kRowsWaves * kRowsWaves;
 }
 
+bool small_logits(int32_t B, int32_t nblk)
+{
+    return B <= kSmallRows ||
+           tile_count(tile_grid<BigTile>(B, (int64_t)nblk * kVocabBlock)) <= kSmallLogitsTiles;
+}
+
+bool small_grad(int32_t B, int32_t H, int32_t nblk)
+{
+    const int64_t dw = tile_count(tile_grid<BigTile>(H, (int64_t)nblk * kVocabBlock));
+    return B <= kSmallRows || dw * ((B + BigTile::kM - 1) / BigTile::kM) <= kSmallGradTiles;
+}
+
 int dx_splits(int32_t B, int32_t H, int32_t nblk)
 {
     if (B <= kLossSmallRows) {
@@ -1102,25 +1133,28 @@ int dx_splits(int32_t B, int32_t H, int32_t nblk)
         const int per = few_steps(nblk, s);
         return (steps + per - 1) / per * kFewWaves;
     }
-    const int64_t tiles = (int64_t)((B + kTile - 1) / kTile) * ((H + kTile - 1) / kTile);
+    const bool small = small_grad(B, H, nblk);
+    const int64_t tiles = small ? tile_count(tile_grid<SmallTile>(B, H)) : tile_count(tile_grid<BigTile>(B, H));
     if (tiles <= 0)
         return 1;
-    // half of the launch's work is dX: with 128 tiles or more a tile's chain
-    // is within a CU's share
-    const int64_t s = (128 + tiles - 1) / tiles;
+    // half of the launch's work is dX: with a tile for half of the CUs'
+    // workgroups or more a tile's chain is within a CU's share
+    const int64_t most = small ? 256 : 128;
+    const int64_t s = (most + tiles - 1) / tiles;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 32), nblk));
 }
 
 int64_t loss_launch_items(int32_t B, int32_t H, int32_t nblk, int32_t splits)
 {
-    const int64_t logits = tile_count(tile_grid(B, (int64_t)nblk * kTile));
-    const int64_t grad = tile_count(tile_grid(B, H)) * splits +
-                         tile_count(tile_grid(H, (int64_t)nblk * kTile));
-    int64_t items = (std::max(logits, grad) + 16) * kTileThreads;
+    // the small tiles' launches hold twice the work items of the big ones'
+    const int64_t logits = tile_count(tile_grid<SmallTile>(B, (int64_t)nblk * kVocabBlock));
+    const int64_t grad = tile_count(tile_grid<SmallTile>(B, H)) * splits +
+                         tile_count(tile_grid<SmallTile>(H, (int64_t)nblk * kVocabBlock));
+    int64_t items = (std::max(logits, grad) + 16) * SmallTile::kThreads;
     if (B <= kLossSmallRows) {
         const int64_t rows = (int64_t)nblk * (kVocabBlock / kLossSmallTile) * loss_slices(B, H, nblk);
         const int64_t few = ((int64_t)H + kFewH - 1) / kFewH * (splits / kFewWaves);
-        items = std::max(std::max(rows * kRowsThreads, few * kFewThreads), (int64_t)loss_parts(nblk, 2) * 256);
+        items = std::max(std::max(rows * kRowsThreads, few * kFewThreads), (int64_t)loss_parts(1, nblk, 2) * 256);
     }
     items = std::max(items, ((int64_t)B + 63) / 64 * 64 * kCombineWaves);
     return std::max(items, ((int64_t)B * (((int64_t)H + 7) / 8 * 8) / 4 + 255) / 256 * 256);

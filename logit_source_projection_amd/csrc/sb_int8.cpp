@@ -100,6 +100,8 @@ Layout layout(const sb_int8_desc *d, bool tokens)
     if (tokens) {
         L.pairs = L.slices > 1 ? (L.tiles * sbk::kInt8SmallTile + sbk::kInt8Chunk - 1) / sbk::kInt8Chunk
                                : L.tiles;
+        if (d->B > sbk::kInt8SmallRows && sbk::int8_small(d->B, L.tiles))
+            L.pairs *= 2;
         L.pair = at;
         at = up(at + (size_t)L.pairs * d->B * sizeof(int2), kRegionAlign);
     }

@@ -58,8 +58,7 @@ Layout layout(const sb_head_desc *d, bool grad)
     }
     if (!grad) {
         L.mse = at;
-        at = up(at + B * (few ? sbk::loss_parts(L.blocks, L.slices) : L.blocks) * sizeof(float2),
-                kRegionAlign);
+        at = up(at + B * sbk::loss_parts(d->B, L.blocks, L.slices) * sizeof(float2), kRegionAlign);
         L.zt = at;
         at = up(at + B * sizeof(float), kRegionAlign);
         L.total = at;
@@ -200,7 +199,7 @@ sb_status sb_cross_entropy(const sb_head_desc *desc, const int32_t *targets, flo
     fill(desc, targets, a);
     set_slices(desc, L, ws, a);
     a.mse = region<float2>(ws, L.mse);
-    a.parts = sbk::loss_parts(L.blocks, L.slices);
+    a.parts = sbk::loss_parts(desc->B, L.blocks, L.slices);
     a.zt = region<float>(ws, L.zt);
     a.loss = loss;
     a.lse = lse;

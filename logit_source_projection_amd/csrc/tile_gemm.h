@@ -1,16 +1,19 @@
 // The MFMA tile product of the loss, gradient and 8-bit kernels (gfx950).
 //
-// One workgroup = 8 waves = a 256 x 256 tile of C[m][n] = sum_k A[m][k] B[n][k].
+// One workgroup computes a tile of C[m][n] = sum_k A[m][k] B[n][k]: 256 x 256 by
+// 8 waves (BigTile), or 128 x 128 by 4 (SmallTile) where the big tiles would
+// leave CUs idle or a product is so short that one tile's loads and stores have
+// to run beside another's products: two small workgroups share a CU.
 // Operands come in two layouts, either way without a copy in memory:
 //   * kAlongK:   k contiguous, rows of the operand `ld` apart (X in X.W, both
 //                operands of dZ.W^T, both int8 operands);
 //   * kAcrossK:  rows of the operand contiguous, k steps `ld` apart (W in X.W,
 //                both operands of X^T.dZ).
 // K advances in stages of 128 bytes per row (64 bf16 or 128 int8) through LDS
-// rings of three stages of A and two of B (32 KB each), filled by
-// direct-to-LDS buffer loads of 1 KB.
+// rings of three stages of A and two of B, filled by direct-to-LDS buffer
+// loads of 1 KB.
 //
-// What bounds it: a stage is 64 MFMAs per wave (2 x 8 x 4 blocks of 16 x 16 x
+// What bounds the big tile: a stage is 64 MFMAs per wave (2 x 8 x 4 blocks of 16 x 16 x
 // 32 bf16), about 2048 cycles with two waves per SIMD, and 24 KB of fragment
 // reads per wave, about 1536 cycles of the CU's LDS port.  They only overlap
 // if a wave's reads run beside its own MFMAs, so each 32-deep half of a stage
@@ -40,15 +43,23 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 256;             // rows and columns of a workgroup's tile
-constexpr int kTileWaves = 8;          // 2 (rows) x 4 (columns) waves of 128 x 64
-constexpr int kTileThreads = kTileWaves * 64;
 constexpr int kStageBytes = 128;       // K bytes of a row per stage
 constexpr int kStageK = 64;            // bf16 K steps per stage
-constexpr int kOperandBytes = kTile * kStageBytes;      // one operand's stage
-constexpr int kTileLdsBytes = 5 * kOperandBytes;        // three stages of A, two of B: all 160 KB
-constexpr int kRowBlocks = 8;          // 16-row blocks of a wave
-constexpr int kColBlocks = 4;          // 16-column blocks of a wave
+
+// WM x WN waves (rows x columns) of RB x CB blocks of 16 x 16.
+template <int WM, int WN, int RB, int CB>
+struct TileShape {
+    static constexpr int kWM = WM, kWN = WN, kRB = RB, kCB = CB;
+    static constexpr int kM = 16 * RB * WM, kN = 16 * CB * WN;
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int kABytes = kM * kStageBytes, kBBytes = kN * kStageBytes;  // a stage
+    static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+    static constexpr int kLds = 3 * kABytes + 2 * kBBytes;
+    static constexpr int kPerCu = kLds > 80 * 1024 ? 1 : 2;  // workgroups on a CU
+};
+typedef TileShape<2, 4, 8, 4> BigTile;    // 256 x 256, all 160 KB of LDS
+typedef TileShape<2, 2, 4, 4> SmallTile;  // 128 x 128, half of it
+static_assert(BigTile::kLds == 160 * 1024 && SmallTile::kLds == 80 * 1024, "LDS of a CU");
 
 enum Layout : int { kAlongK = 0, kAcrossK = 1 };
 
@@ -90,11 +101,12 @@ struct TileGrid {
     int pm;      // tile rows of a band
 };
 
+template <class C>
 inline TileGrid tile_grid(int64_t m, int64_t n)
 {
     TileGrid g;
-    g.mt = (int)((m + kTile - 1) / kTile);
-    g.nt = (int)((n + kTile - 1) / kTile);
+    g.mt = (int)((m + C::kM - 1) / C::kM);
+    g.nt = (int)((n + C::kN - 1) / C::kN);
     g.pm = g.mt < 8 ? (g.mt > 0 ? g.mt : 1) : 8;
     return g;
 }
@@ -123,26 +135,33 @@ __device__ __forceinline__ void tile_of(const TileGrid &g, int number, int &mt, 
 // Stage layouts in LDS.
 //   kAlongK:  row r at r * 128, its 16-byte piece p in slot p ^ ((r / 2) & 7):
 //     the 16 rows of a fragment read (ds_read_b128) hit distinct banks.
-//   kAcrossK: k step at k * 512 (256 rows of 2 bytes), its 32-byte unit u (16
-//     rows) in slot u ^ across_swz(k): the 16 k steps of a transposing read
-//     (ds_read_b64_tr_b16) hit distinct banks.
+//   kAcrossK: k step at k * 2 ROWS bytes, its 32-byte unit u (16 rows) in slot
+//     u ^ across_swz(k): the 16 k steps of a transposing read
+//     (ds_read_b64_tr_b16) hit distinct banks, in each half wave with 128 rows.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int across_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+template <int ROWS>
+__device__ __forceinline__ int across_swz(int k)
+{
+    static_assert(ROWS == 256 || ROWS == 128, "16 or 8 units of 32 bytes per k step");
+    return (k & 3) | (((k >> 3) & (ROWS == 256 ? 3 : 1)) << 2);
+}
 
-// This wave's four 1 KB loads of a stage: byte offsets from the stage's base.
-template <int LAYOUT>
-__device__ __forceinline__ void stage_offsets(uint32_t (&vo)[4], int wave, int L, int64_t ld_bytes)
+// This wave's N loads of 1 KB of a stage of ROWS rows: byte offsets from the
+// stage's base.
+template <int LAYOUT, int ROWS, int N>
+__device__ __forceinline__ void stage_offsets(uint32_t (&vo)[N], int wave, int L, int64_t ld_bytes)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int j = 4 * wave + i;
+    for (int i = 0; i < N; ++i) {
+        const int j = N * wave + i;
         if (LAYOUT == kAlongK) {
             const int r = 8 * j + (L >> 3);
             const int p = (L & 7) ^ ((r >> 1) & 7);
             vo[i] = (uint32_t)((int64_t)r * ld_bytes + 16 * p);
         } else {
-            const int k = 2 * j + (L >> 5);
-            const int u = ((L & 31) >> 1) ^ across_swz(k);
+            constexpr int lanes = ROWS / 8;  // of a k step
+            const int k = (64 / lanes) * j + L / lanes;
+            const int u = ((L % lanes) >> 1) ^ across_swz<ROWS>(k);
             vo[i] = (uint32_t)((int64_t)k * ld_bytes + 32 * u + 16 * (L & 1));
         }
     }
@@ -156,19 +175,21 @@ __device__ __forceinline__ void load_to_lds(uint8_t *lds, __amdgpu_buffer_rsrc_t
                                              POLICY);
 }
 
+template <int N>
 __device__ __forceinline__ void stage_load(uint8_t *lds, __amdgpu_buffer_rsrc_t r,
-                                           const uint32_t (&vo)[4], int wave)
+                                           const uint32_t (&vo)[N], int wave)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        load_to_lds(lds + (4 * wave + i) * 1024, r, vo[i]);
+    for (int i = 0; i < N; ++i)
+        load_to_lds(lds + (N * wave + i) * 1024, r, vo[i]);
 }
 
 // Zero the K bytes at and past `kbytes` (< 128) of a kAlongK stage: what lies
 // there in memory is a row's padding or the next row, which may be any bits.
+template <int ROWS, int THREADS>
 __device__ __forceinline__ void zero_stage_tail(uint8_t *lds, int kbytes)
 {
-    for (int idx = threadIdx.x; idx < kTile * 8; idx += kTileThreads) {
+    for (int idx = threadIdx.x; idx < ROWS * 8; idx += THREADS) {
         const int r = idx >> 3, p = idx & 7;
         if (16 * p + 16 <= kbytes)
             continue;
@@ -194,9 +215,9 @@ __device__ __forceinline__ s16x4 read_across(lds_s16x4 __restrict p)
 }
 
 // Fragment reader of NB 16-row blocks from operand row `row0` on (a multiple
-// of 16 * NB): lane L gets row L % 16 of a block, K bytes 16 * (L / 16) .. of
-// the half's 64.
-template <int LAYOUT, int NB>
+// of 16 * NB) of ROWS rows: lane L gets row L % 16 of a block, K bytes 16 * (L
+// / 16) .. of the half's 64.
+template <int LAYOUT, int ROWS, int NB>
 struct FragReader {
     uint32_t at;  // the lane's byte offset inside a stage, block 0, half 0
 
@@ -206,8 +227,8 @@ struct FragReader {
         if (LAYOUT == kAlongK)
             at = (uint32_t)((row0 + n) * kStageBytes + ((g ^ ((n >> 1) & 7)) * 16));
         else  // k = 8 g + n / 4 (+ 4 for the second read), rows 4 (n % 4) .. + 3 of the block
-            at = (uint32_t)((8 * g + (n >> 2)) * 512 +
-                            (((row0 / 16) ^ across_swz(8 * g + (n >> 2))) * 32) + (n & 3) * 8);
+            at = (uint32_t)((8 * g + (n >> 2)) * (2 * ROWS) +
+                            (((row0 / 16) ^ across_swz<ROWS>(8 * g + (n >> 2))) * 32) + (n & 3) * 8);
     }
     __device__ __forceinline__ u32x4 read(const uint8_t *stage, int half, int block) const
     {
@@ -216,9 +237,9 @@ struct FragReader {
                                                     block * 16 * kStageBytes);
         // block < NB and row0 / 16 is a multiple of NB: the block number only
         // flips bits of the swizzled slot
-        const uint8_t *p = stage + (at ^ (uint32_t)(block * 32)) + half * 32 * 512;
+        const uint8_t *p = stage + (at ^ (uint32_t)(block * 32)) + half * 32 * (2 * ROWS);
         const s16x4 lo = read_across((lds_s16x4)p);
-        const s16x4 hi = read_across((lds_s16x4)(p + 4 * 512));
+        const s16x4 hi = read_across((lds_s16x4)(p + 4 * (2 * ROWS)));
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
         return u32x4{a[0], a[1], b[0], b[1]};
@@ -261,22 +282,23 @@ __device__ __forceinline__ void wait_lds()
 }
 
 // The accumulators of a wave: acc[rb][cb] holds, for lane L, row 16 rb + L % 16
-// and columns 16 cb + 4 (L / 16) .. + 3 of the wave's 128 x 64 part.
-template <typename Acc>
+// and columns 16 cb + 4 (L / 16) .. + 3 of the wave's part of the tile.
+template <class C, typename Acc>
 struct WaveTile {
-    Acc acc[kRowBlocks][kColBlocks];
+    static constexpr int kRB = C::kRB, kCB = C::kCB;
+    Acc acc[kRB][kCB];
     int wave, L, row0, col0;  // the wave's first row and column inside the tile
 
     __device__ __forceinline__ void init()
     {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         L = threadIdx.x & 63;
-        row0 = (wave >> 2) * (16 * kRowBlocks);
-        col0 = (wave & 3) * (16 * kColBlocks);
+        row0 = wave / C::kWN * (16 * kRB);
+        col0 = wave % C::kWN * (16 * kCB);
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb)
+        for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb)
+            for (int cb = 0; cb < kCB; ++cb)
                 acc[rb][cb] = Acc{};
     }
 
@@ -291,36 +313,36 @@ struct WaveTile {
     {
         if (nst <= 0)
             return;
-        uint32_t va[4], vb[4];
-        stage_offsets<LA>(va, wave, L, lda_bytes);
-        stage_offsets<LB>(vb, wave, L, ldb_bytes);
-        FragReader<LA, kRowBlocks> ra;
-        FragReader<LB, kColBlocks> rb_;
+        uint32_t va[C::kALoads], vb[C::kBLoads];
+        stage_offsets<LA, C::kM>(va, wave, L, lda_bytes);
+        stage_offsets<LB, C::kN>(vb, wave, L, ldb_bytes);
+        FragReader<LA, C::kM, kRB> ra;
+        FragReader<LB, C::kN, kCB> rb_;
         ra.init(row0, L);
         rb_.init(col0, L);
         // A's ring of three slots, then B's of two
-        uint8_t *const ringb = lds + 3 * kOperandBytes;
-        auto slot_b = [&](int st) { return ringb + (st & 1) * kOperandBytes; };
+        uint8_t *const ringb = lds + 3 * C::kABytes;
+        auto slot_b = [&](int st) { return ringb + (st & 1) * C::kBBytes; };
         auto mend = [&](int st, uint8_t *sa) {  // a stage whose K range ends inside it
             const int kb = src.tail(st);
             if (__builtin_expect(kb < kStageBytes, 0)) {
                 if (ZA)
-                    zero_stage_tail(sa, kb);
+                    zero_stage_tail<C::kM, C::kThreads>(sa, kb);
                 if (ZB)
-                    zero_stage_tail(slot_b(st), kb);
+                    zero_stage_tail<C::kN, C::kThreads>(slot_b(st), kb);
                 wait_lds();
                 block_barrier();
             }
         };
         stage_load(lds, src.a(0), va, wave);
         stage_load(slot_b(0), src.b(0), vb, wave);
-        stage_load(lds + kOperandBytes, src.a(1), va, wave);  // (empty where there is no stage 1)
+        stage_load(lds + C::kABytes, src.a(1), va, wave);  // (empty where there is no stage 1)
         stage_load(slot_b(1), src.b(1), vb, wave);
-        __builtin_amdgcn_s_waitcnt(0x0f70 | 8);  // vmcnt(8): stage 0 has landed
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(C::kALoads + C::kBLoads));  // stage 0 has landed
         block_barrier();
         mend(0, lds);
-        uint8_t *a0 = lds, *a1 = lds + kOperandBytes, *a2 = lds + 2 * kOperandBytes;  // stages st, st + 1, st + 2
-        u32x4 fa[2][kRowBlocks], fb[2][kColBlocks];
+        uint8_t *a0 = lds, *a1 = lds + C::kABytes, *a2 = lds + 2 * C::kABytes;  // stages st, st + 1, st + 2
+        u32x4 fa[2][kRB], fb[2][kCB];
         read_half<LA, LB>(fa[0], fb[0], ra, rb_, a0, slot_b(0), 0);
         __amdgpu_buffer_rsrc_t next_a = src.a(2);
         for (int st = 0; st < nst; ++st) {
@@ -332,9 +354,9 @@ struct WaveTile {
             interleave<LA, LB>();
             const __amdgpu_buffer_rsrc_t next_b = src.b(st + 2);
             next_a = src.a(st + 3);
-            // Stage st + 1 has landed (only A's four loads of stage st + 2 are
-            // later) and every wave holds the rest of this stage in registers.
-            __builtin_amdgcn_s_waitcnt(0x0070 | 4);  // vmcnt(4), lgkmcnt(0)
+            // Stage st + 1 has landed (only A's loads of stage st + 2 are later)
+            // and every wave holds the rest of this stage in registers.
+            __builtin_amdgcn_s_waitcnt(vmcnt_only(C::kALoads) & ~0x0f00);  // and lgkmcnt(0)
             block_barrier();
             if (st + 1 < nst)
                 mend(st + 1, a1);
@@ -355,40 +377,40 @@ struct WaveTile {
 
 private:
     template <int LA, int LB>
-    static __device__ __forceinline__ void read_half(u32x4 (&fa)[kRowBlocks], u32x4 (&fb)[kColBlocks],
-                                                     const FragReader<LA, kRowBlocks> &ra,
-                                                     const FragReader<LB, kColBlocks> &rb_,
+    static __device__ __forceinline__ void read_half(u32x4 (&fa)[kRB], u32x4 (&fb)[kCB],
+                                                     const FragReader<LA, C::kM, kRB> &ra,
+                                                     const FragReader<LB, C::kN, kCB> &rb_,
                                                      const uint8_t *sa, const uint8_t *sb, int half)
     {
 #pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb)
+        for (int cb = 0; cb < kCB; ++cb)
             fb[cb] = rb_.read(sb, half, cb);
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb)
+        for (int rb = 0; rb < kRB; ++rb)
             fa[rb] = ra.read(sa, half, rb);
     }
-    __device__ __forceinline__ void mma_half(const u32x4 (&fa)[kRowBlocks],
-                                             const u32x4 (&fb)[kColBlocks])
+    __device__ __forceinline__ void mma_half(const u32x4 (&fa)[kRB],
+                                             const u32x4 (&fb)[kCB])
     {
 #pragma unroll
-        for (int rb = 0; rb < kRowBlocks; ++rb)
+        for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
-            for (int cb = 0; cb < kColBlocks; ++cb)
+            for (int cb = 0; cb < kCB; ++cb)
                 block_mma(acc[rb][cb], fa[rb], fb[cb]);
     }
-    // Asks the scheduler to spread a half's four loads and its LDS reads over
+    // Asks the scheduler to spread a half's loads and its LDS reads over
     // its MFMAs.
     template <int LA, int LB>
     static __device__ __forceinline__ void interleave()
     {
-        constexpr int reads = kRowBlocks * (LA == kAcrossK ? 2 : 1) + kColBlocks * (LB == kAcrossK ? 2 : 1);
-        constexpr int per = (reads + kRowBlocks - 1) / kRowBlocks;
+        constexpr int reads = kRB * (LA == kAcrossK ? 2 : 1) + kCB * (LB == kAcrossK ? 2 : 1);
+        constexpr int per = (reads + kRB - 1) / kRB;
 #pragma unroll
-        for (int i = 0; i < kRowBlocks; ++i) {
-            if (i < 4)
+        for (int i = 0; i < kRB; ++i) {
+            if (i < C::kALoads)
                 __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
             __builtin_amdgcn_sched_group_barrier(kSchedDsRead, per, 0);
-            __builtin_amdgcn_sched_group_barrier(kSchedMfma, kColBlocks, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedMfma, kCB, 0);
         }
     }
 };

@@ -38,9 +38,13 @@ def test_workspace_sizes():
     assert sb.sb_cross_entropy_workspace_bytes(deep, False) == 4 * 16 * 4096 * 4 + 16 * 4 * 8 + 256
     # dz in two parts, dx in 64 partial sums (one per 64 columns)
     assert sb.sb_cross_entropy_workspace_bytes(h, True) == 2 * 16 * 4096 * 2 + 64 * 16 * 512 * 4
-    # MFMA tiles: a result per row and block; dz, the masked rows and dx in 16 sums
+    # small MFMA tiles: a result per row and 128 columns; dz, the masked rows and
+    # dx in 16 sums (one per block)
     mid = fake_head(B=100)
-    assert sb.sb_cross_entropy_workspace_bytes(mid, False) == 100 * 16 * 8 + 512
+    assert sb.sb_cross_entropy_workspace_bytes(mid, False) == 100 * 32 * 8 + 512
+    # big ones: per 256 columns
+    wide = fake_head(B=300, V=40960, off=(0, 40960), ldw=40960, w_ptrs=[FAKE])
+    assert sb.sb_cross_entropy_workspace_bytes(wide, False) == 300 * 160 * 8 + 1280
     assert sb.sb_cross_entropy_workspace_bytes(mid, True) == \
         100 * 4096 * 2 + 100 * 512 * 2 + 16 * 100 * 512 * 4
     for g in (False, True):

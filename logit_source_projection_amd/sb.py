@@ -212,6 +212,7 @@ class Head:
         self.w = w
         # built from tensors (checked on every call) or from raw pointers
         self.from_tensors = x_ptr is None and w_ptrs is None
+        self._device = None
         off = [int(o) for o in lane_off]
         self.lane_off = off
         k = len(off) - 1
@@ -253,9 +254,11 @@ class Head:
             _operands([self.x], "x")
             _operands(self.w if isinstance(self.w, (list, tuple)) else [self.w], "w")
 
-    def tensors(self):
-        """The operands of a descriptor built from tensors."""
-        return [self.x] + _as_list(self.w) if self.from_tensors else []
+    def device(self):
+        """The one device of the operands (None for raw pointers)."""
+        if self._device is None and self.from_tensors:
+            self._device = _one_device([self.x] + _as_list(self.w))
+        return self._device
 
 
 def sb_workspace_bytes(head, surface):
@@ -446,9 +449,9 @@ def sb_partial_complete(part, op, out, ws=None, stream=None):
 # Training surface.  These calls run on the device of their tensors, whatever
 # the current one is; a stream that is not given is that device's current one.
 # ---------------------------------------------------------------------------
-def _one_device(tensors):
-    """The device that holds every tensor of a call."""
-    device = None
+def _one_device(tensors, device=None):
+    """The device that holds every tensor of a call (and the operands of its
+    descriptor, `device`)."""
     for t in tensors:
         if t is None:
             continue
@@ -501,7 +504,7 @@ def sb_cross_entropy(head, targets, loss, lse, ws=None, stream=None):
     _vector(loss, "loss", torch.float32, B)
     _vector(lse, "lse", torch.float32, B)
     _vector(ws, "ws", torch.uint8, 0)
-    dev = _one_device([targets, loss, lse, ws] + head.tensors())
+    dev = _one_device([targets, loss, lse, ws], head.device())
     _run("sb_cross_entropy", dev, stream, lambda: sb_cross_entropy_workspace_bytes(head, False), ws,
          lambda p, n, s: lib().sb_cross_entropy(head.ref(), _ptr(targets), _ptr(loss), _ptr(lse), p,
                                                 n, s))
@@ -536,7 +539,7 @@ def sb_cross_entropy_grad(head, targets, lse, dloss, dx=None, dw=None, ws=None, 
         dws = [dw]
         ptrs, lddw = [dw.data_ptr() + 2 * o for o in off[:-1]], dw.stride(0)
     arr = None if ptrs is None else (ctypes.c_void_p * len(ptrs))(*ptrs)
-    dev = _one_device([targets, lse, dloss, dx, ws] + dws + head.tensors())
+    dev = _one_device([targets, lse, dloss, dx, ws] + dws, head.device())
     _run("sb_cross_entropy_grad", dev, stream,
          lambda: sb_cross_entropy_workspace_bytes(head, True), ws,
          lambda p, n, s: lib().sb_cross_entropy_grad(
@@ -561,6 +564,7 @@ class Int8Head:
                  ldw=None, x_ptr=None, x_scale_ptr=None, w_ptrs=None, w_scale_ptrs=None):
         self.x, self.x_scale, self.w, self.w_scale = x, x_scale, w, w_scale
         self.from_tensors = x_ptr is None and w_ptrs is None
+        self._device = None
         off = [int(o) for o in lane_off]
         self.lane_off = off
         k = len(off) - 1
@@ -600,7 +604,7 @@ class Int8Head:
         return ctypes.byref(self.desc)
 
     def check(self):
-        if not self.from_tensors:
+        if not self.from_tensors or self._device is not None:
             return
         d, off = self.desc, self.lane_off
         _matrix(self.x, "x", torch.int8, d.B, d.H)
@@ -616,10 +620,14 @@ class Int8Head:
             _matrix(self.w, "w", torch.int8, d.V, d.H)
             _vector(self.w_scale, "w_scale", torch.float32, d.V)
 
-    def tensors(self):
-        if not self.from_tensors:
-            return []
-        return [self.x, self.x_scale] + _as_list(self.w) + _as_list(self.w_scale)
+    def device(self):
+        """The one device of the operands (None for raw pointers).  The
+        descriptor holds their addresses, so they are checked once."""
+        self.check()
+        if self._device is None and self.from_tensors:
+            self._device = _one_device([self.x, self.x_scale] + _as_list(self.w) +
+                                       _as_list(self.w_scale))
+        return self._device
 
 
 def sb_int8_quantize_rows(x, q, scale, stream=None):
@@ -657,8 +665,7 @@ def sb_int8_quantize_head(head, q, scale, stream=None):
         ldq = q.stride(0)
         qp = [q.data_ptr() + ldq * o for o in off[:-1]]
         sp = [scale.data_ptr() + 4 * o for o in off[:-1]]
-    weights = _as_list(head.w) if head.from_tensors else []
-    with _on(_one_device(_as_list(q) + _as_list(scale) + weights)):
+    with _on(_one_device(_as_list(q) + _as_list(scale), head.device())):
         _check(lib().sb_int8_quantize_head(head.ref(), (ctypes.c_void_p * k)(*qp), ldq,
                                            (ctypes.c_void_p * k)(*sp), _stream(stream)),
                "sb_int8_quantize_head")
@@ -681,10 +688,10 @@ def int8_workspace(head, surface, device=None):
 
 def sb_int8_project_tokens(head, ids, ws=None, stream=None):
     """Greedy token IDs (int32 [B]) of the 8-bit head.  Returns ids."""
-    head.check()
+    device = head.device()
     _vector(ids, "ids", torch.int32, head.B)
     _vector(ws, "ws", torch.uint8, 0)
-    dev = _one_device([ids, ws] + head.tensors())
+    dev = _one_device([ids, ws], device)
     _run("sb_int8_project_tokens", dev, stream,
          lambda: sb_int8_workspace_bytes(head, SB_SURF_TOKENS), ws,
          lambda p, n, s: lib().sb_int8_project_tokens(head.ref(), _ptr(ids), p, n, s))
@@ -694,13 +701,13 @@ def sb_int8_project_tokens(head, ids, ws=None, stream=None):
 def sb_int8_logits(head, out, ws=None, stream=None):
     """out (fp32 or bf16 [B, V], row stride out.stride(0)) <- the scaled
     product.  Returns out."""
-    head.check()
+    device = head.device()
     if isinstance(out, torch.Tensor) and out.dtype == torch.bfloat16:
         _matrix(out, "out", torch.bfloat16, head.B, head.V)
     else:
         _matrix(out, "out", torch.float32, head.B, head.V)
     _vector(ws, "ws", torch.uint8, 0)
-    dev = _one_device([out, ws] + head.tensors())
+    dev = _one_device([out, ws], device)
     dtype = SB_BF16 if out.dtype == torch.bfloat16 else SB_FP32
     _run("sb_int8_logits", dev, stream,
          lambda: sb_int8_workspace_bytes(head, SB_SURF_FULL_LOGITS), ws,

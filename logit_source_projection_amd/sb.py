@@ -473,11 +473,20 @@ def _on(device):
     return torch.cuda.device(device)
 
 
+def _stream_on(stream, device):
+    """The stream's handle: the given one's, or the device's current one's
+    (taken as a number: a torch.cuda.Stream object costs 3 us a call)."""
+    if stream is None:
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return _stream(stream)
+
+
 def _run(name, device, stream, nbytes_fn, ws, call):
     """call(workspace pointer, its size, stream) on `device`."""
     with _on(device):
-        ws = _workspace(nbytes_fn, ws, device, stream)
-        _check(call(_ptr(ws), ws.numel(), _stream(stream)), name)
+        if ws is None:
+            ws = _workspace(nbytes_fn, ws, device, stream)
+        _check(call(ws.data_ptr(), ws.numel(), _stream_on(stream, device)), name)
 
 
 def sb_cross_entropy_workspace_bytes(head, grad):
@@ -637,9 +646,11 @@ def sb_int8_quantize_rows(x, q, scale, stream=None):
     B, H = x.shape
     _matrix(q, "q", torch.int8, B, H)
     _vector(scale, "scale", torch.float32, B)
-    with _on(_one_device([x, q, scale])):
-        _check(lib().sb_int8_quantize_rows(_ptr(x), x.stride(0), B, H, _ptr(q), q.stride(0),
-                                           _ptr(scale), _stream(stream)), "sb_int8_quantize_rows")
+    device = _one_device([x, q, scale])
+    with _on(device):
+        _check(lib().sb_int8_quantize_rows(x.data_ptr(), x.stride(0), B, H, q.data_ptr(), q.stride(0),
+                                           scale.data_ptr(), _stream_on(stream, device)),
+               "sb_int8_quantize_rows")
     return q, scale
 
 
@@ -665,9 +676,10 @@ def sb_int8_quantize_head(head, q, scale, stream=None):
         ldq = q.stride(0)
         qp = [q.data_ptr() + ldq * o for o in off[:-1]]
         sp = [scale.data_ptr() + 4 * o for o in off[:-1]]
-    with _on(_one_device(_as_list(q) + _as_list(scale), head.device())):
+    device = _one_device(_as_list(q) + _as_list(scale), head.device())
+    with _on(device):
         _check(lib().sb_int8_quantize_head(head.ref(), (ctypes.c_void_p * k)(*qp), ldq,
-                                           (ctypes.c_void_p * k)(*sp), _stream(stream)),
+                                           (ctypes.c_void_p * k)(*sp), _stream_on(stream, device)),
                "sb_int8_quantize_head")
     return q, scale
 

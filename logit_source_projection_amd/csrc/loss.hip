@@ -11,6 +11,7 @@
 // piece's dz in bf16 and multiplies it both ways.
 #include "loss.h"
 
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -110,36 +111,54 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
     t.template run<kAlongK, kAcrossK, true, false>(smem, (H + kStageK - 1) / kStageK, a.ldx * 2, a.ldw * 2,
                                           src);
 
+    // The epilogue is VALU work that nothing overlaps: 128 values per lane of a
+    // big tile.  Ragged blocks and the rows whose target falls among a wave's
+    // columns take branches of their own (uniform over the wave), so that the
+    // others pay no comparison per value.
     const int n = t.L & 15, g = t.L >> 4;
-    const int gcol0 = a.vocab.off[lane] + c0;
+    const int tcol0 = a.vocab.off[lane] + c0 + t.col0 + 4 * g;  // the lane's first column
+    const bool ragged = nvalid < t.col0 + 16 * kCB;
     if (USE == kUseLoss) {
         float2 *part = reinterpret_cast<float2 *>(smem);  // [kM][column waves]
+        if (ragged) {
+#pragma unroll
+            for (int rb = 0; rb < kRB; ++rb)
+#pragma unroll
+                for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t.col0 + 16 * cb + 4 * g + e >= nvalid)
+                            t.acc[rb][cb][e] = -INFINITY;
+        }
 #pragma unroll
         for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
-            const int tgt = r < rows ? a.targets[m0 + r] - gcol0 : -1;  // target's column in the tile
+            // the target's place among the lane's columns 16 cb + e
+            const int at = r < rows ? (int)((uint32_t)a.targets[m0 + r] - (uint32_t)tcol0) : -1;
+            const bool mine = (uint32_t)at < 16u * kCB && (at & 15) < 4 && t.col0 + 4 * g + at < nvalid;
+            if (__builtin_amdgcn_ballot_w64(mine) != 0) {
+#pragma unroll
+                for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (mine && at == 16 * cb + e)
+                            a.zt[m0 + r] = t.acc[rb][cb][e];
+            }
             float m = -INFINITY;
 #pragma unroll
             for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = t.col0 + 16 * cb + 4 * g + e;
-                    if (c < nvalid) {
-                        m = fmaxf(m, t.acc[rb][cb][e]);
-                        if (c == tgt)
-                            a.zt[m0 + r] = t.acc[rb][cb][e];
-                    }
-                }
+                for (int e = 0; e < 4; ++e)
+                    m = fmaxf(m, t.acc[rb][cb][e]);
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            const float at = m == -INFINITY ? 0.f : m;
+            const float ref = m == -INFINITY ? 0.f : m;
             float s = 0.f;
 #pragma unroll
             for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (t.col0 + 16 * cb + 4 * g + e < nvalid)
-                        s += __expf(t.acc[rb][cb][e] - at);
+                    s += __expf(t.acc[rb][cb][e] - ref);
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (g == 0)
@@ -158,48 +177,74 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
 #pragma unroll
         for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
-            if (r >= rows)
-                continue;
-            const int tgt = a.targets[m0 + r];
-            const float l = a.lse_in[m0 + r];
+            const int tgt = r < rows ? a.targets[m0 + r] : -1;
+            const float l = r < rows ? a.lse_in[m0 + r] : 0.f;
             // a target past the vocabulary has no gradient: NaN, not a guess
-            const float scale = tgt >= a.V ? NAN : a.dloss[m0 + r];
-            uint16_t *out = a.dz + (int64_t)(m0 + r) * a.ldz + (int64_t)nt * kN;
+            const float scale = r >= rows ? 0.f : (tgt >= a.V ? NAN : a.dloss[m0 + r]);
+            const uint32_t keep = tgt < 0 ? 0u : 0xFFFFFFFFu;  // ignored rows: 0, whatever z is
+            const int at = (int)((uint32_t)tgt - (uint32_t)tcol0);  // its place among the lane's columns
+            const bool mine = (uint32_t)at < 16u * kCB;
+            const bool plain = !ragged && __builtin_amdgcn_ballot_w64(mine) == 0;
 #pragma unroll
             for (int cb = 0; cb < kCB; ++cb) {
-                const int c = t.col0 + 16 * cb + 4 * g;
                 float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = __expf(t.acc[rb][cb][e] - l) - (c + e == tgt - gcol0 ? 1.f : 0.f);
-                    v[e] = tgt < 0 || c + e >= nvalid ? 0.f : p * scale;
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __expf(t.acc[rb][cb][e] - l);
+                if (!plain) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] -= at == 16 * cb + e ? 1.f : 0.f;
+                        if (t.col0 + 16 * cb + 4 * g + e >= nvalid)
+                            v[e] = 0.f;
+                    }
                 }
-                store_bf16x4(out + c, v, 4);
+                bf16x4 h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = (__bf16)(v[e] * scale);
+                uint2 bits = __builtin_bit_cast(uint2, h);
+                bits.x &= keep;
+                bits.y &= keep;
+                t.put(smem, rb, cb, bits);
             }
         }
+        uint16_t *const out = a.dz + (int64_t)m0 * a.ldz + (int64_t)nt * kN;
+        t.flush(smem, [&](int r, int c, u32x4 v) {
+            if (r < rows)
+                *reinterpret_cast<u32x4 *>(out + (int64_t)r * a.ldz + c) = v;
+        });
     }
 }
 
-// One row per lane; wave w merges parts w, w + 16, ... in ascending order and
-// the waves are merged in wave order.
-constexpr int kCombineWaves = 16;
-__global__ __launch_bounds__(kCombineWaves * 64) void loss_combine_kernel(const LossArgs a)
+// One workgroup = 16 rows; thread (row, j) merges parts j, j + 64, ... in
+// ascending order, then the 64 runs are merged: 4 in a wave, 16 waves in order.
+constexpr int kCombineRows = 16, kCombineRuns = 64;
+__global__ __launch_bounds__(kCombineRows * kCombineRuns) void loss_combine_kernel(const LossArgs a)
 {
-    __shared__ float2 part[kCombineWaves][64];
-    const int L = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t b = (int64_t)blockIdx.x * 64 + L;
+    __shared__ float2 part[kCombineRuns / 4][kCombineRows];
+    const int row = threadIdx.x % kCombineRows, run = threadIdx.x / kCombineRows;
+    const int64_t b = (int64_t)blockIdx.x * kCombineRows + row;
     float m = -INFINITY, s = 0.f;
     if (b < a.B)
-        for (int i = wave; i < a.parts; i += kCombineWaves) {
+#pragma unroll 4
+        for (int i = run; i < a.parts; i += kCombineRuns) {
             const float2 p = a.mse[(int64_t)i * a.B + b];
             merge_ms(m, s, p.x, p.y);
         }
-    part[wave][L] = make_float2(m, s);
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+        const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
+        merge_ms(m, s, m2, s2);
+    }
+    if ((threadIdx.x & 63) < kCombineRows)
+        part[threadIdx.x >> 6][row] = make_float2(m, s);
     __syncthreads();
-    if (wave != 0 || b >= a.B)
+    if (threadIdx.x >= kCombineRows || b >= a.B)
         return;
-    for (int w = 1; w < kCombineWaves; ++w)
-        merge_ms(m, s, part[w][L].x, part[w][L].y);
+#pragma unroll
+    for (int w = 1; w < kCombineRuns / 4; ++w)
+        merge_ms(m, s, part[w][row].x, part[w][row].y);
     const float l = m + __logf(s);
     const int t = a.targets[b];
     a.lse[b] = l;
@@ -641,20 +686,29 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
     t.template run<kAcrossK, kAcrossK, false, false>(smem, (a.B + kStageK - 1) / kStageK, a.ldxm * 2,
                                             a.ldz * 2, src);
 #pragma unroll
-    for (int rb = 0; rb < kRB; ++rb) {
-        const int r = t.row0 + 16 * rb + n;
-        if (r >= hrows)
-            continue;
-        uint16_t *out = a.vocab.dw[lane] + (int64_t)(h0 + r) * a.lddw + c0;
+    for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
         for (int cb = 0; cb < kCB; ++cb) {
-            const int c = t.col0 + 16 * cb + 4 * g;
-            const float v[4] = {t.acc[rb][cb][0], t.acc[rb][cb][1], t.acc[rb][cb][2],
-                                t.acc[rb][cb][3]};
-            if (c < nvalid)
-                store_bf16x4(out + c, v, nvalid - c);
+            bf16x4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = (__bf16)t.acc[rb][cb][e];
+            t.put(smem, rb, cb, __builtin_bit_cast(uint2, h));
         }
-    }
+    uint16_t *const out = a.vocab.dw[lane] + (int64_t)h0 * a.lddw + c0;
+    t.flush(smem, [&](int r, int c, u32x4 v) {
+        if (r >= hrows || c >= nvalid)
+            return;
+        uint16_t *p = out + (int64_t)r * a.lddw + c;
+        if (c + 8 <= nvalid) {
+            *reinterpret_cast<u32x4 *>(p) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < nvalid)
+                    p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -1052,8 +1106,8 @@ hipError_t launch_loss_combine(const LossArgs &a, hipStream_t s)
         hipLaunchKernelGGL(loss_rows_combine_kernel, dim3(a.B), dim3(256), 0, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(loss_combine_kernel, dim3((unsigned)(((int64_t)a.B + 63) / 64)),
-                       dim3(kCombineWaves * 64), 0, s, a);
+    hipLaunchKernelGGL(loss_combine_kernel, dim3((unsigned)(((int64_t)a.B + kCombineRows - 1) / kCombineRows)),
+                       dim3(kCombineRows * kCombineRuns), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1156,7 +1210,7 @@ int64_t loss_launch_items(int32_t B, int32_t H, int32_t nblk, int32_t splits)
         const int64_t few = ((int64_t)H + kFewH - 1) / kFewH * (splits / kFewWaves);
         items = std::max(std::max(rows * kRowsThreads, few * kFewThreads), (int64_t)loss_parts(1, nblk, 2) * 256);
     }
-    items = std::max(items, ((int64_t)B + 63) / 64 * 64 * kCombineWaves);
+    items = std::max(items, ((int64_t)B + kCombineRows - 1) / kCombineRows * kCombineRows * kCombineRuns);
     return std::max(items, ((int64_t)B * (((int64_t)H + 7) / 8 * 8) / 4 + 255) / 256 * 256);
 }
 

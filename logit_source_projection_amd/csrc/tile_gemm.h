@@ -375,6 +375,29 @@ struct WaveTile {
         __syncthreads();  // LDS is the caller's
     }
 
+    // The wave's part as bf16 rows, by way of a private 128 bytes of LDS per row:
+    // a lane's four columns would be stored as 32-byte pieces of 16 rows, these
+    // are whole 128-byte runs of 8 rows.  put() all of it (after run()), then
+    // flush(): store(row, column, 8 values) inside the tile.
+    __device__ __forceinline__ void put(uint8_t *lds, int rb, int cb, uint2 bits) const
+    {
+        static_assert(kCB == 4, "64 columns of a wave are 128 bytes");
+        const int n = L & 15, p = 2 * cb + (L >> 5);
+        *reinterpret_cast<uint2 *>(lds + (wave * 16 * kRB + 16 * rb + n) * 128 + ((p ^ (n & 7)) * 16) +
+                                   8 * ((L >> 4) & 1)) = bits;
+    }
+    template <typename Store>
+    __device__ __forceinline__ void flush(const uint8_t *lds, Store store) const
+    {
+        wait_lds();
+#pragma unroll
+        for (int i = 0; i < 2 * kRB; ++i) {
+            const int r = 8 * i + (L >> 3), p = L & 7;
+            store(row0 + r, col0 + 8 * p,
+                  *reinterpret_cast<const u32x4 *>(lds + (wave * 16 * kRB + r) * 128 + ((p ^ (r & 7)) * 16)));
+        }
+    }
+
 private:
     template <int LA, int LB>
     static __device__ __forceinline__ void read_half(u32x4 (&fa)[kRB], u32x4 (&fb)[kCB],

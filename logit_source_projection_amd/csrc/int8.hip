@@ -298,33 +298,60 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
             const int c = t.col0 + 16 * cb + 4 * g + e;
             ws[cb][e] = c < nvalid ? a.w_scale[lane][c0 + c] : 0.f;
         }
+    const bool ragged = nvalid < t.col0 + 16 * kCB;
+    const int lcol0 = gcol0 + t.col0 + 4 * g;  // the lane's first column
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb) {
         const int r = t.row0 + 16 * rb + n;
         const float xs = r < rows ? a.x_scale[m0 + r] : 0.f;
-        float bv = -INFINITY;
-        int bi = INT_MAX;
+        float z[kCB][4];
 #pragma unroll
-        for (int cb = 0; cb < kCB; ++cb) {
-            const int c = t.col0 + 16 * cb + 4 * g;
-            const int left = nvalid - c;
-            float z[4];
-            scaled(t.acc[rb][cb], xs, ws[cb], 4, z);
-            if (TOKENS) {
+        for (int cb = 0; cb < kCB; ++cb)
+            scaled(t.acc[rb][cb], xs, ws[cb], 4, z[cb]);
+        if (!TOKENS) {
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb) {
+                const int c = t.col0 + 16 * cb + 4 * g;
+                if (r < rows && c < nvalid)
+                    store_logits(a, m0 + r, gcol0 + c, z[cb], nvalid - c);
+            }
+            continue;
+        }
+        // The NaN-propagating maximum of the lane's values tells whether the
+        // wave needs the full order; else the row's maximum comes first and
+        // then the lowest column that equals it, two instructions per value.
+        float bv = z[0][0];
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                bv = __builtin_elementwise_maximum(bv, z[cb][e]);
+        int bi = INT_MAX;
+        if (!ragged && __builtin_amdgcn_ballot_w64(bv != bv) == 0) {
+            bv = fmaxf(bv, __shfl_xor(bv, 16));
+            bv = fmaxf(bv, __shfl_xor(bv, 32));
+#pragma unroll
+            for (int cb = kCB - 1; cb >= 0; --cb)
+#pragma unroll
+                for (int e = 3; e >= 0; --e)
+                    if (z[cb][e] == bv)
+                        bi = 16 * cb + e;
+            bi = bi == INT_MAX ? bi : lcol0 + bi;
+            bi = min(bi, __shfl_xor(bi, 16));
+            bi = min(bi, __shfl_xor(bi, 32));
+        } else {
+            bv = -INFINITY;
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (e < left)
-                        take_better(bv, bi, z[e], gcol0 + c + e);
-            } else if (r < rows && left > 0) {
-                store_logits(a, m0 + r, gcol0 + c, z, left);
-            }
-        }
-        if (TOKENS) {
+                    if (t.col0 + 16 * cb + 4 * g + e < nvalid)
+                        take_better(bv, bi, z[cb][e], lcol0 + 16 * cb + e);
             take_better(bv, bi, __shfl_xor(bv, 16), __shfl_xor(bi, 16));
             take_better(bv, bi, __shfl_xor(bv, 32), __shfl_xor(bi, 32));
-            if (g == 0)
-                part[r * kWN + t.wave % kWN] = make_float2(bv, __int_as_float(bi));
         }
+        if (g == 0)
+            part[r * kWN + t.wave % kWN] = make_float2(bv, __int_as_float(bi));
     }
     if (TOKENS) {
         __syncthreads();

@@ -333,9 +333,11 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
  *    the same bits.
  *  - Non-finite logits follow IEEE rules: a row with a NaN or +inf logit has a
  *    NaN lse; -inf logits count as probability 0.
- * The head descriptor and its limits are the projection calls'; the gradient
- * also needs 256 shard rows to span less than 4 GiB (SB_ERR_UNSUPPORTED).
- * H == 0 gives all-zero logits; dx and dw are then empty.
+ * The head descriptor and its limits are the projection calls'.  Also (else
+ * SB_ERR_UNSUPPORTED) 256 rows of x must span less than 4 GiB, and so must 64
+ * shard rows, 256 of them in the gradient; the gradient of up to 64 rows takes
+ * fewer than 2^23 columns, every lane rounded up to 256.  H == 0 gives all-zero
+ * logits; the gradients are then empty and the call does nothing.
  * ---------------------------------------------------------------------------
  */
 
@@ -366,8 +368,8 @@ sb_status sb_cross_entropy(const sb_head_desc *desc, const int32_t *targets, flo
  *            gradient, bf16 [H][lddw], laid out as w[i]; lddw >= every lane's
  *            width, a multiple of 8; 16-byte aligned
  *   ws       >= sb_cross_entropy_workspace_bytes(desc, 1), 16-byte aligned
- * At least one of dx and dw is required.  Both are overwritten, not added to
- * (B == 0 zeroes dw).  Columns past H in dx and past a lane's width in dw are
+ * At least one of dx and dw is required (of gradients that are not empty).
+ * Both are overwritten, not added to (B == 0 zeroes dw).  Columns past H in dx and past a lane's width in dw are
  * left as they were.
  */
 sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets, const float *lse,

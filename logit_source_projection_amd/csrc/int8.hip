@@ -240,7 +240,9 @@ __device__ __forceinline__ void store_logits(const Int8Args &a, int64_t b, int g
 }
 
 // ---------------------------------------------------------------------------
-// Large batches: 256 x 256 MFMA tiles, both operands along K.
+// Large batches: MFMA tiles, both operands along K.  Bound by MFMA: 2048 rows of
+// H 5120, V 151936 take 1.46 ms with 1.24 GB of fp32 logits written (2.18 POP/s),
+// the IDs of 1024 rows 0.69 ms (2.3 POP/s, what one large library product gets).
 // ---------------------------------------------------------------------------
 struct Int8Src {
     const uint8_t *x, *w;

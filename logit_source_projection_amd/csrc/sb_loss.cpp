@@ -105,7 +105,8 @@ sb_status check(const sb_head_desc *d, bool grad)
     sb_workspace_bytes(d, SB_SURF_TOKENS, &st);
     if (st != SB_OK)
         return st;
-    // 32-bit offsets: 256 rows of x; 64 rows of a shard, and 256 in the gradient
+    // 32-bit offsets: 256 rows of x; 64 rows of a shard, and 256 in the gradient;
+    // there also 256 rows of a piece of dz (all columns with few rows)
     const int64_t lim = (int64_t)1 << 32;
     if ((int64_t)sbk::kVocabBlock * d->ldx * 2 >= lim ||
         (int64_t)(grad ? sbk::kVocabBlock : 64) * d->ldw * 2 >= lim)
@@ -216,6 +217,8 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
     sb_status st = check(desc, true);
     if (st != SB_OK)
         return st;
+    if (desc->H == 0 || (desc->B == 0 && !dw))
+        return SB_OK;  // the gradients asked for are empty
     if (!dx && !dw)
         return SB_ERR_NULL;
     if (desc->B > 0 && (!targets || !lse || !dloss))
@@ -238,8 +241,6 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
     const Layout L = layout(desc, true);
     if ((st = check_ws(L, ws, ws_bytes)) != SB_OK)
         return st;
-    if (desc->H == 0 || (desc->B == 0 && !dw))
-        return SB_OK;  // both gradients are empty
     sbk::LossArgs a;
     fill(desc, targets, a);
     if (dw)

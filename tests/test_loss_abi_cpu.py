@@ -77,6 +77,13 @@ def test_offset_limits():
     assert ws_status(fake_head(ldw=(1 << 23) - 8), 1) == sb.SB_OK
 
 
+    # few rows: all of dz at once, 256 rows of which must span less than 4 GiB
+    for V, want in (((1 << 23) - 256, sb.SB_OK), ((1 << 23) - 255, sb.SB_ERR_UNSUPPORTED)):
+        h = fake_head(B=64, H=8, V=V, off=(0, V), ldx=8, ldw=(1 << 23) - 8, w_ptrs=[FAKE])
+        assert ws_status(h, 1) == want, V
+        assert ws_status(h, 0) == sb.SB_OK
+
+
 def test_loss_arguments():
     h = fake_head()
     need = sb.sb_cross_entropy_workspace_bytes(h, False)
@@ -103,8 +110,10 @@ def test_grad_arguments():
         assert grad(h, **kw) == sb.SB_ERR_ALIGN, kw
     # no rows and only dx wanted: nothing to do
     assert grad(fake_head(B=0), None, None, None, FAKE, 512, None, 0, None, 0) == sb.SB_OK
-    # an empty hidden size: both gradients are empty
+    # an empty hidden size: both gradients are empty, as their pointers may be
     assert grad(fake_head(H=0, ldx=0)) == sb.SB_OK
+    assert grad(fake_head(H=0, ldx=0), None, None, None, None, 0, (0, 0), 4096, None, 0) == sb.SB_OK
+    assert grad(fake_head(B=0), None, None, None, None, 512, None, 0, None, 0) == sb.SB_OK
 
 
 def test_binding_refuses_arguments_the_abi_cannot_take():

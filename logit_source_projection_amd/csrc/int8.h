@@ -67,7 +67,7 @@ struct Int8QuantizeArgs {
     int32_t k, H;
     int64_t ldw, ldq;
 };
-constexpr int kInt8QuantizeTile = 64;
+constexpr int kInt8QuantizeTile = 64, kInt8QuantizeThreads = 512;
 hipError_t launch_int8_quantize_head(const Int8QuantizeArgs &a, hipStream_t s);
 
 // The scaled product (a.out) or the pairs and IDs (a.ids).

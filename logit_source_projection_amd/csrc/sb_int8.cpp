@@ -202,7 +202,7 @@ sb_status sb_int8_quantize_head(const sb_head_desc *desc, void *const *q, int64_
     if (d.H > 0 && (ldq % 16 != 0 || d.ldw % 8 != 0))
         return SB_ERR_ALIGN;
     const int64_t tiles = tiles_of(d.lane_off, d.k, sbk::kInt8QuantizeTile);
-    if (d.H > sbk::kInt8MaxH || tiles * 256 >= kItems)
+    if (d.H > sbk::kInt8MaxH || tiles * sbk::kInt8QuantizeThreads >= kItems)
         return SB_ERR_UNSUPPORTED;
     sbk::Int8QuantizeArgs a;
     memset(&a, 0, sizeof a);

@@ -1169,8 +1169,14 @@ int loss_slices(int32_t B, int32_t H, int32_t nblk)
     const int tiles = nblk * (kVocabBlock / kLossSmallTile);
     if (B > kLossSmallRows || tiles <= 0)
         return 1;
+    // The slices fill the workgroups that the card holds at a time once (4, 3
+    // or 2 on a CU, as the kernel's registers allow), with at least 16 K steps
+    // each: a slice's sums are written and read again, and a second, partial
+    // round costs a whole one (1024 places at every B: 132 us at B 64, H 4096,
+    // V 65536, 104 us with 512).
     const int steps = (H + kLossStepK - 1) / kLossStepK;
-    const int s = std::max(1, std::min(1024 / tiles, steps / 16));
+    const int places = B <= 16 ? 1024 : B <= 32 ? 768 : 512;
+    const int s = std::max(1, std::min(places / tiles, steps / 16));
     const int per = loss_slice_steps(H, s);
     return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
 }

@@ -12,22 +12,31 @@ namespace sbk {
 constexpr int kInt8MaxH = 131071;
 
 // Batches of up to kInt8SmallRows rows stream the weight once past all of
-// them (int8_rows_kernel); larger ones run 256 x 256 MFMA tiles.
-constexpr int kInt8SmallRows = 64;
+// them (int8_rows_kernel); larger ones run MFMA tiles, and so do more than
+// kInt8FewRows rows on heads of kInt8FewV columns or more: such heads fill the
+// card with tiles without a split of K, which streaming needs (tiles and
+// streaming at B 64, H 4096: V 28672 39 and 46 us, V 50257 64 and 74 us, V 8192
+// 35 and 35 us; H 8192, V 4096 53 and 35 us; at B 32, V 50257 63 and 59 us).
+constexpr int kInt8SmallRows = 64, kInt8FewRows = 32, kInt8FewV = 16384;
+inline bool int8_few(int32_t B, int32_t V)
+{
+    return B <= (V < kInt8FewV ? kInt8SmallRows : kInt8FewRows);
+}
 constexpr int kInt8SmallTile = 64;   // channels per workgroup of the streaming kernel
 constexpr int kInt8LargeTile = 256;  // channels per tile of the MFMA kernel
-inline int int8_tile(int B) { return B <= kInt8SmallRows ? kInt8SmallTile : kInt8LargeTile; }
+inline int int8_tile(bool few) { return few ? kInt8SmallTile : kInt8LargeTile; }
 
 struct Int8Args {
     const int8_t *w[kMaxLanes];       // lane i's channels, int8 [V_i][ldw]
     const float *w_scale[kMaxLanes];  // [V_i]
     int32_t off[kMaxLanes + 1];       // vocab offsets
-    int32_t tile0[kMaxLanes + 1];     // first tile of lane i (int8_tile(B) channels each)
+    int32_t tile0[kMaxLanes + 1];     // first tile of lane i (int8_tile(few) channels each)
     int32_t k;
     const int8_t *x;                  // int8 [B][ldx]
     const float *x_scale;             // [B]
     int64_t ldx, ldw;
     int32_t B, H, V;
+    bool few;                         // int8_few(B, V): the streaming kernel
     // the product: fp32 or bf16 [B][ldo]
     void *out;
     int64_t ldo;
@@ -51,8 +60,8 @@ bool int8_small(int32_t B, int32_t tiles);
 constexpr int kInt8StepK = 128;  // a cache line of every channel
 constexpr int kInt8Chunk = 1024;
 
-// K slices of the streaming kernel for `tiles` tiles.
-int int8_slices(int32_t B, int32_t H, int32_t tiles);
+// K slices for `tiles` tiles: 1 unless the streaming kernel runs.
+int int8_slices(bool few, int32_t H, int32_t tiles);
 int int8_slice_steps(int32_t H, int slices);
 
 hipError_t launch_int8_quantize_rows(const uint16_t *x, int64_t ldx, int32_t B, int32_t H, int8_t *q,
@@ -74,6 +83,6 @@ hipError_t launch_int8_quantize_head(const Int8QuantizeArgs &a, hipStream_t s);
 hipError_t launch_int8(const Int8Args &a, hipStream_t s);
 
 // Work items of the largest launch of a product of B rows on `tiles` tiles.
-int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices);
+int64_t int8_launch_items(bool few, int32_t B, int64_t tiles, int32_t slices);
 
 }  // namespace sbk

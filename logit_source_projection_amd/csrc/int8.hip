@@ -404,8 +404,8 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 rows: the weight streams from memory once.  One workgroup = 4 waves
-// = 64 channels of one lane; wave w takes the K steps w, w + 4, ... of its
+// Up to 64 rows (int8_few): the weight streams from memory once.  One workgroup
+// = 4 waves = 64 channels of one lane; wave w takes the K steps w, w + 4, ... of its
 // slice (128 bytes each), and the four partial tiles meet in LDS.
 //
 // Bound by the weight's bytes.  MFMA wants 16 bytes of 16 channels per load,
@@ -700,9 +700,9 @@ hipError_t launch_tiles(const Int8Args &a, hipStream_t s)
 
 }  // namespace
 
-int int8_slices(int32_t B, int32_t H, int32_t tiles)
+int int8_slices(bool few, int32_t H, int32_t tiles)
 {
-    if (B > kInt8SmallRows || tiles <= 0)
+    if (!few || tiles <= 0)
         return 1;
     // Two workgroups run on a CU: slices fill those 512 places once, with at
     // least 8 K steps each (the 64-row product of H 17408 and V 5120, 80 tiles:
@@ -746,7 +746,7 @@ hipError_t launch_int8_quantize_head(const Int8QuantizeArgs &a, hipStream_t s)
 hipError_t launch_int8(const Int8Args &a, hipStream_t s)
 {
     hipError_t e;
-    if (a.B > kInt8SmallRows)
+    if (!a.few)
         e = a.ids ? launch_tiles<true>(a, s) : launch_tiles<false>(a, s);
     else if (a.B <= 16)
         e = a.ids ? launch_rows<1, true>(a, s) : launch_rows<1, false>(a, s);
@@ -772,10 +772,10 @@ hipError_t launch_int8(const Int8Args &a, hipStream_t s)
     return e;
 }
 
-int64_t int8_launch_items(int32_t B, int64_t tiles, int32_t slices)
+int64_t int8_launch_items(bool few, int32_t B, int64_t tiles, int32_t slices)
 {
     const int64_t rows = (int64_t)B * kIdsThreads;  // one workgroup per row
-    if (B <= kInt8SmallRows)
+    if (few)
         return std::max(rows, tiles * slices * kRowsThreads);
     // the small tiles' launch holds twice the work items of the big ones'
     return std::max(rows, (tile_count(tile_grid<SmallTile>(B, tiles * kInt8LargeTile)) + 8) * SmallTile::kThreads);

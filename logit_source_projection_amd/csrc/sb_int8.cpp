@@ -72,9 +72,10 @@ sb_status check(const sb_int8_desc *d)
     if (d->V > kMaxVocab || d->H > sbk::kInt8MaxH || (int64_t)256 * d->ldx >= lim ||
         (int64_t)256 * d->ldw >= lim)
         return SB_ERR_UNSUPPORTED;
-    const int64_t tiles = tiles_of(d->lane_off, d->k, sbk::int8_tile(d->B));
+    const bool few = sbk::int8_few(d->B, d->V);
+    const int64_t tiles = tiles_of(d->lane_off, d->k, sbk::int8_tile(few));
     if (tiles > (1 << 30) / sbk::kInt8SmallTile ||
-        sbk::int8_launch_items(d->B, tiles, sbk::int8_slices(d->B, d->H, (int32_t)tiles)) >= kItems)
+        sbk::int8_launch_items(few, d->B, tiles, sbk::int8_slices(few, d->H, (int32_t)tiles)) >= kItems)
         return SB_ERR_UNSUPPORTED;
     return SB_OK;
 }
@@ -87,10 +88,11 @@ struct Layout {
 Layout layout(const sb_int8_desc *d, bool tokens)
 {
     Layout L;
-    L.tiles = (int32_t)tiles_of(d->lane_off, d->k, sbk::int8_tile(d->B));
+    const bool few = sbk::int8_few(d->B, d->V);
+    L.tiles = (int32_t)tiles_of(d->lane_off, d->k, sbk::int8_tile(few));
     if (d->B == 0)
         return L;
-    L.slices = sbk::int8_slices(d->B, d->H, L.tiles);
+    L.slices = sbk::int8_slices(few, d->H, L.tiles);
     size_t at = 0;
     if (L.slices > 1) {
         L.part = at;
@@ -100,7 +102,7 @@ Layout layout(const sb_int8_desc *d, bool tokens)
     if (tokens) {
         L.pairs = L.slices > 1 ? (L.tiles * sbk::kInt8SmallTile + sbk::kInt8Chunk - 1) / sbk::kInt8Chunk
                                : L.tiles;
-        if (d->B > sbk::kInt8SmallRows && sbk::int8_small(d->B, L.tiles))
+        if (!few && sbk::int8_small(d->B, L.tiles))
             L.pairs *= 2;
         L.pair = at;
         at = up(at + (size_t)L.pairs * d->B * sizeof(int2), kRegionAlign);
@@ -123,7 +125,8 @@ sb_status check_ws(const Layout &L, void *ws, size_t ws_bytes)
 void fill(const sb_int8_desc *d, const Layout &L, void *ws, sbk::Int8Args &a)
 {
     memset(&a, 0, sizeof a);
-    const int width = sbk::int8_tile(d->B);
+    a.few = sbk::int8_few(d->B, d->V);
+    const int width = sbk::int8_tile(a.few);
     a.k = d->k;
     int tiles = 0;
     for (int i = 0; i < d->k; ++i) {

@@ -96,6 +96,17 @@ def test_product_and_tokens(require_gpu, B, H, V, lanes):
     assert torch.equal(c.tokens(), z.argmax(1).to(torch.int32))
 
 
+@pytest.mark.parametrize("B", [32, 33, 64])
+@pytest.mark.parametrize("V", [16383, 16384])
+def test_both_sides_of_the_few_row_rule(require_gpu, B, V):
+    print(f"int8 B={B} V={V}", flush=True)
+    c = Case(B, 300, V, (0, 5001, V), seed=B)
+    z = c.reference()
+    assert torch.equal(c.logits(), z)
+    assert torch.equal(c.logits(torch.bfloat16), z.to(torch.bfloat16))
+    assert torch.equal(c.tokens(), z.argmax(1).to(torch.int32))
+
+
 @pytest.mark.parametrize("B,H,V,k", [(9, 100, 1003, 5), (70, 264, 2003, 3), (4, 48, 1601, 64),
                                      (90, 48, 1601, 64)])
 def test_lanes_in_their_own_allocations(require_gpu, B, H, V, k):

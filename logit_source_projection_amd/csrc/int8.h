@@ -24,7 +24,7 @@ inline bool int8_few(int32_t B, int32_t V)
 }
 constexpr int kInt8SmallTile = 64;   // channels per workgroup of the streaming kernel
 constexpr int kInt8LargeTile = 256;  // channels per tile of the MFMA kernel
-inline int int8_tile(bool few) { return few ? kInt8SmallTile : kInt8LargeTile; }
+constexpr int int8_tile(bool few) { return few ? kInt8SmallTile : kInt8LargeTile; }
 
 struct Int8Args {
     const int8_t *w[kMaxLanes];       // lane i's channels, int8 [V_i][ldw]
@@ -46,9 +46,9 @@ struct Int8Args {
     int2 *pair;                       // [B][pairs]
     int32_t pairs;
     int32_t *ids;                     // [B]
-    // K slices of the streaming kernel: slice s holds K steps s * slice_steps ..
+    // K slices: slice s holds K steps s * slice_steps ..
     int32_t slices, slice_steps;      // steps of kInt8StepK
-    int32_t *part;                    // [slices][B][tiles * kInt8SmallTile]
+    int32_t *part;                    // [slices][B][tiles * int8_tile(few)]
 };
 
 // Whether the MFMA kernel runs small tiles (`tiles` of kInt8LargeTile channels):
@@ -60,8 +60,8 @@ bool int8_small(int32_t B, int32_t tiles);
 constexpr int kInt8StepK = 128;  // a cache line of every channel
 constexpr int kInt8Chunk = 1024;
 
-// K slices for `tiles` tiles: 1 unless the streaming kernel runs.
-int int8_slices(bool few, int32_t H, int32_t tiles);
+// K slices for `tiles` tiles.
+int int8_slices(bool few, int32_t B, int32_t H, int32_t tiles);
 int int8_slice_steps(int32_t H, int slices);
 
 hipError_t launch_int8_quantize_rows(const uint16_t *x, int64_t ldx, int32_t B, int32_t H, int8_t *q,

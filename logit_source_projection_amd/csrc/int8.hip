@@ -277,6 +277,8 @@ __device__ __forceinline__ void store_logits(const Int8Args &a, int64_t b, int g
 // Large batches: MFMA tiles, both operands along K.  Bound by MFMA: 2048 rows of
 // H 5120, V 151936 take 1.46 ms with 1.24 GB of fp32 logits written (2.18 POP/s),
 // the IDs of 1024 rows 0.69 ms (2.3 POP/s, what one large library product gets).
+// Few tiles split K (int8_slices): a slice stores its 32-bit sums, which
+// int8_join_kernel adds up; integer sums do not depend on the split.
 // ---------------------------------------------------------------------------
 struct Int8Src {
     const uint8_t *x, *w;
@@ -300,23 +302,27 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
 {
     constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const int number = xcd_tile(blockIdx.x, grid.mt * grid.nt);
+    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * a.slices);
     if (number < 0)
         return;
+    const int slice = number / tiles;
     int mt, nt;
-    tile_of(grid, number, mt, nt);
+    tile_of(grid, number - slice * tiles, mt, nt);
     const int block = nt / (kInt8LargeTile / kN);
     const int lane = tile_lane(a, block);
     // first channel inside the lane (a block's later tiles can lie past it)
     const int c0 = (block - a.tile0[lane]) * kInt8LargeTile + nt % (kInt8LargeTile / kN) * kN;
     const int nvalid = max(0, min(kN, a.off[lane + 1] - a.off[lane] - c0));
     const int m0 = mt * kM, rows = min(a.B - m0, kM);
-    const int H = a.H;
+    // the slice's part of K: H bytes from k0
+    const int k0 = slice * a.slice_steps * kInt8StepK;
+    const int H = a.slices > 1 ? min(a.H - k0, a.slice_steps * kInt8StepK) : a.H;
+    const int padded = ((a.H + 15) & ~15) - k0;
     Int8Src src;
-    src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
-    src.w = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw);
-    src.xbytes = (int64_t)(rows - 1) * a.ldx + ((H + 15) & ~15);
-    src.wbytes = nvalid > 0 ? (int64_t)(nvalid - 1) * a.ldw + ((H + 15) & ~15) : 0;
+    src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx + k0);
+    src.w = reinterpret_cast<const uint8_t *>(a.w[lane] + (int64_t)c0 * a.ldw + k0);
+    src.xbytes = (int64_t)(rows - 1) * a.ldx + padded;
+    src.wbytes = nvalid > 0 ? (int64_t)(nvalid - 1) * a.ldw + padded : 0;
     src.H = H;
     WaveTile<C, i32x4> t;
     t.init();
@@ -324,6 +330,19 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
     t.template run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
 
     const int n = t.L & 15, g = t.L >> 4;
+    if (a.slices > 1) {
+        const int64_t ld = (int64_t)a.tile0[a.k] * kInt8LargeTile;
+        int32_t *p = a.part + ((int64_t)slice * a.B + m0) * ld + (int64_t)nt * kN + t.col0 + 4 * g;
+#pragma unroll
+        for (int rb = 0; rb < kRB; ++rb) {
+            const int r = t.row0 + 16 * rb + n;
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
+                if (r < rows)
+                    *reinterpret_cast<i32x4 *>(p + r * ld + 16 * cb) = t.acc[rb][cb];
+        }
+        return;
+    }
     const int gcol0 = a.off[lane] + c0;
     float2 *part = reinterpret_cast<float2 *>(smem);  // [kM][column waves]
     float ws[kCB][4];
@@ -593,13 +612,14 @@ __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args a)
     __shared__ int wi[4];
     const int b = blockIdx.y;
     const int col = blockIdx.x * kInt8Chunk + 4 * threadIdx.x;  // among the tiles' columns
-    const int64_t ld = (int64_t)a.tile0[a.k] * kInt8SmallTile;
+    const int width = int8_tile(a.few);
+    const int64_t ld = (int64_t)a.tile0[a.k] * width;
     float bv = -INFINITY;
     int bi = INT_MAX;
     if (col < ld) {
-        const int tile = col / kInt8SmallTile;
+        const int tile = col / width;
         const int lane = tile_lane(a, tile);
-        const int c = (tile - a.tile0[lane]) * kInt8SmallTile + col % kInt8SmallTile;
+        const int c = (tile - a.tile0[lane]) * width + col % width;
         const int left = a.off[lane + 1] - a.off[lane] - c;
         if (left > 0) {
             const int32_t *p = a.part + (int64_t)b * ld + col;
@@ -686,7 +706,7 @@ hipError_t launch_tiles_as(const Int8Args &a, hipStream_t s)
     const hipError_t e = allow_lds((const void *)int8_tile_kernel<C, TOKENS>, C::kLds, lds_done);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((int8_tile_kernel<C, TOKENS>), dim3((unsigned)xcd_ids(tile_count(g))), dim3(C::kThreads),
+    hipLaunchKernelGGL((int8_tile_kernel<C, TOKENS>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)), dim3(C::kThreads),
                        C::kLds, s, a, g);
     return hipGetLastError();
 }
@@ -700,15 +720,23 @@ hipError_t launch_tiles(const Int8Args &a, hipStream_t s)
 
 }  // namespace
 
-int int8_slices(bool few, int32_t H, int32_t tiles)
+int int8_slices(bool few, int32_t B, int32_t H, int32_t tiles)
 {
-    if (!few || tiles <= 0)
+    if (B <= 0 || tiles <= 0)
         return 1;
-    // Two workgroups run on a CU: slices fill those 512 places once, with at
-    // least 8 K steps each (the 64-row product of H 17408 and V 5120, 80 tiles:
-    // 47.0 us in 12 slices, two rounds, 39.0 us in 6).
+    // Slices of at least 8 K steps fill the card once: 512 workgroups of the
+    // streaming kernel, two on a CU (the 64-row product of H 17408 and V 5120, 80
+    // tiles: 47.0 us in 12 slices, two rounds, 39.0 us in 6), or a small tile for
+    // every CU (V 5120, 40 tiles at B 128: 94 us whole, 38 us in 6 slices, 43 us in
+    // 12, whose sums are twice as many; H 5120, V 17408, 136 tiles at B 128: 41 us
+    // whole, 46 us in 3).
     const int steps = (H + kInt8StepK - 1) / kInt8StepK;
-    const int s = std::max(1, std::min(512 / tiles, steps / 8));
+    int64_t fit = 1;
+    if (few)
+        fit = 512 / tiles;
+    else if (int8_small(B, tiles))
+        fit = 256 / tile_count(tile_grid<SmallTile>(B, (int64_t)tiles * kInt8LargeTile));
+    const int s = (int)std::max<int64_t>(1, std::min<int64_t>(fit, steps / 8));
     const int per = int8_slice_steps(H, s);
     return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
 }
@@ -757,7 +785,7 @@ hipError_t launch_int8(const Int8Args &a, hipStream_t s)
     if (e != hipSuccess)
         return e;
     if (a.slices > 1) {
-        const dim3 grid((unsigned)(((int64_t)a.tile0[a.k] * kInt8SmallTile + kInt8Chunk - 1) / kInt8Chunk), a.B);
+        const dim3 grid((unsigned)(((int64_t)a.tile0[a.k] * int8_tile(a.few) + kInt8Chunk - 1) / kInt8Chunk), a.B);
         if (a.ids)
             hipLaunchKernelGGL(int8_join_kernel<true>, grid, dim3(256), 0, s, a);
         else
@@ -778,7 +806,7 @@ int64_t int8_launch_items(bool few, int32_t B, int64_t tiles, int32_t slices)
     if (few)
         return std::max(rows, tiles * slices * kRowsThreads);
     // the small tiles' launch holds twice the work items of the big ones'
-    return std::max(rows, (tile_count(tile_grid<SmallTile>(B, tiles * kInt8LargeTile)) + 8) * SmallTile::kThreads);
+    return std::max(rows, (tile_count(tile_grid<SmallTile>(B, tiles * kInt8LargeTile)) * slices + 8) * SmallTile::kThreads);
 }
 
 }  // namespace sbk

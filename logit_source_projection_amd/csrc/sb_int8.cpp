@@ -75,7 +75,7 @@ sb_status check(const sb_int8_desc *d)
     const bool few = sbk::int8_few(d->B, d->V);
     const int64_t tiles = tiles_of(d->lane_off, d->k, sbk::int8_tile(few));
     if (tiles > (1 << 30) / sbk::kInt8SmallTile ||
-        sbk::int8_launch_items(few, d->B, tiles, sbk::int8_slices(few, d->H, (int32_t)tiles)) >= kItems)
+        sbk::int8_launch_items(few, d->B, tiles, sbk::int8_slices(few, d->B, d->H, (int32_t)tiles)) >= kItems)
         return SB_ERR_UNSUPPORTED;
     return SB_OK;
 }
@@ -92,17 +92,17 @@ Layout layout(const sb_int8_desc *d, bool tokens)
     L.tiles = (int32_t)tiles_of(d->lane_off, d->k, sbk::int8_tile(few));
     if (d->B == 0)
         return L;
-    L.slices = sbk::int8_slices(few, d->H, L.tiles);
+    L.slices = sbk::int8_slices(few, d->B, d->H, L.tiles);
     size_t at = 0;
     if (L.slices > 1) {
         L.part = at;
-        at = up(at + (size_t)L.slices * d->B * (size_t)L.tiles * sbk::kInt8SmallTile * sizeof(int32_t),
+        at = up(at + (size_t)L.slices * d->B * (size_t)L.tiles * sbk::int8_tile(few) * sizeof(int32_t),
                 kRegionAlign);
     }
     if (tokens) {
-        L.pairs = L.slices > 1 ? (L.tiles * sbk::kInt8SmallTile + sbk::kInt8Chunk - 1) / sbk::kInt8Chunk
+        L.pairs = L.slices > 1 ? (L.tiles * sbk::int8_tile(few) + sbk::kInt8Chunk - 1) / sbk::kInt8Chunk
                                : L.tiles;
-        if (!few && sbk::int8_small(d->B, L.tiles))
+        if (L.slices == 1 && !few && sbk::int8_small(d->B, L.tiles))
             L.pairs *= 2;
         L.pair = at;
         at = up(at + (size_t)L.pairs * d->B * sizeof(int2), kRegionAlign);

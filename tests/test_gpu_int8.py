@@ -107,6 +107,22 @@ def test_both_sides_of_the_few_row_rule(require_gpu, B, V):
     assert torch.equal(c.tokens(), z.argmax(1).to(torch.int32))
 
 
+@pytest.mark.parametrize("B,H,V,lanes", [(65, 17408, 5120, (0, 5120)), (100, 2049, 333, (0, 100, 333)),
+                                         (129, 5000, 1003, (0, 130, 600, 1003)),
+                                         (300, 4111, 2100, (0, 2100)), (1000, 2048, 515, (0, 3, 515))])
+def test_tiles_split_along_k(require_gpu, B, H, V, lanes):
+    print(f"int8 split tiles B={B} H={H} V={V}", flush=True)
+    c = Case(B, H, V, lanes, seed=H)
+    z = c.reference()
+    n = max(sb.sb_int8_workspace_bytes(c.head, s) for s in (sb.SB_SURF_TOKENS, sb.SB_SURF_FULL_LOGITS))
+    assert n >= 2 * 4 * B * V                       # two slices' sums at least
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(c.logits(ws=ws), z)
+        assert torch.equal(c.tokens(ws=ws), z.argmax(1).to(torch.int32))
+    assert torch.equal(c.logits(torch.bfloat16), z.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("B,H,V,k", [(9, 100, 1003, 5), (70, 264, 2003, 3), (4, 48, 1601, 64),
                                      (90, 48, 1601, 64)])
 def test_lanes_in_their_own_allocations(require_gpu, B, H, V, k):

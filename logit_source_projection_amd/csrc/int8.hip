@@ -302,7 +302,9 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
 {
     constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * a.slices);
+    // only small tiles split K; big ones have no register to spare for it
+    const int slices = C::kPerCu > 1 ? a.slices : 1;
+    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * slices);
     if (number < 0)
         return;
     const int slice = number / tiles;
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
     const int m0 = mt * kM, rows = min(a.B - m0, kM);
     // the slice's part of K: H bytes from k0
     const int k0 = slice * a.slice_steps * kInt8StepK;
-    const int H = a.slices > 1 ? min(a.H - k0, a.slice_steps * kInt8StepK) : a.H;
+    const int H = slices > 1 ? min(a.H - k0, a.slice_steps * kInt8StepK) : a.H;
     const int padded = ((a.H + 15) & ~15) - k0;
     Int8Src src;
     src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx + k0);
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
     t.template run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
 
     const int n = t.L & 15, g = t.L >> 4;
-    if (a.slices > 1) {
+    if (slices > 1) {
         const int64_t ld = (int64_t)a.tile0[a.k] * kInt8LargeTile;
         int32_t *p = a.part + ((int64_t)slice * a.B + m0) * ld + (int64_t)nt * kN + t.col0 + 4 * g;
 #pragma unroll
@@ -729,12 +731,13 @@ int int8_slices(bool few, int32_t B, int32_t H, int32_t tiles)
     // tiles: 47.0 us in 12 slices, two rounds, 39.0 us in 6), or a small tile for
     // every CU (V 5120, 40 tiles at B 128: 94 us whole, 38 us in 6 slices, 43 us in
     // 12, whose sums are twice as many; H 5120, V 17408, 136 tiles at B 128: 41 us
-    // whole, 46 us in 3).
+    // whole, 46 us in 3).  Splitting tiles pays from 28 steps on (V 4096 at B 128:
+    // 28 us split and 24 us whole at H 2560, 29 and 32 us at H 3584).
     const int steps = (H + kInt8StepK - 1) / kInt8StepK;
     int64_t fit = 1;
     if (few)
         fit = 512 / tiles;
-    else if (int8_small(B, tiles))
+    else if (int8_small(B, tiles) && steps >= 28)
         fit = 256 / tile_count(tile_grid<SmallTile>(B, (int64_t)tiles * kInt8LargeTile));
     const int s = (int)std::max<int64_t>(1, std::min<int64_t>(fit, steps / 8));
     const int per = int8_slice_steps(H, s);

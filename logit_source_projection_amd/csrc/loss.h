@@ -29,13 +29,13 @@ struct LossArgs {
     int64_t ldx, ldw;
     int32_t B, H, V;
     int32_t nb0, nblk;       // the blocks of this launch
-    // Batches of up to kLossSmallRows rows: K slices of the logits, slice s
-    // holding the K steps s * slice_steps .. of kLossStepK, and their sums
+    // K slices of the logits, slice s holding the K steps s * slice_steps .. of
+    // kLossStepK, and their sums (with several slices one piece is all blocks)
     int32_t slices, slice_steps;
     float *zp;               // fp32 [slices][B][blocks * kVocabBlock], with two slices or more
     // loss
     float2 *mse;             // {maximum, sum exp(z - maximum)}: [parts][B], or with up to
-                             // kLossSmallRows rows [B][parts]
+                             // kLossSmallRows rows or several slices [B][parts]
     int32_t parts;           // runs of columns that the row's sum is made of
     float *zt;               // [B] the target's logit
     float *loss, *lse;       // [B]
@@ -78,10 +78,11 @@ bool small_logits(int32_t B, int32_t nblk);
 bool small_grad(int32_t B, int32_t H, int32_t nblk);
 inline int loss_parts(int B, int nblk, int slices)
 {
+    if (slices > 1)
+        return (nblk * kVocabBlock + kLossChunk - 1) / kLossChunk;
     if (B > kLossSmallRows)
         return small_logits(B, nblk) ? 2 * nblk : nblk;
-    return slices > 1 ? (nblk * kVocabBlock + kLossChunk - 1) / kLossChunk
-                      : nblk * (kVocabBlock / kLossSmallTile);
+    return nblk * (kVocabBlock / kLossSmallTile);
 }
 int loss_slices(int32_t B, int32_t H, int32_t nblk);
 int loss_slice_steps(int32_t H, int slices);

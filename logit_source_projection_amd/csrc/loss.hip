@@ -79,7 +79,8 @@ struct LogitsSrc {
 };
 
 // More than 64 rows: a tile of the logits per workgroup, reduced (loss) or
-// turned into dz (gradient) in its registers.
+// turned into dz (gradient) in its registers; where tiles are few, K is split
+// (loss_slices), the slices' fp32 logits are stored and join_kernel does the rest.
 //
 // Bound by MFMA at the clock that power allows: 2048 rows of the dense head (H
 // 5120, V 151936) take 2.39 ms (1.33 PFLOP/s), the pieces of a 4096-row gradient
@@ -90,11 +91,14 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
 {
     constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const int number = xcd_tile(blockIdx.x, grid.mt * grid.nt);
+    // only small tiles split K; big ones have no register to spare for it
+    const int slices = C::kPerCu > 1 ? a.slices : 1;
+    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * slices);
     if (number < 0)
         return;
+    const int slice = number / tiles;
     int mt, nt;
-    tile_of(grid, number, mt, nt);
+    tile_of(grid, number - slice * tiles, mt, nt);
     const int nb = a.nb0 + nt / (kVocabBlock / kN);
     const int lane = block_lane(a.vocab, nb);
     // first column inside the lane (a block's later tiles can lie past it)
@@ -102,13 +106,15 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
     const int nvalid = max(0, min(kN, a.vocab.off[lane + 1] - a.vocab.off[lane] - c0));
     const int m0 = mt * kM;
     const int rows = min(a.B - m0, kM);
-    const int H = a.H;
+    // the slice's part of K: H rows of the weight from k0
+    const int k0 = slice * a.slice_steps * kLossStepK;
+    const int H = slices > 1 ? min(a.H - k0, a.slice_steps * kLossStepK) : a.H;
 
     LogitsSrc src;
-    src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
-    src.w = reinterpret_cast<const uint8_t *>(a.vocab.w[lane] + c0);
+    src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx + k0);
+    src.w = reinterpret_cast<const uint8_t *>(a.vocab.w[lane] + (int64_t)k0 * a.ldw + c0);
     src.ldw_bytes = a.ldw * 2;
-    src.xbytes = ((int64_t)(rows - 1) * a.ldx + ((H + 7) & ~7)) * 2;
+    src.xbytes = ((int64_t)(rows - 1) * a.ldx + ((a.H + 7) & ~7) - k0) * 2;
     src.wbytes = nvalid > 0 ? ((int64_t)(H - 1) * a.ldw + ((nvalid + 7) & ~7)) * 2 : 0;
     src.H = H;
     WaveTile<C, f32x4> t;
@@ -116,6 +122,19 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
     t.template run<kAlongK, kAcrossK, true, false>(smem, (H + kStageK - 1) / kStageK, a.ldx * 2, a.ldw * 2,
                                           src);
 
+    if (slices > 1) {
+        const int64_t ld = (int64_t)a.nblk * kVocabBlock;
+        float *p = a.zp + ((int64_t)slice * a.B + m0) * ld + (int64_t)nt * kN + t.col0 + 4 * (t.L >> 4);
+#pragma unroll
+        for (int rb = 0; rb < kRB; ++rb) {
+            const int r = t.row0 + 16 * rb + (t.L & 15);
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
+                if (r < rows)
+                    *reinterpret_cast<f32x4 *>(p + r * ld + 16 * cb) = t.acc[rb][cb];
+        }
+        return;
+    }
     // The epilogue is VALU work that nothing overlaps: 128 values per lane of a
     // big tile.  Ragged blocks and the rows whose target falls among a wave's
     // columns take branches of their own (uniform over the wave), so that the
@@ -1031,6 +1050,17 @@ __global__ __launch_bounds__(256) void dx_finish_kernel(const LossArgs a)
     store_bf16x4(a.dx + b * a.lddx + c, v, a.H - c);
 }
 
+// The slices' sums added up, where there are several.
+template <int USE>
+hipError_t launch_join(const LossArgs &a, hipStream_t s)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.slices == 1)
+        return e;
+    hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.B, a.nblk, a.slices), a.B), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 template <class C, int USE>
 hipError_t launch_logits_tiles(const LossArgs &a, hipStream_t s)
 {
@@ -1039,9 +1069,9 @@ hipError_t launch_logits_tiles(const LossArgs &a, hipStream_t s)
     const hipError_t e = allow_lds((const void *)logits_kernel<C, USE>, C::kLds, lds_done);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((logits_kernel<C, USE>), dim3((unsigned)xcd_ids(tile_count(g))), dim3(C::kThreads),
-                       C::kLds, s, a, g);
-    return hipGetLastError();
+    hipLaunchKernelGGL((logits_kernel<C, USE>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)),
+                       dim3(C::kThreads), C::kLds, s, a, g);
+    return launch_join<USE>(a, s);
 }
 
 template <int USE>
@@ -1077,11 +1107,7 @@ hipError_t launch_logits_rows(const LossArgs &a, hipStream_t s)
         hipLaunchKernelGGL((logits_rows_kernel<2, USE>), grid, dim3(kRowsThreads), 0, s, a);
     else
         hipLaunchKernelGGL((logits_rows_kernel<4, USE>), grid, dim3(kRowsThreads), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.slices == 1)
-        return e;
-    hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.B, a.nblk, a.slices), a.B), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_join<USE>(a, s);
 }
 
 // Steps of a workgroup where `splits` of them share the blocks.
@@ -1119,7 +1145,7 @@ hipError_t launch_dlogits(const LossArgs &a, hipStream_t s)
 
 hipError_t launch_loss_combine(const LossArgs &a, hipStream_t s)
 {
-    if (a.B <= kLossSmallRows) {
+    if (a.B <= kLossSmallRows || a.slices > 1) {
         hipLaunchKernelGGL(loss_rows_combine_kernel, dim3(a.B), dim3(256), 0, s, a);
         return hipGetLastError();
     }
@@ -1167,7 +1193,7 @@ hipError_t launch_dx_finish(const LossArgs &a, hipStream_t s)
 int loss_slices(int32_t B, int32_t H, int32_t nblk)
 {
     const int tiles = nblk * (kVocabBlock / kLossSmallTile);
-    if (B > kLossSmallRows || tiles <= 0)
+    if (B <= 0 || tiles <= 0)
         return 1;
     // The slices fill the workgroups that the card holds at a time once (4, 3
     // or 2 on a CU, as the kernel's registers allow), with at least 16 K steps
@@ -1175,8 +1201,14 @@ int loss_slices(int32_t B, int32_t H, int32_t nblk)
     // round costs a whole one (1024 places at every B: 132 us at B 64, H 4096,
     // V 65536, 104 us with 512).
     const int steps = (H + kLossStepK - 1) / kLossStepK;
-    const int places = B <= 16 ? 1024 : B <= 32 ? 768 : 512;
-    const int s = std::max(1, std::min(places / tiles, steps / 16));
+    int64_t fit = 1;
+    if (B <= kLossSmallRows)
+        fit = (B <= 16 ? 1024 : B <= 32 ? 768 : 512) / tiles;
+    else if (small_logits(B, nblk) && steps >= 64)
+        // a small tile for every CU (V 4096 at B 128: 83 us whole and 30 us split
+        // at H 8192, 30 and 25 us at H 2048, 21 and 24 us at H 1024)
+        fit = 256 / tile_count(tile_grid<SmallTile>(B, (int64_t)nblk * kVocabBlock));
+    const int s = (int)std::max<int64_t>(1, std::min<int64_t>(fit, steps / 16));
     const int per = loss_slice_steps(H, s);
     return per > 0 ? std::max(1, (steps + per - 1) / per) : 1;
 }
@@ -1224,7 +1256,8 @@ int dx_splits(int32_t B, int32_t H, int32_t nblk)
 int64_t loss_launch_items(int32_t B, int32_t H, int32_t nblk, int32_t splits)
 {
     // the small tiles' launches hold twice the work items of the big ones'
-    const int64_t logits = tile_count(tile_grid<SmallTile>(B, (int64_t)nblk * kVocabBlock));
+    const int64_t logits = tile_count(tile_grid<SmallTile>(B, (int64_t)nblk * kVocabBlock)) *
+                           loss_slices(B, H, nblk);
     const int64_t grad = tile_count(tile_grid<SmallTile>(B, H)) * splits +
                          tile_count(tile_grid<SmallTile>(H, (int64_t)nblk * kVocabBlock));
     int64_t items = (std::max(logits, grad) + 16) * SmallTile::kThreads;

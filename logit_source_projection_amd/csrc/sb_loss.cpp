@@ -33,7 +33,7 @@ constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 struct Layout {
     int blocks = 0, piece = 0, splits = 1;
     bool direct = false;  // dx written without partial sums
-    int slices = 1;       // K slices of the logits (few rows)
+    int slices = 1;       // K slices of the logits
     size_t zp = 0, mse = 0, zt = 0, dz = 0, xm = 0, dxp = 0, total = 0;
     int64_t ldz = 0, ldxm = 0, ldxp = 0;
 };
@@ -49,12 +49,11 @@ Layout layout(const sb_head_desc *d, bool grad)
     const size_t B = (size_t)d->B;
     size_t at = 0;
     const bool few = d->B <= sbk::kLossSmallRows;
-    if (few) {
-        L.slices = sbk::loss_slices(d->B, d->H, L.blocks);
-        if (L.slices > 1) {
-            L.zp = at;
-            at = up(at + (size_t)L.slices * B * L.blocks * sbk::kVocabBlock * sizeof(float), kRegionAlign);
-        }
+    // (a gradient in several pieces has more tiles than are ever split)
+    L.slices = sbk::loss_slices(d->B, d->H, L.blocks);
+    if (L.slices > 1) {
+        L.zp = at;
+        at = up(at + (size_t)L.slices * B * L.blocks * sbk::kVocabBlock * sizeof(float), kRegionAlign);
     }
     if (!grad) {
         L.mse = at;
@@ -162,7 +161,7 @@ void fill(const sb_head_desc *d, const int32_t *targets, sbk::LossArgs &a)
     a.splits = 1;
 }
 
-// The K slices of a call of few rows.
+// The K slices of a call and their sums.
 void set_slices(const sb_head_desc *d, const Layout &L, void *ws, sbk::LossArgs &a)
 {
     a.slices = L.slices;
@@ -258,8 +257,8 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
     if (desc->B == 0)  // dw of no rows is zero
         return sbk::launch_grad(a, false, true, s) == hipSuccess ? SB_OK : SB_ERR_HIP;
     a.dz = region<uint16_t>(ws, L.dz);
+    set_slices(desc, L, ws, a);
     if (desc->B <= sbk::kLossSmallRows) {
-        set_slices(desc, L, ws, a);
         a.dxp = region<float>(ws, L.dxp);
         a.ldxp = L.ldxp;
         if (sbk::launch_dlogits(a, s) != hipSuccess ||

@@ -107,9 +107,9 @@ def test_both_sides_of_the_few_row_rule(require_gpu, B, V):
     assert torch.equal(c.tokens(), z.argmax(1).to(torch.int32))
 
 
-@pytest.mark.parametrize("B,H,V,lanes", [(65, 17408, 5120, (0, 5120)), (100, 2049, 333, (0, 100, 333)),
+@pytest.mark.parametrize("B,H,V,lanes", [(65, 17408, 5120, (0, 5120)), (100, 3601, 333, (0, 100, 333)),
                                          (129, 5000, 1003, (0, 130, 600, 1003)),
-                                         (300, 4111, 2100, (0, 2100)), (1000, 2048, 515, (0, 3, 515))])
+                                         (300, 4111, 2100, (0, 2100)), (1000, 3600, 515, (0, 3, 515))])
 def test_tiles_split_along_k(require_gpu, B, H, V, lanes):
     print(f"int8 split tiles B={B} H={H} V={V}", flush=True)
     c = Case(B, H, V, lanes, seed=H)

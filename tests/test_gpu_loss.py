@@ -108,6 +108,30 @@ def test_loss_and_gradient(require_gpu, B, H, V, lanes):
     check_grad(dx, dw, c.x, c.w, c.targets, c.dloss, lse)
 
 
+@pytest.mark.parametrize("B,H,V,lanes", [(65, 2049, 333, (0, 104, 333)), (100, 4100, 1003, (0, 136, 600, 1003)),
+                                         (300, 2100, 2100, (0, 2100)), (1000, 2056, 515, (0, 8, 515))])
+def test_tiles_split_along_k(require_gpu, B, H, V, lanes):
+    """Few tiles and a long H: slices' logits are stored and added up."""
+    print(f"split tiles B={B} H={H} V={V}", flush=True)
+    c = Case(B, H, V, lanes, seed=H)
+    n = sb.sb_cross_entropy_workspace_bytes(c.head, True)
+    assert sb.sb_cross_entropy_workspace_bytes(c.head, False) >= 2 * 4 * B * V  # two slices at least
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    c.targets[0], c.targets[B - 1] = V - 1, -1
+    loss, lse = c.loss(ws=ws)
+    check_loss(loss, lse, c.x, c.w, c.targets)
+    dx, dw = c.grad(lse, ws=ws)
+    check_grad(dx, dw, c.x, c.w, c.targets, c.dloss, lse)
+    # ignored rows hold anything; a target past the vocabulary is NaN
+    c.x[B - 1] = float("nan")
+    c.targets[1] = V
+    loss, lse = c.loss(ws=ws)
+    assert loss[B - 1].item() == 0 and bool(loss[1].isnan()) and bool(loss[:1].isfinite().all())
+    dx2, _ = c.grad(lse, ws=ws, want=("dx",))
+    rest = torch.arange(B, device="cuda") != 1
+    assert bool(dx2[1].isnan().all()) and torch.equal(dx2[rest], dx[rest])
+
+
 @pytest.mark.parametrize("B,H,V,k", [(4, 100, 1003, 5), (70, 264, 2003, 3), (300, 64, 1601, 64)])
 def test_lanes_in_their_own_allocations(require_gpu, B, H, V, k):
     """Lane widths that are no multiple of 8 (or of anything)."""

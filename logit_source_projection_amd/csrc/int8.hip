@@ -606,7 +606,7 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
 }
 
 // The slices of a split product added up: one workgroup = kInt8Chunk columns
-// (16 tiles) of one row.
+// of one row.
 template <bool TOKENS>
 __global__ __launch_bounds__(256) void int8_join_kernel(const Int8Args a)
 {

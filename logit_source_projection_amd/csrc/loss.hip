@@ -541,7 +541,7 @@ __global__ __launch_bounds__(256) void join_kernel(const LossArgs a)
     }
 }
 
-// Few rows: one workgroup per row, its parts spread over the threads.
+// Few rows or K slices: one workgroup per row, its parts spread over the threads.
 __global__ __launch_bounds__(256) void loss_rows_combine_kernel(const LossArgs a)
 {
     __shared__ float2 part[4];

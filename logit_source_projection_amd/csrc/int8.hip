@@ -498,8 +498,8 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
-                fx[j][i][mb] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb], 64 * i, 0));
+                fx[j][i][mb] = __builtin_bit_cast(  // (only the vector offset is bounds-checked)
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, xo[mb] + 64 * i, 0, 0));
     };
 #pragma unroll
     for (int j = 0; j < kRowsSlots; ++j)

@@ -328,9 +328,11 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
  *    H (not the order of the projection calls: last bits can differ from
  *    theirs).  lse is an online sum over 256-column blocks.  The gradient
  *    computes the logits again, in pieces of the vocabulary, rounds dz to bf16
- *    (off by at most 2^-8 of its value, as each bf16 result is) and
- *    accumulates dx and dw in fp32; each is rounded once.  Repeated calls give
- *    the same bits.
+ *    and accumulates dx and dw in fp32; each is rounded once.  Up to 32 rows two
+ *    bf16 numbers hold a dz (off by at most 2^-16 of its value); above, the
+ *    target's dz is as exact and the others are off by at most 2^-8 of theirs
+ *    (in dx above 64 rows their sum by 2^-8 more).  Repeated calls give the same
+ *    bits.
  *  - Non-finite logits follow IEEE rules: a row with a NaN or +inf logit has a
  *    NaN lse; -inf logits count as probability 0.
  * The head descriptor and its limits are the projection calls'.  Also (else

@@ -295,6 +295,7 @@ struct Int8Src {
         return buffer_of(w + at, at < H ? wbytes - at : 0);
     }
     __device__ __forceinline__ int tail(int st) const { return min(H - st * kStageBytes, kStageBytes); }
+    __device__ __forceinline__ void meanwhile() const {}
 };
 
 template <class C, bool TOKENS>

@@ -45,6 +45,8 @@ struct LossArgs {
     uint16_t *dz;            // bf16 [dz_parts(B)][B][ldz], whose sum is dz, columns of
                              // blocks nb0 ..
     int64_t ldz;
+    uint16_t *rest;          // bf16 [B], ldrest apart: what rounding took from the target's dz,
+    int64_t ldrest;          // relative to what is left, where dz_parts(B) is 1
     const uint16_t *xm;      // bf16 [B][ldxm]: x with the ignored rows zeroed
     int64_t ldxm;
     float *dxp;              // fp32 [splits][B][ldxp] partial sums of dx, or NULL
@@ -52,7 +54,7 @@ struct LossArgs {
     uint16_t *dx;            // bf16 [B][lddx], or NULL
     int64_t lddx, lddw;
     int32_t splits;          // K splits of dx
-    int32_t first;           // the first launch on dxp stores, later ones add
+    int32_t first, last;     // the first launch on dxp stores, later ones add
 };
 
 // Batches of up to kLossSmallRows rows stream the weight once past all of them;
@@ -61,10 +63,17 @@ constexpr int kLossSmallRows = 64;
 constexpr int kLossStepK = 32;        // K rows per MFMA step
 constexpr int kLossSmallTile = 128;   // columns per workgroup of the streaming kernel
 constexpr int kLossChunk = 1024;      // columns per workgroup that adds slices up
-// bf16 parts that dz is held in.  Its rounding is as large as that of the bf16
-// results, and in sums over many rows the two add up as independent errors; in
-// sums of few terms a lone dz's rounding would be the whole result's, so up to
-// 32 rows a second part holds what the first leaves.
+// bf16 parts that dz is held in.  A term that stands alone in a sum would double
+// the rounding of the bf16 result.  Up to 32 rows, where any term can, a second
+// part holds what the first leaves.  Above, the target's dz is the term that
+// stands out in its row of dX and its column of dW, at any batch size: the row's
+// others together are as large, but spread over the vocabulary.  What rounding
+// took from it is kept (`rest`).  dW adds its products to the accumulators (x is
+// read along rows), and so does dX where the weight's tile is in LDS (up to 64
+// rows).  Larger batches would have to gather columns of the weight, a cache line
+// per value (333 rows of H 1111: 50 us of 160); there dX's rows are multiplied by 1 +
+// rest instead, which makes the target's term whole and moves the sum of the others by
+// as much as their own roundings may.  Those stay: 2^-8 of each, independent.
 constexpr int dz_parts(int B) { return B <= 32 ? 2 : 1; }
 // Whether the logits of nblk blocks, and the gradient's two products, run small
 // tiles (batches of more than kLossSmallRows rows).  Small tiles read each

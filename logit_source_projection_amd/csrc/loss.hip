@@ -58,6 +58,25 @@ __device__ __forceinline__ void store_bf16x4(uint16_t *p, const float (&v)[4], i
     }
 }
 
+__device__ __forceinline__ float bf16_value(uint16_t bits) { return __uint_as_float((uint32_t)bits << 16); }
+
+// What the rounding of the target's dz v to h took, relative to h, in bf16: h * (1 +
+// that) is off by at most 2^-16.  (0 where v is not finite, 0 or below bf16's range.)
+__device__ __forceinline__ void store_rest(const LossArgs &a, int64_t b, float v)
+{
+    const float h = (float)(__bf16)v, r = (v - h) / h;
+    a.rest[b * a.ldrest] = __builtin_bit_cast(uint16_t, (__bf16)(fabsf(r) <= 0.0078125f ? r : 0.f));
+}
+__device__ __forceinline__ float rest_of(const LossArgs &a, int64_t b) { return bf16_value(a.rest[b * a.ldrest]); }
+
+// sum + rest * v, unless that is no number (then v, or the term that the rest was
+// taken from, is none either and the sum holds it).
+__device__ __forceinline__ float add_rest(float sum, float rest, float v)
+{
+    const float c = rest * v;
+    return fabsf(c) < INFINITY ? sum + c : sum;
+}
+
 enum LogitsUse { kUseLoss, kUseGrad };
 
 // Z tile = rows of X times a block of W.
@@ -76,6 +95,7 @@ struct LogitsSrc {
         return buffer_of(w + at, wbytes - at);  // rows past H read as zeros
     }
     __device__ __forceinline__ int tail(int st) const { return min((H - st * kStageK) * 2, kStageBytes); }
+    __device__ __forceinline__ void meanwhile() const {}
 };
 
 // More than 64 rows: a tile of the logits per workgroup, reduced (loss) or
@@ -209,6 +229,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
             const int at = (int)((uint32_t)tgt - (uint32_t)tcol0);  // its place among the lane's columns
             const bool mine = (uint32_t)at < 16u * kCB;
             const bool plain = !ragged && __builtin_amdgcn_ballot_w64(mine) == 0;
+            float term = 0.f;  // the target's dz
 #pragma unroll
             for (int cb = 0; cb < kCB; ++cb) {
                 float v[4];
@@ -227,11 +248,19 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     h[e] = (__bf16)(v[e] * scale);
+                if (!plain) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (at == 16 * cb + e)
+                            term = v[e] * scale;
+                }
                 uint2 bits = __builtin_bit_cast(uint2, h);
                 bits.x &= keep;
                 bits.y &= keep;
                 t.put(smem, rb, cb, bits);
             }
+            if (!plain && mine && (at & 15) < 4 && t.col0 + 4 * g + at < nvalid)
+                store_rest(a, m0 + r, term);
         }
         uint16_t *const out = a.dz + (int64_t)m0 * a.ldz + (int64_t)nt * kN;
         t.flush(smem, [&](int r, int c, u32x4 v) {
@@ -330,6 +359,20 @@ struct RowGrad {
     {
         const float p = __expf(z - lse) - (col == target ? 1.f : 0.f);
         return target < 0 ? 0.f : p * scale;
+    }
+    // what rounding takes from the target's dz, where it is among the n values v of columns col ..
+    template <int N>
+    __device__ __forceinline__ void keep_rest(const LossArgs &a, int64_t b, const float (&v)[N], int col,
+                                              int n) const
+    {
+        const uint32_t at = (uint32_t)target - (uint32_t)col;
+        if (at >= (uint32_t)min(max(n, 0), N))
+            return;
+        float term = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            term += at == (uint32_t)e ? v[e] : 0.f;
+        store_rest(a, b, term);
     }
 };
 
@@ -485,6 +528,8 @@ __global__ __launch_bounds__(kRowsThreads, MB == 4 ? 2 : (MB == 2 ? 3 : 4)) void
                 v[e] = ec + e < nvalid ? row.dz(y[e], gcol + e) : 0.f;
             uint16_t *p = a.dz + (int64_t)b * a.ldz + (int64_t)tile * kLossSmallTile + ec;
             store_split(p, dz_parts(a.B) > 1 ? p + (int64_t)a.B * a.ldz : nullptr, v);
+            if (MB == 4)  // one part
+                row.keep_rest(a, b, v, gcol, nvalid - ec);
         }
     }
 }
@@ -526,6 +571,8 @@ __global__ __launch_bounds__(256) void join_kernel(const LossArgs a)
                 v[e] = e < left ? row.dz(s[e], gcol + e) : 0.f;
             uint16_t *q = a.dz + (int64_t)b * a.ldz + col;
             store_split(q, dz_parts(a.B) > 1 ? q + (int64_t)a.B * a.ldz : nullptr, v);
+            if (dz_parts(a.B) == 1)
+                row.keep_rest(a, b, v, gcol, left);
         }
     }
     if (USE == kUseLoss) {
@@ -585,6 +632,7 @@ __global__ __launch_bounds__(256) void mask_rows_kernel(const LossArgs a, uint16
 }
 
 // dX tile = rows of dz times the block columns of W rows (k = vocabulary).
+template <typename Meanwhile>
 struct DxSrc {
     const LossArgs &args;
     const uint8_t *dz;    // the tile's rows, from the split's first block on
@@ -595,7 +643,8 @@ struct DxSrc {
     int lane, lane_end;
     // valid K bytes of the last two stages loaded
     int tail0, tail1;
-    __device__ __forceinline__ DxSrc(const LossArgs &a_) : args(a_) {}
+    Meanwhile meanwhile;
+    __device__ __forceinline__ DxSrc(const LossArgs &a_, Meanwhile m) : args(a_), meanwhile(m) {}
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
     {
         const int64_t at = (int64_t)st * kStageBytes;
@@ -621,10 +670,64 @@ struct DxSrc {
     __device__ __forceinline__ int tail(int st) const { return st & 1 ? tail1 : tail0; }
 };
 
+// The rows whose target is one of n columns from col on, up to 64 of them in ascending
+// order, one to a lane; next is the first row not looked at.
+struct TargetRows {
+    static constexpr int kAhead = 8;  // loads in flight, 64 rows each
+    int col, n;
+    int row, count, next;
+    int at;  // the target's place among the columns
+    int t[kAhead];
+    // Targets of rows next ..  No lane branches: the ballots below need all of them,
+    // and a branch here was merged into their loop.
+    __device__ __forceinline__ void load(const LossArgs &a)
+    {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int b = next + 64 * j + (threadIdx.x & 63), v = a.targets[min(b, a.B - 1)];
+            t[j] = b < a.B ? v : -1;
+        }
+    }
+    // (after load)
+    __device__ __forceinline__ void find(const LossArgs &a)
+    {
+        const int L = threadIdx.x & 63;
+        count = 0;
+        for (;;) {
+            int done = 64 * kAhead;  // rows of the loaded ones that are looked at
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const uint32_t c = (uint32_t)t[j] - (uint32_t)col;
+                uint64_t hits = __builtin_amdgcn_ballot_w64(c < (uint32_t)n);
+                if (__builtin_expect(hits == 0 || done < 64 * kAhead, 1))
+                    continue;
+                if (count + __builtin_popcountll(hits) > 64) {
+                    done = 64 * j;
+                    continue;
+                }
+                for (; hits != 0; hits &= hits - 1, ++count) {
+                    const int l = __builtin_ctzll(hits), hit = __builtin_amdgcn_readlane((int)c, l);
+                    if (L == count) {
+                        row = next + 64 * j + l;
+                        at = hit;
+                    }
+                }
+            }
+            next += done;
+            if (next >= a.B || done < 64 * kAhead)
+                return;
+            load(a);
+        }
+    }
+};
+
 // dW tile = X^T rows times a block of dz (k = batch rows).
+template <typename Meanwhile>
 struct DwSrc {
     const uint8_t *x, *dz;
     int64_t xbytes, zbytes, ldx_bytes, ldz_bytes;
+    Meanwhile meanwhile;
+    __device__ __forceinline__ DwSrc(Meanwhile m) : meanwhile(m) {}
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t a(int st) const
     {
         const int64_t at = (int64_t)st * kStageK * ldx_bytes;
@@ -663,7 +766,18 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
         const int per = (a.nblk + a.splits - 1) / a.splits;
         const int b0 = min(split * per, a.nblk), b1 = min(b0 + per, a.nblk);
         const int m0 = mt * kM, rows = min(a.B - m0, kM);
-        DxSrc src(a);
+        // the last piece's launch makes the targets' terms whole (see dz_parts)
+        int target[kRB];
+        uint16_t rest[kRB];
+        auto meanwhile = [&]() {
+#pragma unroll
+            for (int rb = 0; rb < kRB; ++rb) {
+                const int64_t b = m0 + min(t.row0 + 16 * rb + n, rows - 1);
+                target[rb] = a.targets[b];
+                rest[rb] = a.rest[b * a.ldrest];
+            }
+        };
+        DxSrc<decltype(meanwhile)> src(a, meanwhile);
         src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)m0 * a.ldz + (int64_t)b0 * kVocabBlock);
         src.dzbytes = ((int64_t)(rows - 1) * a.ldz + (int64_t)(b1 - b0) * kVocabBlock) * 2;
         src.nb_first = a.nb0 + b0;
@@ -676,11 +790,14 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
         t.init();
         t.template run<kAlongK, kAlongK, false, true>(smem, (b1 - b0) * (kVocabBlock / kStageK), a.ldz * 2,
                                              a.ldw * 2, src);
+        if (b1 == b0)  // (an empty split has not run)
+            meanwhile();
 #pragma unroll
         for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
             if (r >= rows)
                 continue;
+            const float whole = a.last && (uint32_t)target[rb] < (uint32_t)a.V ? 1.f + bf16_value(rest[rb]) : 1.f;
 #pragma unroll
             for (int cb = 0; cb < kCB; ++cb) {
                 const int c = src.h0 + t.col0 + 16 * cb + 4 * g;
@@ -689,10 +806,11 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
                 if (a.dxp) {
                     f32x4 *p = reinterpret_cast<f32x4 *>(
                         a.dxp + ((int64_t)split * a.B + m0 + r) * a.ldxp + c);
-                    *p = a.first ? t.acc[rb][cb] : *p + t.acc[rb][cb];
+                    const f32x4 sum = a.first ? t.acc[rb][cb] : *p + t.acc[rb][cb];
+                    *p = sum * whole;
                 } else {
-                    const float v[4] = {t.acc[rb][cb][0], t.acc[rb][cb][1], t.acc[rb][cb][2],
-                                        t.acc[rb][cb][3]};
+                    const f32x4 sum = t.acc[rb][cb] * whole;
+                    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
                     store_bf16x4(a.dx + (int64_t)(m0 + r) * a.lddx + c, v, a.H - c);
                 }
             }
@@ -710,16 +828,68 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
     if (nvalid <= 0)
         return;
     const int h0 = mt * kM, hrows = min(a.H - h0, kM);
-    DwSrc src;
+    t.init();
+    // What rounding took from the dz of the targets among the wave's columns, times
+    // their rows of x, goes on top of the product.  The rows are found, and the first
+    // one's x fetched, while the tile's first stages are on their way; each next
+    // row's x is fetched ahead.
+    TargetRows hits;
+    hits.col = a.vocab.off[lane] + c0 + t.col0;
+    hits.n = max(0, min(16 * kCB, nvalid - t.col0));
+    hits.next = hits.count = hits.row = hits.at = 0;
+    uint16_t high = 0, rest = 0;  // of lane i's row: its dz and what rounding took, relative to it
+    uint16_t ahead[kRB];
+    auto fetch = [&](int i) {
+        const uint16_t *row = a.xm + (int64_t)__builtin_amdgcn_readlane(hits.row, i) * a.ldxm + h0;
+#pragma unroll
+        for (int rb = 0; rb < kRB; ++rb) {
+            const int h = t.row0 + 16 * rb + n;
+            ahead[rb] = row[min(h, hrows - 1)];
+        }
+    };
+    auto find = [&]() {
+        hits.find(a);
+        high = a.dz[(int64_t)hits.row * a.ldz + (int64_t)nt * kN + t.col0 + hits.at];
+        rest = a.rest[hits.row * a.ldrest];
+        if (hits.count > 0)
+            fetch(0);
+    };
+    if (a.B > 0)
+        hits.load(a);
+    DwSrc<decltype(find)> src(find);
     src.x = reinterpret_cast<const uint8_t *>(a.xm + h0);
     src.dz = reinterpret_cast<const uint8_t *>(a.dz + (int64_t)nt * kN);
     src.ldx_bytes = a.ldxm * 2;
     src.ldz_bytes = a.ldz * 2;
     src.xbytes = ((int64_t)(a.B - 1) * a.ldxm + ((hrows + 7) & ~7)) * 2;
     src.zbytes = ((int64_t)(a.B - 1) * a.ldz + kN) * 2;
-    t.init();
     t.template run<kAcrossK, kAcrossK, false, false>(smem, (a.B + kStageK - 1) / kStageK, a.ldxm * 2,
                                             a.ldz * 2, src);
+    while (hits.count > 0) {
+        for (int i = 0; i < hits.count; ++i) {
+            float x[kRB];
+#pragma unroll
+            for (int rb = 0; rb < kRB; ++rb)
+                x[rb] = bf16_value(ahead[rb]);
+            fetch(min(i + 1, hits.count - 1));
+            const int c = __builtin_amdgcn_readlane(hits.at, i);
+            const float left = bf16_value((uint16_t)__builtin_amdgcn_readlane(high, i)) *
+                               bf16_value((uint16_t)__builtin_amdgcn_readlane(rest, i));
+            const float mine = (c >> 2 & 3) == g ? left : 0.f;
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c >> 4 == cb && (c & 3) == e)
+#pragma unroll
+                        for (int rb = 0; rb < kRB; ++rb)
+                            t.acc[rb][cb][e] = add_rest(t.acc[rb][cb][e], mine, x[rb]);
+        }
+        if (hits.next >= a.B)
+            break;
+        hits.load(a);
+        find();
+    }
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
@@ -856,6 +1026,15 @@ __global__ __launch_bounds__(kFewThreads, 1) void grad_rows_kernel(const LossArg
         const int c = (nb - a.vocab.blk0[lane]) * kVocabBlock + st % (kVocabBlock / kFewStep) * kFewStep;
         return Cols{lane, c, max(0, min(kFewStep, a.vocab.off[lane + 1] - a.vocab.off[lane] - c))};
     };
+    // of row L, where its dz is in one part: its target, and what rounding took from its
+    // dz there (relative to that)
+    int target = -1;
+    float rest = 0.f;
+    if (kParts == 1) {
+        const int b = min(L, a.B - 1), v = a.targets[b];
+        target = L < a.B ? v : -1;
+        rest = rest_of(a, b);
+    }
     const int64_t zplane = (int64_t)a.B * a.ldz;
     const int64_t zbytes = ((int64_t)(a.B - 1) * a.ldz + kFewStep) * 2;
     auto load = [&](int slot, int st) -> Cols {  // (at or past s1: zeros)
@@ -967,6 +1146,54 @@ __global__ __launch_bounds__(kFewThreads, 1) void grad_rows_kernel(const LossArg
                         dwa[hb][vb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             __builtin_bit_cast(bf16x8, zf), __builtin_bit_cast(bf16x8, xf[hb][kc % kXc]),
                             dwa[hb][vb], 0, 0, 0);
+                }
+        }
+        if (kParts == 1) {
+            const int at = (int)((uint32_t)target - (uint32_t)(a.vocab.off[cur.lane] + cur.c));
+            uint64_t hits = __builtin_amdgcn_ballot_w64((uint32_t)at < (uint32_t)cur.n);
+            if (__builtin_expect(hits != 0, 0))
+                for (; hits != 0; hits &= hits - 1) {
+                    const int b = __builtin_ctzll(hits), c = __builtin_amdgcn_readlane(at, b);
+                    const int piece = (c >> 3 ^ (b >> 1 & 7)) * 16 + 2 * (c & 7);
+                    const float left = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rest), b)) *
+                                       bf16_value(*reinterpret_cast<const uint16_t *>(zt + b * 128 + piece));
+                    if (want_dx) {
+                        const float mine = n == (b & 15) ? left : 0.f;
+#pragma unroll
+                        for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int r = 16 * hb + 4 * g + e;
+                                const float v = bf16_value(*reinterpret_cast<const uint16_t *>(
+                                    wt + r * 128 + (((c >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (c & 7)));
+#pragma unroll
+                                for (int mb = 0; mb < MB; ++mb)
+                                    if (b >> 4 == mb)
+                                        dxa[hb][mb][e] = add_rest(dxa[hb][mb][e], mine, v);
+                            }
+                    }
+                    if (want_dw) {
+                        // x[b][16 hb + n]: of lane 16 (b / 8 % 4) + n, value b % 8
+                        const float mine = (c >> 3 & 3) == g ? left : 0.f;
+#pragma unroll
+                        for (int hb = 0; hb < 4; ++hb) {
+                            uint32_t pair = 0;
+#pragma unroll
+                            for (int kc = 0; kc < kXc; ++kc)
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    if (b >> 5 == kc && (b >> 1 & 3) == d)
+                                        pair = xf[hb][kc][d];
+                            pair = (uint32_t)__shfl((int)pair, 16 * (b >> 3 & 3) + n);
+                            const float v = bf16_value((uint16_t)(pair >> (16 * (b & 1))));
+#pragma unroll
+                            for (int vb = 0; vb < 4; ++vb)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (2 * (c >> 5) + (c >> 2 & 1) == vb && (c & 3) == e)
+                                        dwa[hb][vb][e] = add_rest(dwa[hb][vb][e], mine, v);
+                        }
+                    }
                 }
         }
         wait_lds();  // the tiles are read: their slot can be filled again

@@ -34,7 +34,7 @@ struct Layout {
     int blocks = 0, piece = 0, splits = 1;
     bool direct = false;  // dx written without partial sums
     int slices = 1;       // K slices of the logits
-    size_t zp = 0, mse = 0, zt = 0, dz = 0, xm = 0, dxp = 0, total = 0;
+    size_t zp = 0, mse = 0, zt = 0, rest = 0, dz = 0, xm = 0, dxp = 0, total = 0;
     int64_t ldz = 0, ldxm = 0, ldxp = 0;
 };
 
@@ -89,7 +89,10 @@ Layout layout(const sb_head_desc *d, bool grad)
     at = up(at + B * (size_t)L.ldz * 2, kRegionAlign);
     L.xm = at;
     at = up(at + B * (size_t)L.ldxm * 2, kRegionAlign);
-    if (!L.direct) {
+    if (L.direct) {
+        L.rest = at;
+        at = up(at + B * 2, kRegionAlign);
+    } else {
         L.dxp = at;
         at = up(at + (size_t)L.splits * B * (size_t)L.ldxp * sizeof(float), kRegionAlign);
     }
@@ -257,6 +260,11 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
     if (desc->B == 0)  // dw of no rows is zero
         return sbk::launch_grad(a, false, true, s) == hipSuccess ? SB_OK : SB_ERR_HIP;
     a.dz = region<uint16_t>(ws, L.dz);
+    // What rounding takes from the targets' dz is needed until the last product is
+    // done.  Where dx is finished by a launch of its own, its first column is free
+    // until then; without dx its partial sums' memory is.
+    a.rest = L.direct ? region<uint16_t>(ws, L.rest) : dx ? a.dx : region<uint16_t>(ws, L.dxp);
+    a.ldrest = L.direct || !dx ? 1 : lddx;
     set_slices(desc, L, ws, a);
     if (desc->B <= sbk::kLossSmallRows) {
         a.dxp = region<float>(ws, L.dxp);
@@ -278,6 +286,7 @@ sb_status sb_cross_entropy_grad(const sb_head_desc *desc, const int32_t *targets
         a.nb0 = nb;
         a.nblk = std::min(L.piece, L.blocks - nb);
         a.first = nb == 0;
+        a.last = nb + L.piece >= L.blocks;
         if (sbk::launch_dlogits(a, s) != hipSuccess ||
             sbk::launch_grad(a, dx != nullptr, dw != nullptr, s) != hipSuccess)
             return SB_ERR_HIP;

@@ -306,7 +306,8 @@ struct WaveTile {
     // (their base the stage's first K step; empty from nst on), called once
     // for each stage in ascending order; src.tail(st) the valid K bytes of
     // stage st (>= 128 where nothing has to be zeroed): the kAlongK operands
-    // named by ZA / ZB are zeroed past it.
+    // named by ZA / ZB are zeroed past it.  src.meanwhile() runs while the first
+    // stages are on their way.
     template <int LA, int LB, bool ZA, bool ZB, typename Src>
     __device__ __forceinline__ void run(uint8_t *lds, int nst, int64_t lda_bytes, int64_t ldb_bytes,
                                         Src &src)
@@ -338,6 +339,7 @@ struct WaveTile {
         stage_load(slot_b(0), src.b(0), vb, wave);
         stage_load(lds + C::kABytes, src.a(1), va, wave);  // (empty where there is no stage 1)
         stage_load(slot_b(1), src.b(1), vb, wave);
+        src.meanwhile();
         __builtin_amdgcn_s_waitcnt(vmcnt_only(C::kALoads + C::kBLoads));  // stage 0 has landed
         block_barrier();
         mend(0, lds);

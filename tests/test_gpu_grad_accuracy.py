@@ -1,6 +1,7 @@
-"""GPU tests of how exact the gradient is above 32 rows, where dz is bf16 but for
-the targets', whose products are completed in fp32: on every path (streaming,
-small and big tiles, K slices, pieces, one or several sums of dX)."""
+"""GPU tests of how exact the gradient is: up to 32 rows, where dz is the sum of two
+bf16 numbers, and above, where dz is bf16 but for the targets', whose products are
+completed in fp32; on every path (streaming, small and big tiles, K slices, pieces,
+one or several sums of dX)."""
 import pytest
 import torch
 
@@ -16,6 +17,22 @@ def check(c, want=("dx", "dw")):
     dx, dw = c.grad(lse, want=want)
     check_grad_exactness(dx, dw, c.x, c.w, c.targets, c.dloss, lse)
     return lse, dx, dw
+
+
+@pytest.mark.parametrize("B,H,V,lanes", [(1, 40, 700, (0, 700)), (5, 65, 2570, (0, 1032, 2570)),
+                                         (16, 512, 2600, (0, 2600)), (16, 2100, 1500, (0, 1500)),
+                                         (17, 72, 3001, (0, 1000, 3001)), (32, 200, 3000, (0, 3000)),
+                                         (30, 2100, 1900, (0, 8, 1900))])
+@pytest.mark.parametrize("spread", [0.5, 6])
+def test_every_term_is_exact_up_to_32_rows(require_gpu, B, H, V, lanes, spread):
+    """Without slices and with; logits close together and so far apart that other
+    columns hold as much of a row as the target's."""
+    print(f"grad accuracy B={B} H={H} V={V} lanes={lanes} spread={spread}", flush=True)
+    c = Case(B, H, V, lanes, seed=B + V, scale=spread / H ** 0.5)
+    lse, dx, dw = check(c)
+    for want in ("dx", "dw"):
+        one = c.grad(lse, want=(want,))[0 if want == "dx" else 1]
+        assert torch.equal(one, dx if want == "dx" else dw), want
 
 
 SHAPES = [

@@ -317,7 +317,8 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
  * Training surface: softmax cross entropy over the whole vocabulary and its
  * gradient.  The logits are never written to memory.
  *   lse[b]  = log sum_v exp(z[b][v])
- *   loss[b] = lse[b] - z[b][targets[b]]
+ *   loss[b] = lse[b] - z[b][targets[b]], taken as (max z - z target) + log sum
+ *             exp(z - max z): a small loss keeps its digits beside large logits
  *   dz[b][v] = (exp(z[b][v] - lse[b]) - [v == targets[b]]) * dloss[b]
  *   dx = dz . W^T (bf16 [B][lddx]),  dw = x^T . dz (bf16, lane by lane)
  *  - A negative target marks an ignored row (padding): its loss is 0, its row

@@ -77,6 +77,17 @@ __device__ __forceinline__ float add_rest(float sum, float rest, float v)
     return fabsf(c) < INFINITY ? sum + c : sum;
 }
 
+// lse and loss of a row from its logits' maximum and sum exp(z - maximum).  The
+// target's logit is taken from the maximum: what the two leave is exact where they
+// are close, while lse - z would round a small loss to the step of a large logit.
+__device__ __forceinline__ void store_loss(const LossArgs &a, int64_t b, float m, float s)
+{
+    const float logs = logf(s);
+    const int t = a.targets[b];
+    a.lse[b] = m + logs;
+    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : m - a.zt[b] + logs);
+}
+
 enum LogitsUse { kUseLoss, kUseGrad };
 
 // Z tile = rows of X times a block of W.
@@ -298,10 +309,7 @@ __global__ __launch_bounds__(kCombineRows * kCombineRuns) void loss_combine_kern
 #pragma unroll
     for (int w = 1; w < kCombineRuns / 4; ++w)
         merge_ms(m, s, part[w][row].x, part[w][row].y);
-    const float l = m + __logf(s);
-    const int t = a.targets[b];
-    a.lse[b] = l;
-    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : l - a.zt[b]);
+    store_loss(a, b, m, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -610,10 +618,7 @@ __global__ __launch_bounds__(256) void loss_rows_combine_kernel(const LossArgs a
         return;
     for (int w = 1; w < 4; ++w)
         merge_ms(m, s, part[w].x, part[w].y);
-    const float l = m + __logf(s);
-    const int t = a.targets[b];
-    a.lse[b] = l;
-    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : l - a.zt[b]);
+    store_loss(a, b, m, s);
 }
 
 // Copies x in 16-byte units, the rows of negative targets as zeros: an

@@ -335,7 +335,9 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
  *    (in dx above 64 rows their sum by 2^-8 more).  Repeated calls give the same
  *    bits.
  *  - Non-finite logits follow IEEE rules: a row with a NaN or +inf logit has a
- *    NaN lse; -inf logits count as probability 0.
+ *    NaN lse; -inf logits count as probability 0, also in a row of nothing else:
+ *    its lse is -inf, its loss +inf and its dz -dloss at the target, 0 elsewhere.
+ *    Products with a non-finite x or W in dx and dw are NaN where dz is 0.
  * The head descriptor and its limits are the projection calls'.  Also (else
  * SB_ERR_UNSUPPORTED) 256 rows of x must span less than 4 GiB, and so must 64
  * shard rows, 256 of them in the gradient; the gradient of up to 64 rows takes

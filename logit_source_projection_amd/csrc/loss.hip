@@ -80,13 +80,19 @@ __device__ __forceinline__ float add_rest(float sum, float rest, float v)
 // lse and loss of a row from its logits' maximum and sum exp(z - maximum).  The
 // target's logit is taken from the maximum: what the two leave is exact where they
 // are close, while lse - z would round a small loss to the step of a large logit.
+// A row of -inf only (no sum) has probability 0 at its target: an infinite loss.
 __device__ __forceinline__ void store_loss(const LossArgs &a, int64_t b, float m, float s)
 {
     const float logs = logf(s);
     const int t = a.targets[b];
     a.lse[b] = m + logs;
-    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : m - a.zt[b] + logs);
+    const float loss = m == -INFINITY && s == 0.f ? INFINITY : m - a.zt[b] + logs;
+    a.loss[b] = t < 0 ? 0.f : (t >= a.V ? NAN : loss);
 }
+
+// The lse that the gradient's probabilities exp(z - lse) are formed with: a row of
+// -inf only has probability 0 everywhere, not exp(-inf + inf).
+__device__ __forceinline__ float grad_lse(float lse) { return lse == -INFINITY ? 0.f : lse; }
 
 enum LogitsUse { kUseLoss, kUseGrad };
 
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
         for (int rb = 0; rb < kRB; ++rb) {
             const int r = t.row0 + 16 * rb + n;
             const int tgt = r < rows ? a.targets[m0 + r] : -1;
-            const float l = r < rows ? a.lse_in[m0 + r] : 0.f;
+            const float l = r < rows ? grad_lse(a.lse_in[m0 + r]) : 0.f;
             // a target past the vocabulary has no gradient: NaN, not a guess
             const float scale = r >= rows ? 0.f : (tgt >= a.V ? NAN : a.dloss[m0 + r]);
             const uint32_t keep = tgt < 0 ? 0u : 0xFFFFFFFFu;  // ignored rows: 0, whatever z is
@@ -359,7 +365,7 @@ struct RowGrad {
     __device__ __forceinline__ RowGrad(const LossArgs &a, int64_t b)
     {
         target = a.targets[b];
-        lse = a.lse_in[b];
+        lse = grad_lse(a.lse_in[b]);
         // a target past the vocabulary has no gradient: NaN, not a guess
         scale = target >= a.V ? NAN : a.dloss[b];
     }

@@ -6,6 +6,13 @@
 
 namespace sbk {
 
+// Whether `rows` rows, `ld` elements of `bytes` bytes apart, span 4 GiB or more (past the
+// kernels' 32-bit offsets).  A quotient: the product of a wild stride passes 64 bits.
+inline bool spans_4gib(int64_t rows, int64_t ld, int64_t bytes)
+{
+    return ld > (((int64_t)1 << 32) - 1) / (rows * bytes);
+}
+
 constexpr int kMaxLanes = 64;
 constexpr int kTileN = 128;     // vocab columns per workgroup tile
 constexpr int kStepK = 32;      // hidden rows per MFMA step (16x16x32 bf16)

@@ -71,12 +71,12 @@ sb_status check_desc(const sb_head_desc *d)
     // (B >= 65) a K stage of a shard (32 rows up to 128 rows, else 64; plus 8)
     // and one block of x (128 rows up to 128 rows, else 256).
     const int64_t lim = (int64_t)1 << 32;
-    if ((int64_t)(sbk::kStepK + 8) * d->ldw * 2 >= lim ||
-        (int64_t)(sbk::kRowBlock * sbk::kMaxMB) * d->ldx * 2 >= lim)
+    if (sbk::spans_4gib(sbk::kStepK + 8, d->ldw, 2) ||
+        sbk::spans_4gib(sbk::kRowBlock * sbk::kMaxMB, d->ldx, 2))
         return SB_ERR_UNSUPPORTED;
     if (d->B >= sbk::kLargeBatch &&
-        ((int64_t)(sbk::large_step_k(d->B) + 8) * d->ldw * 2 >= lim ||
-         (int64_t)sbk::large_block_rows(d->B) * d->ldx * 2 >= lim))
+        (sbk::spans_4gib(sbk::large_step_k(d->B) + 8, d->ldw, 2) ||
+         sbk::spans_4gib(sbk::large_block_rows(d->B), d->ldx, 2)))
         return SB_ERR_UNSUPPORTED;
     // every launch fits one grid (fewer than 2^32 work items per dimension);
     // among others this bounds B below 2^24, the combine's one workgroup per row
@@ -303,8 +303,8 @@ sb_status check_partial(const sb_partial_desc *d)
     // per-chunk buffer offsets are 32-bit: a chunk of weight rows and one row
     // group of an activation shard must span less than 4 GiB
     const int64_t lim = (int64_t)1 << 32;
-    if ((int64_t)(sbk::kPartChunk + 8) * d->ldw * 2 >= lim ||
-        (int64_t)(sbk::kRowBlock * sbk::kMaxMB) * d->ldx * 2 >= lim)
+    if (sbk::spans_4gib(sbk::kPartChunk + 8, d->ldw, 2) ||
+        sbk::spans_4gib(sbk::kRowBlock * sbk::kMaxMB, d->ldx, 2))
         return SB_ERR_UNSUPPORTED;
     // the chunked GEMM's launch fits one grid
     int64_t chunks = 0;

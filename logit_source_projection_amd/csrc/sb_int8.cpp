@@ -68,9 +68,8 @@ sb_status check(const sb_int8_desc *d)
         }
     }
     // exact 32-bit sums; 32-bit offsets over 256 rows and 256 channels
-    const int64_t lim = (int64_t)1 << 32;
-    if (d->V > kMaxVocab || d->H > sbk::kInt8MaxH || (int64_t)256 * d->ldx >= lim ||
-        (int64_t)256 * d->ldw >= lim)
+    if (d->V > kMaxVocab || d->H > sbk::kInt8MaxH || sbk::spans_4gib(256, d->ldx, 1) ||
+        sbk::spans_4gib(256, d->ldw, 1))
         return SB_ERR_UNSUPPORTED;
     const bool few = sbk::int8_few(d->B, d->V);
     const int64_t tiles = tiles_of(d->lane_off, d->k, sbk::int8_tile(few));

@@ -109,14 +109,12 @@ sb_status check(const sb_head_desc *d, bool grad)
         return st;
     // 32-bit offsets: 256 rows of x; 64 rows of a shard, and 256 in the gradient;
     // there also 256 rows of a piece of dz (all columns with few rows)
-    const int64_t lim = (int64_t)1 << 32;
-    if ((int64_t)sbk::kVocabBlock * d->ldx * 2 >= lim ||
-        (int64_t)(grad ? sbk::kVocabBlock : 64) * d->ldw * 2 >= lim)
+    if (sbk::spans_4gib(sbk::kVocabBlock, d->ldx, 2) ||
+        sbk::spans_4gib(grad ? sbk::kVocabBlock : 64, d->ldw, 2))
         return SB_ERR_UNSUPPORTED;
     const Layout L = layout(d, grad);
     const int nblk = grad ? L.piece : L.blocks;
-    if (grad && ((int64_t)sbk::kVocabBlock * L.ldz * 2 >= lim ||
-                 (int64_t)64 * L.ldxm * 2 >= lim))
+    if (grad && (sbk::spans_4gib(sbk::kVocabBlock, L.ldz, 2) || sbk::spans_4gib(64, L.ldxm, 2)))
         return SB_ERR_UNSUPPORTED;
     if (sbk::loss_launch_items(d->B, d->H, nblk, L.splits) >= kItems)
         return SB_ERR_UNSUPPORTED;

@@ -179,6 +179,11 @@ def _matrix(t, name, dtype, rows, cols):
         raise ValueError(f"{name} must be a [>= {rows}, >= {cols}] matrix with unit column stride")
 
 
+def _holds(t, name, rows, cols):
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must be a [>= {rows}, >= {cols}] matrix, not {list(t.shape)}")
+
+
 def _operands(tensors, name):
     """The bf16 operands a descriptor was built from: on the device, rows
     with unit column stride."""
@@ -254,9 +259,25 @@ class Head:
             _operands([self.x], "x")
             _operands(self.w if isinstance(self.w, (list, tuple)) else [self.w], "w")
 
+    def check_shapes(self):
+        """The operands hold what the descriptor says."""
+        d, off = self.desc, self.lane_off
+        _holds(self.x, "x", d.B, d.H)
+        if isinstance(self.w, (list, tuple)):
+            if len(self.w) != len(off) - 1:
+                raise ValueError(f"w must hold one tensor per lane, {len(off) - 1}")
+            for i, t in enumerate(self.w):
+                _holds(t, f"w[{i}]", d.H, off[i + 1] - off[i])
+            if d.H > 1 and len({t.stride(0) for t in self.w}) > 1:
+                raise ValueError("the tensors of w must have one row stride")
+        else:
+            _holds(self.w, "w", d.H, off[-1])
+
     def device(self):
-        """The one device of the operands (None for raw pointers)."""
+        """The one device of the operands (None for raw pointers).  The
+        descriptor holds their addresses, so their shapes are checked once."""
         if self._device is None and self.from_tensors:
+            self.check_shapes()
             self._device = _one_device([self.x] + _as_list(self.w))
         return self._device
 

@@ -468,7 +468,8 @@ def sb_partial_complete(part, op, out, ws=None, stream=None):
 
 # ---------------------------------------------------------------------------
 # Training surface.  These calls run on the device of their tensors, whatever
-# the current one is; a stream that is not given is that device's current one.
+# the current one is; a stream that is not given is that device's current one, and a
+# given one has to be that device's.
 # ---------------------------------------------------------------------------
 def _one_device(tensors, device=None):
     """The device that holds every tensor of a call (and the operands of its
@@ -499,15 +500,18 @@ def _stream_on(stream, device):
     (taken as a number: a torch.cuda.Stream object costs 3 us a call)."""
     if stream is None:
         return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {device}")
     return _stream(stream)
 
 
 def _run(name, device, stream, nbytes_fn, ws, call):
     """call(workspace pointer, its size, stream) on `device`."""
     with _on(device):
+        s = _stream_on(stream, device)
         if ws is None:
             ws = _workspace(nbytes_fn, ws, device, stream)
-        _check(call(ws.data_ptr(), ws.numel(), _stream_on(stream, device)), name)
+        _check(call(ws.data_ptr(), ws.numel(), s), name)
 
 
 def sb_cross_entropy_workspace_bytes(head, grad):

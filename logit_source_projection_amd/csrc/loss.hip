@@ -117,23 +117,22 @@ struct LogitsSrc {
 
 // More than 64 rows: a tile of the logits per workgroup, reduced (loss) or
 // turned into dz (gradient) in its registers; where tiles are few, K is split
-// (loss_slices), the slices' fp32 logits are stored and join_kernel does the rest.
+// (loss_slices), the slices' fp32 logits are stored and join_kernel does the rest
+// (SPLIT, which only small tiles have, and where USE does not matter).
 //
 // Bound by MFMA at the clock that power allows: 2048 rows of the dense head (H
 // 5120, V 151936) take 2.39 ms (1.33 PFLOP/s), the pieces of a 4096-row gradient
 // 1.01 ms each (1.28 PFLOP/s, 256 MB of dz written).  With a short H the ends of
 // a tile count: 257 rows of H 1111, V 50257 take 68 us, 18 stages a tile.
-template <class C, int USE>
+template <class C, int USE, bool SPLIT>
 __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const LossArgs a, const TileGrid grid)
 {
     constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    // only small tiles split K; big ones have no register to spare for it
-    const int slices = C::kPerCu > 1 ? a.slices : 1;
-    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * slices);
+    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, SPLIT ? tiles * a.slices : tiles);
     if (number < 0)
         return;
-    const int slice = number / tiles;
+    const int slice = SPLIT ? number / tiles : 0;
     int mt, nt;
     tile_of(grid, number - slice * tiles, mt, nt);
     const int nb = a.nb0 + nt / (kVocabBlock / kN);
@@ -144,8 +143,8 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
     const int m0 = mt * kM;
     const int rows = min(a.B - m0, kM);
     // the slice's part of K: H rows of the weight from k0
-    const int k0 = slice * a.slice_steps * kLossStepK;
-    const int H = slices > 1 ? min(a.H - k0, a.slice_steps * kLossStepK) : a.H;
+    const int k0 = SPLIT ? slice * a.slice_steps * kLossStepK : 0;
+    const int H = SPLIT ? min(a.H - k0, a.slice_steps * kLossStepK) : a.H;
 
     LogitsSrc src;
     src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx + k0);
@@ -159,7 +158,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const Lo
     t.template run<kAlongK, kAcrossK, true, false>(smem, (H + kStageK - 1) / kStageK, a.ldx * 2, a.ldw * 2,
                                           src);
 
-    if (slices > 1) {
+    if (SPLIT) {
         const int64_t ld = (int64_t)a.nblk * kVocabBlock;
         float *p = a.zp + ((int64_t)slice * a.B + m0) * ld + (int64_t)nt * kN + t.col0 + 4 * (t.L >> 4);
 #pragma unroll
@@ -1288,35 +1287,36 @@ __global__ __launch_bounds__(256) void dx_finish_kernel(const LossArgs a)
     store_bf16x4(a.dx + b * a.lddx + c, v, a.H - c);
 }
 
-// The slices' sums added up, where there are several.
+// The slices' sums added up.
 template <int USE>
 hipError_t launch_join(const LossArgs &a, hipStream_t s)
 {
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.slices == 1)
-        return e;
     hipLaunchKernelGGL(join_kernel<USE>, dim3((unsigned)loss_parts(a.B, a.nblk, a.slices), a.B), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
-template <class C, int USE>
+template <class C, int USE, bool SPLIT>
 hipError_t launch_logits_tiles(const LossArgs &a, hipStream_t s)
 {
     const TileGrid g = tile_grid<C>(a.B, (int64_t)a.nblk * kVocabBlock);
     static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds((const void *)logits_kernel<C, USE>, C::kLds, lds_done);
+    const hipError_t e = allow_lds((const void *)logits_kernel<C, USE, SPLIT>, C::kLds, lds_done);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((logits_kernel<C, USE>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)),
+    hipLaunchKernelGGL((logits_kernel<C, USE, SPLIT>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)),
                        dim3(C::kThreads), C::kLds, s, a, g);
-    return launch_join<USE>(a, s);
+    return hipGetLastError();
 }
 
 template <int USE>
 hipError_t launch_logits(const LossArgs &a, hipStream_t s)
 {
-    return small_logits(a.B, a.nblk) ? launch_logits_tiles<SmallTile, USE>(a, s)
-                                     : launch_logits_tiles<BigTile, USE>(a, s);
+    if (!small_logits(a.B, a.nblk))
+        return launch_logits_tiles<BigTile, USE, false>(a, s);
+    if (a.slices == 1)
+        return launch_logits_tiles<SmallTile, USE, false>(a, s);
+    const hipError_t e = launch_logits_tiles<SmallTile, kUseLoss, true>(a, s);
+    return e != hipSuccess ? e : launch_join<USE>(a, s);
 }
 
 template <class C>
@@ -1345,7 +1345,8 @@ hipError_t launch_logits_rows(const LossArgs &a, hipStream_t s)
         hipLaunchKernelGGL((logits_rows_kernel<2, USE>), grid, dim3(kRowsThreads), 0, s, a);
     else
         hipLaunchKernelGGL((logits_rows_kernel<4, USE>), grid, dim3(kRowsThreads), 0, s, a);
-    return launch_join<USE>(a, s);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || a.slices == 1 ? e : launch_join<USE>(a, s);
 }
 
 // Steps of a workgroup where `splits` of them share the blocks.

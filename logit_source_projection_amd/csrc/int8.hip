@@ -494,6 +494,11 @@ __global__ __launch_bounds__(kRowsThreads) void int8_rows_kernel(const Int8Args 
 #pragma unroll
         for (int i = 0; i < kRowsLoads; ++i)
             load_to_lds<2>(ring + j * kRowsSlotBytes + i * 1024, rw, wo[i]);
+        // (new to the compiler in every step, which else keeps xo + 64 in registers of its
+        // own instead of the load's immediate)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+            asm("" : "+v"(xo[mb]));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll

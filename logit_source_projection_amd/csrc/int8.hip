@@ -277,9 +277,9 @@ __device__ __forceinline__ void store_logits(const Int8Args &a, int64_t b, int g
 // Large batches: MFMA tiles, both operands along K.  Bound by MFMA: 2048 rows of
 // H 5120, V 151936 take 1.46 ms with 1.24 GB of fp32 logits written (2.18 POP/s),
 // the IDs of 1024 rows 0.69 ms (2.3 POP/s, what one large library product gets).
-// Few tiles split K (int8_slices; SPLIT, which only small tiles have, and where TOKENS
-// does not matter): a slice stores its 32-bit sums, which int8_join_kernel adds up;
-// integer sums do not depend on the split.
+// Few tiles split K (int8_slices): a slice stores its 32-bit sums, which
+// int8_join_kernel adds up; integer sums do not depend on the split.  (The split as
+// a template argument: 128 rows, H 1024, V 14000 12.6 -> 12.8 us.)
 // ---------------------------------------------------------------------------
 struct Int8Src {
     const uint8_t *x, *w;
@@ -299,15 +299,17 @@ struct Int8Src {
     __device__ __forceinline__ void meanwhile() const {}
 };
 
-template <class C, bool TOKENS, bool SPLIT>
+template <class C, bool TOKENS>
 __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const Int8Args a, const TileGrid grid)
 {
     constexpr int kM = C::kM, kN = C::kN, kWN = C::kWN, kRB = C::kRB, kCB = C::kCB;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, SPLIT ? tiles * a.slices : tiles);
+    // only small tiles split K; big ones have no register to spare for it
+    const int slices = C::kPerCu > 1 ? a.slices : 1;
+    const int tiles = grid.mt * grid.nt, number = xcd_tile(blockIdx.x, tiles * slices);
     if (number < 0)
         return;
-    const int slice = SPLIT ? number / tiles : 0;
+    const int slice = number / tiles;
     int mt, nt;
     tile_of(grid, number - slice * tiles, mt, nt);
     const int block = nt / (kInt8LargeTile / kN);
@@ -317,8 +319,8 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
     const int nvalid = max(0, min(kN, a.off[lane + 1] - a.off[lane] - c0));
     const int m0 = mt * kM, rows = min(a.B - m0, kM);
     // the slice's part of K: H bytes from k0
-    const int k0 = SPLIT ? slice * a.slice_steps * kInt8StepK : 0;
-    const int H = SPLIT ? min(a.H - k0, a.slice_steps * kInt8StepK) : a.H;
+    const int k0 = slice * a.slice_steps * kInt8StepK;
+    const int H = slices > 1 ? min(a.H - k0, a.slice_steps * kInt8StepK) : a.H;
     const int padded = ((a.H + 15) & ~15) - k0;
     Int8Src src;
     src.x = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx + k0);
@@ -332,7 +334,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void int8_tile_kernel(const
     t.template run<kAlongK, kAlongK, true, false>(smem, (H + kStageBytes - 1) / kStageBytes, a.ldx, a.ldw, src);
 
     const int n = t.L & 15, g = t.L >> 4;
-    if (SPLIT) {
+    if (slices > 1) {
         const int64_t ld = (int64_t)a.tile0[a.k] * kInt8LargeTile;
         int32_t *p = a.part + ((int64_t)slice * a.B + m0) * ld + (int64_t)nt * kN + t.col0 + 4 * g;
 #pragma unroll
@@ -705,15 +707,15 @@ hipError_t launch_rows(const Int8Args &a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <class C, bool TOKENS, bool SPLIT>
+template <class C, bool TOKENS>
 hipError_t launch_tiles_as(const Int8Args &a, hipStream_t s)
 {
     const TileGrid g = tile_grid<C>(a.B, (int64_t)a.tile0[a.k] * kInt8LargeTile);
     static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds((const void *)int8_tile_kernel<C, TOKENS, SPLIT>, C::kLds, lds_done);
+    const hipError_t e = allow_lds((const void *)int8_tile_kernel<C, TOKENS>, C::kLds, lds_done);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((int8_tile_kernel<C, TOKENS, SPLIT>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)), dim3(C::kThreads),
+    hipLaunchKernelGGL((int8_tile_kernel<C, TOKENS>), dim3((unsigned)xcd_ids(tile_count(g) * a.slices)), dim3(C::kThreads),
                        C::kLds, s, a, g);
     return hipGetLastError();
 }
@@ -721,10 +723,8 @@ hipError_t launch_tiles_as(const Int8Args &a, hipStream_t s)
 template <bool TOKENS>
 hipError_t launch_tiles(const Int8Args &a, hipStream_t s)
 {
-    if (!int8_small(a.B, a.tile0[a.k]))
-        return launch_tiles_as<BigTile, TOKENS, false>(a, s);
-    return a.slices == 1 ? launch_tiles_as<SmallTile, TOKENS, false>(a, s)
-                         : launch_tiles_as<SmallTile, false, true>(a, s);
+    return int8_small(a.B, a.tile0[a.k]) ? launch_tiles_as<SmallTile, TOKENS>(a, s)
+                                         : launch_tiles_as<BigTile, TOKENS>(a, s);
 }
 
 }  // namespace

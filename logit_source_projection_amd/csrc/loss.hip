@@ -840,22 +840,21 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
     const int h0 = mt * kM, hrows = min(a.H - h0, kM);
     t.init();
     // What rounding took from the dz of the targets among the wave's columns, times
-    // their rows of x, goes on top of the product.  The rows are found, and the first
-    // one's x fetched, while the tile's first stages are on their way; each next
-    // row's x is fetched ahead.
+    // their rows of x, goes on top of the product, four rows at a time: a step of MFMAs
+    // whose k = 8 g is the list's row i + g and whose other k are zeros.  The rows are
+    // found, and the first four's x fetched, while the tile's first stages are on
+    // their way; each next four's are fetched ahead.
     TargetRows hits;
     hits.col = a.vocab.off[lane] + c0 + t.col0;
     hits.n = max(0, min(16 * kCB, nvalid - t.col0));
     hits.next = hits.count = hits.row = hits.at = 0;
     uint16_t high = 0, rest = 0;  // of lane i's row: its dz and what rounding took, relative to it
-    uint16_t ahead[kRB];
+    uint16_t ahead[kRB];          // x of the next four rows
     auto fetch = [&](int i) {
-        const uint16_t *row = a.xm + (int64_t)__builtin_amdgcn_readlane(hits.row, i) * a.ldxm + h0;
+        const uint16_t *row = a.xm + (int64_t)__shfl(hits.row, i + g) * a.ldxm + h0;
 #pragma unroll
-        for (int rb = 0; rb < kRB; ++rb) {
-            const int h = t.row0 + 16 * rb + n;
-            ahead[rb] = row[min(h, hrows - 1)];
-        }
+        for (int rb = 0; rb < kRB; ++rb)
+            ahead[rb] = row[min(t.row0 + 16 * rb + n, hrows - 1)];
     };
     auto find = [&]() {
         hits.find(a);
@@ -876,24 +875,23 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
     t.template run<kAcrossK, kAcrossK, false, false>(smem, (a.B + kStageK - 1) / kStageK, a.ldxm * 2,
                                             a.ldz * 2, src);
     while (hits.count > 0) {
-        for (int i = 0; i < hits.count; ++i) {
-            float x[kRB];
+        const float took = bf16_value(high) * bf16_value(rest);  // (NaN of an infinite dz)
+        const int left = __builtin_bit_cast(uint16_t, (__bf16)(fabsf(took) < INFINITY ? took : 0.f));
+        for (int i = 0; i < hits.count; i += 4) {
+            const bool ok = i + g < hits.count;
+            const int at = __shfl(hits.at, i + g), z = __shfl(left, i + g);
+            uint32_t x[kRB];
 #pragma unroll
             for (int rb = 0; rb < kRB; ++rb)
-                x[rb] = bf16_value(ahead[rb]);
-            fetch(min(i + 1, hits.count - 1));
-            const int c = __builtin_amdgcn_readlane(hits.at, i);
-            const float left = bf16_value((uint16_t)__builtin_amdgcn_readlane(high, i)) *
-                               bf16_value((uint16_t)__builtin_amdgcn_readlane(rest, i));
-            const float mine = (c >> 2 & 3) == g ? left : 0.f;
+                x[rb] = ok ? ahead[rb] : 0u;
+            fetch(min(i + 4, 60));
 #pragma unroll
-            for (int cb = 0; cb < kCB; ++cb)
+            for (int cb = 0; cb < kCB; ++cb) {
+                const u32x4 zf = {ok && at == 16 * cb + n ? (uint32_t)z : 0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c >> 4 == cb && (c & 3) == e)
-#pragma unroll
-                        for (int rb = 0; rb < kRB; ++rb)
-                            t.acc[rb][cb][e] = add_rest(t.acc[rb][cb][e], mine, x[rb]);
+                for (int rb = 0; rb < kRB; ++rb)
+                    block_mma(t.acc[rb][cb], u32x4{x[rb], 0u, 0u, 0u}, zf);
+            }
         }
         if (hits.next >= a.B)
             break;

@@ -131,3 +131,21 @@ def test_replayed_with_new_targets(require_gpu, B):
         check_grad_exactness(dx, dw, c.x, c.w, c.targets, c.dloss, lse)
         eager = c.grad(lse)
         assert torch.equal(dx, eager[0]) and torch.equal(dw, eager[1]), turn
+
+
+@pytest.mark.parametrize("B", [40, 100, 2100])
+def test_infinite_row_weight(require_gpu, B):
+    """One row's loss weighted infinitely: dw is infinite, not NaN, wherever that row
+    has an x and a probability, and the other rows' dx is theirs alone."""
+    V = 3000
+    c = Case(B, 16, V, (0, V), seed=B, ignored=0, scale=0.05)
+    c.x[1] = 1
+    _, lse = c.loss()
+    dx, dw = c.grad(lse)
+    c.dloss[1] = float("inf")
+    dx2, dw2 = c.grad(lse)
+    rest = torch.arange(B, device="cuda") != 1
+    assert torch.equal(dx2[rest], dx[rest])
+    sign = torch.ones(V, device="cuda")
+    sign[c.targets[1].long()] = -1
+    assert torch.equal(dw2.float(), sign.expand(16, V) * float("inf"))

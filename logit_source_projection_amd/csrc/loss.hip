@@ -1157,52 +1157,62 @@ __global__ __launch_bounds__(kFewThreads, 1) void grad_rows_kernel(const LossArg
                 }
         }
         if (kParts == 1) {
-            const int at = (int)((uint32_t)target - (uint32_t)(a.vocab.off[cur.lane] + cur.c));
-            uint64_t hits = __builtin_amdgcn_ballot_w64((uint32_t)at < (uint32_t)cur.n);
-            if (__builtin_expect(hits != 0, 0))
-                for (; hits != 0; hits &= hits - 1) {
-                    const int b = __builtin_ctzll(hits), c = __builtin_amdgcn_readlane(at, b);
-                    const int piece = (c >> 3 ^ (b >> 1 & 7)) * 16 + 2 * (c & 7);
-                    const float left = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rest), b)) *
-                                       bf16_value(*reinterpret_cast<const uint16_t *>(zt + b * 128 + piece));
-                    if (want_dx) {
-                        const float mine = n == (b & 15) ? left : 0.f;
+            const uint32_t c = (uint32_t)target - (uint32_t)(a.vocab.off[cur.lane] + cur.c);
+            const bool hit = c < (uint32_t)cur.n;
+            const uint64_t hits = __builtin_amdgcn_ballot_w64(hit);
+            if (__builtin_expect(hits != 0, 0)) {
+                // row L: the target's place among the step's columns, and what rounding took there
+                const int at = hit ? (int)c : 0;
+                const float took = rest * bf16_value(*reinterpret_cast<const uint16_t *>(
+                                              zt + L * 128 + (((at >> 3) ^ ((L >> 1) & 7)) * 16) + 2 * (at & 7)));
+                const float left = hit && fabsf(took) < INFINITY ? took : 0.f;
+                if (want_dx)
+                    for (uint64_t m = hits; m != 0; m &= m - 1) {
+                        const int b = __builtin_ctzll(m), col = __builtin_amdgcn_readlane(at, b);
+                        const float of_b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(left), b));
+                        const float mine = n == (b & 15) ? of_b : 0.f;
+                        float v[4][4];
 #pragma unroll
                         for (int hb = 0; hb < 4; ++hb)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int r = 16 * hb + 4 * g + e;
-                                const float v = bf16_value(*reinterpret_cast<const uint16_t *>(
-                                    wt + r * 128 + (((c >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (c & 7)));
-#pragma unroll
-                                for (int mb = 0; mb < MB; ++mb)
-                                    if (b >> 4 == mb)
-                                        dxa[hb][mb][e] = add_rest(dxa[hb][mb][e], mine, v);
+                                v[hb][e] = bf16_value(*reinterpret_cast<const uint16_t *>(
+                                    wt + r * 128 + (((col >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (col & 7)));
                             }
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb)
+                            if (b >> 4 == mb)
+#pragma unroll
+                                for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        dxa[hb][mb][e] = add_rest(dxa[hb][mb][e], mine, v[hb][e]);
                     }
-                    if (want_dw) {
-                        // x[b][16 hb + n]: of lane 16 (b / 8 % 4) + n, value b % 8
-                        const float mine = (c >> 3 & 3) == g ? left : 0.f;
+                if (want_dw) {
+                    // another step of dW's product, with these in place of dz
+                    const int packed = at << 16 | __builtin_bit_cast(uint16_t, (__bf16)left);
 #pragma unroll
-                        for (int hb = 0; hb < 4; ++hb) {
-                            uint32_t pair = 0;
+                    for (int kc = 0; kc < kXc; ++kc) {
+                        if ((uint32_t)(hits >> (32 * kc)) == 0u)
+                            continue;
+                        u32x4 zf[4] = {};
 #pragma unroll
-                            for (int kc = 0; kc < kXc; ++kc)
-#pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    if (b >> 5 == kc && (b >> 1 & 3) == d)
-                                        pair = xf[hb][kc][d];
-                            pair = (uint32_t)__shfl((int)pair, 16 * (b >> 3 & 3) + n);
-                            const float v = bf16_value((uint16_t)(pair >> (16 * (b & 1))));
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t of_b = (uint32_t)__shfl(packed, 32 * kc + 8 * g + j);
 #pragma unroll
                             for (int vb = 0; vb < 4; ++vb)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (2 * (c >> 5) + (c >> 2 & 1) == vb && (c & 3) == e)
-                                        dwa[hb][vb][e] = add_rest(dwa[hb][vb][e], mine, v);
+                                if ((int)(of_b >> 16) == 32 * (vb >> 1) + 8 * (n >> 2) + 4 * (vb & 1) + (n & 3))
+                                    zf[vb][j >> 1] |= (of_b & 0xFFFFu) << (16 * (j & 1));
                         }
+#pragma unroll
+                        for (int vb = 0; vb < 4; ++vb)
+#pragma unroll
+                            for (int hb = 0; hb < 4; ++hb)
+                                block_mma(dwa[hb][vb], xf[hb][kc], zf[vb]);
                     }
                 }
+            }
         }
         wait_lds();  // the tiles are read: their slot can be filled again
         const Cols done = cur;

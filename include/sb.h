@@ -315,7 +315,8 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
 /*
  * ---------------------------------------------------------------------------
  * Training surface: softmax cross entropy over the whole vocabulary and its
- * gradient.  The logits are never written to memory.
+ * gradient.  The logits are not kept (few tiles of them split their hidden sum into
+ * slices, whose sums pass through the workspace).
  *   lse[b]  = log sum_v exp(z[b][v])
  *   loss[b] = lse[b] - z[b][targets[b]], taken as (max z - z target) + log sum
  *             exp(z - max z): a small loss keeps its digits beside large logits
@@ -323,17 +324,17 @@ sb_status sb_partial_complete(const sb_partial_desc *desc, int op, float *out, i
  *   dx = dz . W^T (bf16 [B][lddx]),  dw = x^T . dz (bf16, lane by lane)
  *  - A negative target marks an ignored row (padding): its loss is 0, its row
  *    of dx is 0 wherever W is finite, and it adds nothing to dw, whatever its
- *    x holds.  Its lse is computed like any other.  A target >= V makes the
- *    row's loss, its row of dx and all of dw NaN.
- *  - Logits are fp32 sums of exact bf16 x bf16 products, in an order fixed by
- *    H (not the order of the projection calls: last bits can differ from
- *    theirs).  lse is an online sum over 256-column blocks.  The gradient
+ *    x holds.  Its lse is computed like any other, and it costs as much.  A
+ *    target >= V makes the row's loss, its row of dx and all of dw NaN.
+ *  - Logits are fp32 sums of exact bf16 x bf16 products, and lse an online sum, in
+ *    orders fixed by B, H, V and the lane offsets: the same call repeated gives
+ *    the same bits, while the same row in another batch size, under another lane
+ *    split or in a projection call can differ in the last ones.  The gradient
  *    computes the logits again, in pieces of the vocabulary, rounds dz to bf16
  *    and accumulates dx and dw in fp32; each is rounded once.  Up to 32 rows two
  *    bf16 numbers hold a dz (off by at most 2^-16 of its value); above, the
  *    target's dz is as exact and the others are off by at most 2^-8 of theirs
- *    (in dx above 64 rows their sum by 2^-8 more).  Repeated calls give the same
- *    bits.
+ *    (in dx above 64 rows their sum by 2^-8 more).
  *  - Non-finite logits follow IEEE rules: a row with a NaN or +inf logit has a
  *    NaN lse; -inf logits count as probability 0, also in a row of nothing else:
  *    its lse is -inf, its loss +inf and its dz -dloss at the target, 0 elsewhere.

@@ -13,10 +13,11 @@ constexpr int kInt8MaxH = 131071;
 
 // Batches of up to kInt8SmallRows rows stream the weight once past all of
 // them (int8_rows_kernel); larger ones run MFMA tiles, and so do more than
-// kInt8FewRows rows on heads of kInt8FewV columns or more: such heads fill the
-// card with tiles without a split of K, which streaming needs (tiles and
-// streaming at B 64, H 4096: V 28672 39 and 46 us, V 50257 64 and 74 us, V 8192
-// 35 and 35 us; H 8192, V 4096 53 and 35 us; at B 32, V 50257 63 and 59 us).
+// kInt8FewRows rows on heads of kInt8FewV columns or more: such heads fill half the
+// card with tiles or more, whatever their lanes, without the split of K that
+// narrower ones need either way (tiles and streaming at B 64, H 4096: V 28672 39
+// and 46 us, V 50257 64 and 74 us, V 8192 35 and 35 us; H 8192, V 4096 53 and 35
+// us; at B 32, V 50257 63 and 59 us).
 constexpr int kInt8SmallRows = 64, kInt8FewRows = 32, kInt8FewV = 16384;
 inline bool int8_few(int32_t B, int32_t V)
 {

@@ -57,8 +57,8 @@ struct LossArgs {
     int32_t first, last;     // the first launch on dxp stores, later ones add
 };
 
-// Batches of up to kLossSmallRows rows stream the weight once past all of them;
-// larger ones run 256 x 256 MFMA tiles.
+// Batches of up to kLossSmallRows rows stream the weight past all of them; larger
+// ones run MFMA tiles of two sizes (small_logits, small_grad).
 constexpr int kLossSmallRows = 64;
 constexpr int kLossStepK = 32;        // K rows per MFMA step
 constexpr int kLossSmallTile = 128;   // columns per workgroup of the streaming kernel
@@ -73,7 +73,10 @@ constexpr int kLossChunk = 1024;      // columns per workgroup that adds slices 
 // rows).  Larger batches would have to gather columns of the weight, a cache line
 // per value (333 rows of H 1111: 50 us of 160); there dX's rows are multiplied by 1 +
 // rest instead, which makes the target's term whole and moves the sum of the others by
-// as much as their own roundings may.  Those stay: 2^-8 of each, independent.
+// as much as their own roundings may.  Those stay: 2^-8 of each, independent.  The
+// results are off by 1.65e-3 of their norm, their own rounding (2.4e-3 without the
+// rests), for 4.8 us of 193 at 333 rows of H 1111, V 50257 and 0.19 ms of 15.2 at 4096
+// of the dense head; two parts everywhere would be two more products.
 constexpr int dz_parts(int B) { return B <= 32 ? 2 : 1; }
 // Whether the logits of nblk blocks, and the gradient's two products, run small
 // tiles (batches of more than kLossSmallRows rows).  Small tiles read each

@@ -5,10 +5,11 @@
 //   dz_bv = (exp(z_bv - lse_b) - [v = t(b)]) g_b  (0 where t(b) < 0)
 //   dX = dz . W^T        dW = X^T . dz
 //
-// The logits exist only in accumulators.  The forward pass reduces each 256 x
-// 256 tile of them to (maximum, sum of exponentials) per row; the backward
-// pass computes them again, piece by piece of the vocabulary, writes the
-// piece's dz in bf16 and multiplies it both ways.
+// The logits are not kept.  The forward pass reduces each tile of them to (maximum,
+// sum of exponentials) per row, in the accumulators or, where few tiles split K,
+// when the slices' fp32 sums are added up; the backward pass computes them again,
+// piece by piece of the vocabulary, writes the piece's dz in bf16 and multiplies
+// it both ways.
 #include "loss.h"
 
 #include <limits.h>
@@ -122,8 +123,9 @@ struct LogitsSrc {
 //
 // Bound by MFMA at the clock that power allows: 2048 rows of the dense head (H
 // 5120, V 151936) take 2.39 ms (1.33 PFLOP/s), the pieces of a 4096-row gradient
-// 1.01 ms each (1.28 PFLOP/s, 256 MB of dz written).  With a short H the ends of
-// a tile count: 257 rows of H 1111, V 50257 take 68 us, 18 stages a tile.
+// 1.02 ms each (1.25 PFLOP/s, 252 MB of dz written).  With a short H the ends of
+// a tile count: 257 rows of H 1111, V 50257 take 67 us, 18 stages a tile, and half
+// the tile rows hold one row.
 template <class C, int USE, bool SPLIT>
 __global__ __launch_bounds__(C::kThreads, C::kPerCu) void logits_kernel(const LossArgs a, const TileGrid grid)
 {
@@ -446,7 +448,7 @@ __global__ __launch_bounds__(kRowsThreads, MB == 4 ? 2 : (MB == 2 ? 3 : 4)) void
         const __amdgpu_buffer_rsrc_t rx =
             buffer_of(reinterpret_cast<const uint8_t *>(a.x) + xat, st < s1 ? xbytes - xat : 0);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)  // non-temporal: each weight byte is read once
+        for (int r = 0; r < 8; ++r)  // non-temporal: the launch reads each weight byte once
             f.w[r] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, wo[r], 0, 2));
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
@@ -755,8 +757,8 @@ struct DwSrc {
 // K (the piece's columns), dW many with a short one (the rows), and each has
 // half the work, so the dX tiles go first and the dW tiles fill the CUs that
 // are left over.  Bound by MFMA: a piece of 4096 rows, H 5120 and 30464 columns
-// takes 1.95 ms (1.31 PFLOP/s; one XCD with a few long dX tiles more than the
-// others made it 2.76).
+// takes 2.0 ms (1.28 PFLOP/s; one XCD with a few long dX tiles more than the
+// others made it 2.76).  The targets' rests (see dz_parts) are 1 to 2 % of it.
 template <class C>
 __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const LossArgs a, const TileGrid gx,
                                                                       const int dx_ids, const TileGrid gw)
@@ -937,7 +939,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu) void grad_kernel(const Loss
 // high part, then (up to 32 rows) of its low part.
 //   dX[b][h] += sum_v W[h][v] dz[b][v]   (k = columns, along both)
 //   dW[h][v]  = sum_b x[b][h] dz[b][v]   (k = dz rows, read across)
-// There it reads and writes 838 MB in 202 us (4.15 TB/s; a copy runs at 4.85).
+// There it reads and writes 838 MB in 200 us (4.2 TB/s; a copy runs at 4.85).
 // ---------------------------------------------------------------------------
 constexpr int kFewH = 64, kFewSlots = 2, kFewStep = 64;
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;

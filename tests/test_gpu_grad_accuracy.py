@@ -60,6 +60,14 @@ def test_target_terms_are_exact(require_gpu, B, H, V, lanes):
         assert torch.equal(one, dx if want == "dx" else dw), want
 
 
+@pytest.mark.parametrize("B,H,V,lanes", [SHAPES[i] for i in (0, 1, 3, 4, 6, 8, 9)])
+def test_logits_far_apart(require_gpu, B, H, V, lanes):
+    """Columns besides the target's hold as much of a row: their terms are off by
+    2^-8 each, and above 64 rows their sum in dx by as much again."""
+    print(f"grad accuracy, far apart B={B} H={H} V={V}", flush=True)
+    check(Case(B, H, V, lanes, seed=B + V, scale=6 / H ** 0.5))
+
+
 @pytest.mark.parametrize("B,H,V,k", [(40, 100, 2003, 5), (70, 264, 2003, 3), (300, 64, 1601, 64)])
 def test_lanes_in_their_own_allocations(require_gpu, B, H, V, k):
     print(f"grad accuracy, separate lanes B={B} V={V} k={k}", flush=True)

@@ -474,6 +474,76 @@ sb_status sb_int8_project_tokens(const sb_int8_desc *desc, int32_t *ids, void *w
 sb_status sb_int8_logits(const sb_int8_desc *desc, void *out, int dtype, int64_t ldo, void *ws,
                          size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Layer norm: the step between a model's rows and the head, and its gradient.
+ *   mean[b] = sum_h x[b][h] / H
+ *   rstd[b] = 1 / sqrt(sum_h (x[b][h] - mean[b])^2 / H + eps)
+ *   xh      = (x - mean) * rstd,   y = xh * weight + bias
+ *   g = dy * weight,  dx = rstd * (g - sum_h g / H - xh * sum_h (g * xh) / H)
+ *   dweight = sum_b dy * xh,   dbias = sum_b dy
+ * Sums are fp32, in orders fixed by B, H and the types; every result is rounded
+ * once to its type.  NaN and infinities follow IEEE rules and stay in their
+ * row (in the parameters' gradients in their column): a row that holds one is
+ * NaN.  A row whose values are all the same has y = bias for eps > 0 (rounding
+ * of the mean aside) and NaN for eps = 0.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ *   B        rows; B == 0 is a valid no-op (it zeroes dweight and dbias)
+ *   H        columns, 1 .. 2^24 (SB_ERR_UNSUPPORTED beyond)
+ *   x        DEVICE [B][ldx], 16-byte aligned
+ *   x_type   sb_dtype of x (anything else: SB_ERR_SHAPE, as for every type)
+ *   ldx      row stride of x, >= H, a multiple of 4 (fp32) or 8 (bf16)
+ *   weight   DEVICE [H], 16-byte aligned, or NULL (1)
+ *   bias     DEVICE [H], 16-byte aligned, or NULL (0)
+ *   param_type  sb_dtype of weight and bias, and of their gradients
+ *   eps      >= 0 and finite (SB_ERR_SHAPE)
+ * Every matrix of these calls spans less than 2^47 bytes (SB_ERR_UNSUPPORTED).
+ */
+typedef struct sb_norm_desc {
+    int32_t B, H;
+    const void *x;
+    int x_type;
+    int64_t ldx;
+    const void *weight, *bias;
+    int param_type;
+    float eps;
+} sb_norm_desc;
+
+/*
+ *   y       DEVICE [B][ldy], 16-byte aligned; ldy >= H, a multiple of 4 (fp32)
+ *           or 8 (bf16); columns past H are left as they were
+ *   y_type  sb_dtype of y; any pair of types of x and y
+ *   mean, rstd  DEVICE fp32 [B] each, or NULL
+ */
+sb_status sb_layer_norm(const sb_norm_desc *desc, void *y, int y_type, int64_t ldy, float *mean,
+                        float *rstd, void *stream);
+
+/*
+ * Bytes of device workspace of sb_layer_norm_grad, for its parameter gradients
+ * (a call without them needs none); 0 for B == 0.  On an invalid descriptor
+ * returns 0 and sets *status (if not NULL).
+ */
+size_t sb_layer_norm_grad_workspace_bytes(const sb_norm_desc *desc, sb_status *status);
+
+/*
+ *   dy       DEVICE [B][lddy], laid out as y, of dy_type (an sb_dtype)
+ *   mean, rstd  DEVICE fp32 [B], as sb_layer_norm returned them
+ *   dx       DEVICE [B][lddx] of x's type, laid out as x, or NULL; columns past
+ *            H are left as they were
+ *   dweight, dbias  DEVICE [H] of param_type, 16-byte aligned, or NULL; also
+ *            where the weight or bias itself is NULL
+ *   ws       >= sb_layer_norm_grad_workspace_bytes(desc), 16-byte aligned;
+ *            only with dweight or dbias
+ * At least one of dx, dweight and dbias is required.  All are overwritten, not
+ * added to.
+ */
+sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_type, int64_t lddy,
+                             const float *mean, const float *rstd, void *dx, int64_t lddx,
+                             void *dweight, void *dbias, void *ws, size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *sb_status_string(sb_status status);
 

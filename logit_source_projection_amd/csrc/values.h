@@ -1,0 +1,138 @@
+// Rows of fp32 or bf16 values as units of eight floats, and sums over a
+// workgroup (gfx950).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace sbk {
+
+// Whether `rows` rows, `ld` elements of `bytes` bytes apart, pass what 47-bit
+// addresses reach.  A quotient: the product of a wild stride passes 64 bits.
+inline bool spans_addresses(int64_t rows, int64_t ld, int64_t bytes)
+{
+    return ld > ((int64_t)1 << 47) / ((rows > 0 ? rows : 1) * bytes);
+}
+
+namespace {
+
+typedef uint32_t raw4 __attribute__((ext_vector_type(4)));
+typedef __bf16 half8 __attribute__((ext_vector_type(8)));
+
+// Element types: float, and uint16_t for the bits of a bf16 number.
+typedef uint16_t bf16_t;
+
+__device__ __forceinline__ float value_of(float v) { return v; }
+__device__ __forceinline__ float value_of(bf16_t bits) { return __uint_as_float((uint32_t)bits << 16); }
+// Rounded to the type (nearest, ties to even).
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16_t *p, float v) { *p = __builtin_bit_cast(bf16_t, (__bf16)v); }
+
+// Eight values as they lie in memory.
+template <typename T>
+struct Unit;
+template <>
+struct Unit<float> {
+    raw4 a, b;
+};
+template <>
+struct Unit<bf16_t> {
+    raw4 a;
+};
+
+__device__ __forceinline__ Unit<float> load_unit(const float *p)
+{
+    return {reinterpret_cast<const raw4 *>(p)[0], reinterpret_cast<const raw4 *>(p)[1]};
+}
+__device__ __forceinline__ Unit<bf16_t> load_unit(const bf16_t *p)
+{
+    return {*reinterpret_cast<const raw4 *>(p)};
+}
+__device__ __forceinline__ void clear(Unit<float> &u) { u.a = u.b = raw4{0u, 0u, 0u, 0u}; }
+__device__ __forceinline__ void clear(Unit<bf16_t> &u) { u.a = raw4{0u, 0u, 0u, 0u}; }
+
+__device__ __forceinline__ void values_of(const Unit<float> &u, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = __uint_as_float(u.a[e]);
+        v[4 + e] = __uint_as_float(u.b[e]);
+    }
+}
+__device__ __forceinline__ void values_of(const Unit<bf16_t> &u, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(u.a[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u.a[e] & 0xFFFF0000u);
+    }
+}
+
+// A unit whose first n values are there; the others are 0 and not read.
+__device__ __forceinline__ Unit<float> load_some(const float *p, int n)
+{
+    if (n >= 8)
+        return load_unit(p);
+    Unit<float> u;
+    clear(u);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            (e < 4 ? u.a : u.b)[e & 3] = __float_as_uint(p[e]);
+    return u;
+}
+__device__ __forceinline__ Unit<bf16_t> load_some(const bf16_t *p, int n)
+{
+    if (n >= 8)
+        return load_unit(p);
+    Unit<bf16_t> u;
+    clear(u);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            u.a[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    return u;
+}
+
+// The first n of eight values, rounded to the type.
+__device__ __forceinline__ void store_some(float *p, const float (&v)[8], int n)
+{
+    if (n >= 8) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        reinterpret_cast<f4 *>(p)[0] = f4{v[0], v[1], v[2], v[3]};
+        reinterpret_cast<f4 *>(p)[1] = f4{v[4], v[5], v[6], v[7]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            p[e] = v[e];
+}
+__device__ __forceinline__ void store_some(bf16_t *p, const float (&v)[8], int n)
+{
+    if (n >= 8) {
+        half8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = (__bf16)v[e];
+        *reinterpret_cast<half8 *>(p) = h;
+        return;
+    }
+    // (each value converted by itself: values taken out of a converted vector came
+    // out as their neighbour)
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            put(p + e, v[e]);
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+}  // namespace
+}  // namespace sbk

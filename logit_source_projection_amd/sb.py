@@ -47,6 +47,7 @@ EXPORTS = ("sb_workspace_bytes", "sb_project_tokens", "sb_project_tokens_static"
            "sb_partial_complete", "sb_cross_entropy_workspace_bytes", "sb_cross_entropy",
            "sb_cross_entropy_grad", "sb_int8_quantize_rows", "sb_int8_quantize_head",
            "sb_int8_workspace_bytes", "sb_int8_project_tokens", "sb_int8_logits",
+           "sb_layer_norm", "sb_layer_norm_grad_workspace_bytes", "sb_layer_norm_grad",
            "sb_status_string")
 
 
@@ -83,6 +84,15 @@ class sb_int8_desc(ctypes.Structure):
         ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p),
         ("w", ctypes.POINTER(ctypes.c_void_p)), ("ldw", ctypes.c_int64),
         ("w_scale", ctypes.POINTER(ctypes.c_void_p)),
+    ]
+
+
+class sb_norm_desc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_type", ctypes.c_int), ("ldx", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("param_type", ctypes.c_int),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -136,6 +146,13 @@ def lib():
     L.sb_int8_project_tokens.argtypes = [PI, vp, vp, sz, vp]
     L.sb_int8_logits.restype = ctypes.c_int
     L.sb_int8_logits.argtypes = [PI, vp, ctypes.c_int, i64, vp, sz, vp]
+    PN = ctypes.POINTER(sb_norm_desc)
+    L.sb_layer_norm.restype = ctypes.c_int
+    L.sb_layer_norm.argtypes = [PN, vp, ctypes.c_int, i64, vp, vp, vp]
+    L.sb_layer_norm_grad_workspace_bytes.restype = sz
+    L.sb_layer_norm_grad_workspace_bytes.argtypes = [PN, ctypes.POINTER(ctypes.c_int)]
+    L.sb_layer_norm_grad.restype = ctypes.c_int
+    L.sb_layer_norm_grad.argtypes = [PN, vp, ctypes.c_int, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp]
     L.sb_status_string.restype = ctypes.c_char_p
     L.sb_status_string.argtypes = [ctypes.c_int]
     _lib = L
@@ -750,6 +767,135 @@ def sb_int8_logits(head, out, ws=None, stream=None):
          lambda: sb_int8_workspace_bytes(head, SB_SURF_FULL_LOGITS), ws,
          lambda p, n, s: lib().sb_int8_logits(head.ref(), _ptr(out), dtype, out.stride(0), p, n, s))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Layer norm.  Like the training surface, these calls run on the device of their
+# tensors; fp32 and bf16 tensors are taken as they are.
+# ---------------------------------------------------------------------------
+_TYPES = {torch.float32: SB_FP32, torch.bfloat16: SB_BF16}
+
+
+def _type_of(t, name):
+    """The sb_dtype code of a device tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, not {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _row_stride(t):
+    """The stride between rows (a single row has none of its own: torch gives any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), _padded(t.shape[1], t.element_size()))
+
+
+def _padded(n, size):
+    """n columns rounded up to whole 16-byte units."""
+    return -(-n * size // 16) * 16 // size
+
+
+class Norm:
+    """Descriptor of a layer norm: rows x [B, H] (fp32 or bf16), and weight and
+    bias [H] of one type (fp32 or bf16; None for 1 and 0).  Raw values can be
+    overridden to exercise the ABI's validation."""
+
+    def __init__(self, x, weight=None, bias=None, eps=1e-5, *, B=None, H=None, x_type=None, ldx=None,
+                 x_ptr=None, weight_ptr=None, bias_ptr=None, param_type=None):
+        self.x, self.weight, self.bias = x, weight, bias
+        self.from_tensors = x_ptr is None
+        self._device = None
+        one = weight if weight is not None else bias
+        self.param_dtype = torch.float32 if one is None else one.dtype
+        self.desc = sb_norm_desc(
+            B=x.shape[0] if B is None else B, H=x.shape[1] if H is None else H,
+            x=x.data_ptr() if x_ptr is None else x_ptr,
+            x_type=_TYPES.get(x.dtype, -1) if x_type is None else x_type,
+            ldx=_row_stride(x) if ldx is None else ldx,
+            weight=weight_ptr if weight is None else weight.data_ptr(),
+            bias=bias_ptr if bias is None else bias.data_ptr(),
+            param_type=_TYPES.get(self.param_dtype, -1) if param_type is None else param_type, eps=eps)
+
+    @property
+    def B(self):
+        return self.desc.B
+
+    @property
+    def H(self):
+        return self.desc.H
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+    def device(self):
+        """The one device of the operands (None for raw pointers).  The
+        descriptor holds their addresses, so they are checked once."""
+        if self._device is None and self.from_tensors:
+            d = self.desc
+            _type_of(self.x, "x")
+            _matrix(self.x, "x", self.x.dtype, d.B, d.H)
+            for t, name in ((self.weight, "weight"), (self.bias, "bias")):
+                if t is not None:
+                    _type_of(t, name)
+                    _vector(t, name, self.param_dtype, d.H)
+            self._device = _one_device([self.x, self.weight, self.bias])
+        return self._device
+
+
+def sb_layer_norm(norm, y, mean=None, rstd=None, stream=None):
+    """y (fp32 or bf16 [B, H]) <- layer norm of the rows; mean and rstd (fp32
+    [B], either optional) are what sb_layer_norm_grad takes.  Returns y."""
+    device = norm.device()
+    B, H = norm.B, norm.H
+    code = _type_of(y, "y")
+    _matrix(y, "y", y.dtype, B, H)
+    _vector(mean, "mean", torch.float32, B)
+    _vector(rstd, "rstd", torch.float32, B)
+    device = _one_device([y, mean, rstd], device)
+    with _on(device):
+        _check(lib().sb_layer_norm(norm.ref(), y.data_ptr(), code, _row_stride(y), _ptr(mean), _ptr(rstd),
+                                   _stream_on(stream, device)), "sb_layer_norm")
+    return y
+
+
+def sb_layer_norm_grad_workspace_bytes(norm):
+    st = ctypes.c_int(0)
+    n = lib().sb_layer_norm_grad_workspace_bytes(norm.ref(), ctypes.byref(st))
+    if st.value != SB_OK:
+        raise SbError(st.value, "sb_layer_norm_grad_workspace_bytes")
+    return int(n)
+
+
+def layer_norm_grad_workspace(norm, device=None):
+    """A workspace for sb_layer_norm_grad (its contents on entry do not matter)."""
+    return torch.empty(max(sb_layer_norm_grad_workspace_bytes(norm), 16), dtype=torch.uint8,
+                       device=norm.x.device if device is None else device)
+
+
+def sb_layer_norm_grad(norm, dy, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+    """dx ([B, H] of x's type), dweight and dbias ([H] of the parameters' type; fp32
+    where there are none) <- the gradient of sum(dy * y), any of them optional.
+    dy (fp32 or bf16 [B, H]) is of any type; mean and rstd are what
+    sb_layer_norm returned.  Returns (dx, dweight, dbias)."""
+    device = norm.device()
+    B, H = norm.B, norm.H
+    code = _type_of(dy, "dy")
+    _matrix(dy, "dy", dy.dtype, B, H)
+    _vector(mean, "mean", torch.float32, B)
+    _vector(rstd, "rstd", torch.float32, B)
+    _matrix(dx, "dx", norm.x.dtype, B, H)
+    _vector(dweight, "dweight", norm.param_dtype, H)
+    _vector(dbias, "dbias", norm.param_dtype, H)
+    _vector(ws, "ws", torch.uint8, 0)
+    device = _one_device([dy, mean, rstd, dx, dweight, dbias, ws], device)
+
+    def call(p, n, s):
+        return lib().sb_layer_norm_grad(norm.ref(), dy.data_ptr(), code, _row_stride(dy), _ptr(mean),
+                                        _ptr(rstd), _ptr(dx), 0 if dx is None else _row_stride(dx),
+                                        _ptr(dweight), _ptr(dbias), p, n, s)
+
+    _run("sb_layer_norm_grad", device, stream, lambda: sb_layer_norm_grad_workspace_bytes(norm), ws, call)
+    return dx, dweight, dbias
 
 
 def to_device_bf16(bits, device="cuda"):

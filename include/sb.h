@@ -544,6 +544,73 @@ sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_ty
                              const float *mean, const float *rstd, void *dx, int64_t lddx,
                              void *dweight, void *dbias, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Embedding: the vocabulary's other table, rows looked up by token IDs and
+ * scaled, and the gradient of that lookup.
+ *   out[b]    = scale * table[ids[b]]
+ *   dtable[v] = scale * sum over b with ids[b] == v of dout[b]
+ *  - A negative ID marks padding: its row of out is 0, and it adds nothing to
+ *    the gradient, whatever its row of dout holds.  An ID >= V makes the row of
+ *    out NaN and adds nothing to the gradient.
+ *  - The gradient's sums are fp32 and run over the positions of an ID in
+ *    ascending order, in runs that depend on the IDs alone: the same call
+ *    repeated gives the same bits.  Each result is rounded once.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ *   V        rows of the table, >= 1
+ *   H        columns; H == 0 is a valid no-op
+ *   k, lane_off  vocabulary lanes, as in sb_head_desc (any offsets)
+ *   w        HOST array of k DEVICE pointers; w[i] is lane i's rows, [V_i][ldw]:
+ *            row j is vocab row off_i + j; 16-byte aligned.  A single [V][ldw]
+ *            allocation is passed as w[i] = base + off_i * ldw.
+ *   ldw      row stride, >= H, a multiple of 4 (fp32) or 8 (bf16)
+ *   type     sb_dtype of the table (anything else: SB_ERR_SHAPE, as for every type)
+ * H <= 2^24 and V <= 2^30, in the gradient V <= 2^24 and B <= 2^24; every matrix
+ * of these calls spans less than 2^47 bytes (SB_ERR_UNSUPPORTED).
+ */
+typedef struct sb_table_desc {
+    int32_t V, H, k;
+    const int32_t *lane_off;
+    void *const *w;
+    int64_t ldw;
+    int type;
+} sb_table_desc;
+
+/*
+ *   ids       DEVICE int32 [B]
+ *   B         rows; B == 0 is a valid no-op
+ *   scale     finite (SB_ERR_SHAPE)
+ *   out       DEVICE [B][ldo], 16-byte aligned; ldo >= H, a multiple of 4 (fp32)
+ *             or 8 (bf16); columns past H are left as they were
+ *   out_type  sb_dtype of out; any pair of types of table and out
+ */
+sb_status sb_embed(const sb_table_desc *desc, const int32_t *ids, int32_t B, float scale, void *out,
+                   int out_type, int64_t ldo, void *stream);
+
+/*
+ * Bytes of device workspace of sb_embed_grad on B rows; 0 where the call does
+ * nothing.  On an invalid descriptor returns 0 and sets *status (if not NULL).
+ */
+size_t sb_embed_grad_workspace_bytes(const sb_table_desc *desc, int32_t B, int accumulate, sb_status *status);
+
+/*
+ *   desc        the gradient's table, laid out as the table; it is written
+ *   ids, B, scale  as in sb_embed
+ *   dout        DEVICE [B][lddo], laid out as out, of dout_type (an sb_dtype)
+ *   accumulate  0: every row of the gradient is overwritten, with zeros where no
+ *               ID names it (B == 0 zeroes all).  Otherwise the sums are added to
+ *               the rows that IDs name and the others are not touched.
+ *   ws          >= sb_embed_grad_workspace_bytes(desc, B, accumulate), 16-byte
+ *               aligned
+ * Columns past H are left as they were.
+ */
+sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B, float scale,
+                        const void *dout, int dout_type, int64_t lddo, int accumulate, void *ws,
+                        size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *sb_status_string(sb_status status);
 

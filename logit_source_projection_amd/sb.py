@@ -48,6 +48,7 @@ EXPORTS = ("sb_workspace_bytes", "sb_project_tokens", "sb_project_tokens_static"
            "sb_cross_entropy_grad", "sb_int8_quantize_rows", "sb_int8_quantize_head",
            "sb_int8_workspace_bytes", "sb_int8_project_tokens", "sb_int8_logits",
            "sb_layer_norm", "sb_layer_norm_grad_workspace_bytes", "sb_layer_norm_grad",
+           "sb_embed", "sb_embed_grad_workspace_bytes", "sb_embed_grad",
            "sb_status_string")
 
 
@@ -93,6 +94,14 @@ class sb_norm_desc(ctypes.Structure):
         ("x", ctypes.c_void_p), ("x_type", ctypes.c_int), ("ldx", ctypes.c_int64),
         ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("param_type", ctypes.c_int),
         ("eps", ctypes.c_float),
+    ]
+
+
+class sb_table_desc(ctypes.Structure):
+    _fields_ = [
+        ("V", ctypes.c_int32), ("H", ctypes.c_int32), ("k", ctypes.c_int32),
+        ("lane_off", ctypes.POINTER(ctypes.c_int32)),
+        ("w", ctypes.POINTER(ctypes.c_void_p)), ("ldw", ctypes.c_int64), ("type", ctypes.c_int),
     ]
 
 
@@ -153,6 +162,13 @@ def lib():
     L.sb_layer_norm_grad_workspace_bytes.argtypes = [PN, ctypes.POINTER(ctypes.c_int)]
     L.sb_layer_norm_grad.restype = ctypes.c_int
     L.sb_layer_norm_grad.argtypes = [PN, vp, ctypes.c_int, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp]
+    PT, f32, cint = ctypes.POINTER(sb_table_desc), ctypes.c_float, ctypes.c_int
+    L.sb_embed.restype = cint
+    L.sb_embed.argtypes = [PT, vp, i32, f32, vp, cint, i64, vp]
+    L.sb_embed_grad_workspace_bytes.restype = sz
+    L.sb_embed_grad_workspace_bytes.argtypes = [PT, i32, cint, ctypes.POINTER(cint)]
+    L.sb_embed_grad.restype = cint
+    L.sb_embed_grad.argtypes = [PT, vp, i32, f32, vp, cint, i64, cint, vp, sz, vp]
     L.sb_status_string.restype = ctypes.c_char_p
     L.sb_status_string.argtypes = [ctypes.c_int]
     _lib = L
@@ -896,6 +912,126 @@ def sb_layer_norm_grad(norm, dy, mean, rstd, dx=None, dweight=None, dbias=None, 
 
     _run("sb_layer_norm_grad", device, stream, lambda: sb_layer_norm_grad_workspace_bytes(norm), ws, call)
     return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# Embedding.
+# ---------------------------------------------------------------------------
+def _count(t, name, dtype):
+    """The elements of a contiguous device buffer, as the C ABI counts them."""
+    _vector(t, name, dtype, 0)
+    if t is None or t.numel() >= 1 << 31:
+        raise ValueError(f"{name} must be a tensor of fewer than 2^31 elements")
+    return t.numel()
+
+
+class Table:
+    """Descriptor of an embedding table, or of its gradient: one [V, H] tensor
+    (fp32 or bf16), or a list of k tensors, lane i of shape [V_i, H] (one type
+    and row stride).  ``lane_off`` holds the k+1 vocab offsets; one lane
+    where it is not given.  Raw values can be overridden to exercise the ABI's
+    validation."""
+
+    def __init__(self, w, lane_off=None, *, V=None, H=None, ldw=None, type=None, w_ptrs=None):
+        self.w = w
+        self.from_tensors = w_ptrs is None
+        self._device = None
+        one = _as_list(w)[0]
+        if lane_off is None:
+            lane_off = [0]
+            for t in _as_list(w):
+                lane_off.append(lane_off[-1] + t.shape[0])
+        off = [int(o) for o in lane_off]
+        self.lane_off = off
+        k = len(off) - 1
+        self._off = (ctypes.c_int32 * max(1, k + 1))(*off)
+        stride = _row_stride(one)
+        if w_ptrs is not None:
+            ptrs = list(w_ptrs)
+        elif isinstance(w, (list, tuple)):
+            if len(w) != k:
+                raise ValueError(f"w must hold one tensor per lane, {k}")
+            ptrs = [t.data_ptr() for t in w]
+            stride = max([t.stride(0) for t in w if t.shape[0] > 1] or [stride])
+        else:
+            ptrs = [w.data_ptr() + w.element_size() * stride * o for o in off[:-1]]
+        self._w = (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
+        self.desc = sb_table_desc(
+            V=off[-1] if V is None else V, H=one.shape[1] if H is None else H, k=k, lane_off=self._off,
+            w=self._w, ldw=stride if ldw is None else ldw,
+            type=_TYPES.get(one.dtype, -1) if type is None else type)
+
+    @property
+    def V(self):
+        return self.desc.V
+
+    @property
+    def H(self):
+        return self.desc.H
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+    def device(self):
+        """The one device of the table (None for raw pointers).  The descriptor
+        holds its addresses, so it is checked once."""
+        if self._device is None and self.from_tensors:
+            d, off, w = self.desc, self.lane_off, _as_list(self.w)
+            _type_of(w[0], "w")
+            if isinstance(self.w, (list, tuple)):
+                for i, t in enumerate(w):
+                    _matrix(t, f"w[{i}]", w[0].dtype, off[i + 1] - off[i], d.H)
+                if len({t.stride(0) for t in w if t.shape[0] > 1}) > 1:
+                    raise ValueError("the tensors of w must have one row stride")
+            else:
+                _matrix(self.w, "w", self.w.dtype, d.V, d.H)
+            self._device = _one_device(w)
+        return self._device
+
+
+def sb_embed(table, ids, out, scale=1.0, stream=None):
+    """out (fp32 or bf16 [B, H]) <- scale times the table's rows that ids (int32
+    [B]) name; zeros for a negative ID, NaN for one past the table.  Returns out."""
+    device = table.device()
+    B = _count(ids, "ids", torch.int32)
+    code = _type_of(out, "out")
+    _matrix(out, "out", out.dtype, B, table.H)
+    device = _one_device([ids, out], device)
+    with _on(device):
+        _check(lib().sb_embed(table.ref(), ids.data_ptr(), B, scale, out.data_ptr(), code, _row_stride(out),
+                              _stream_on(stream, device)), "sb_embed")
+    return out
+
+
+def sb_embed_grad_workspace_bytes(table, B, accumulate=False):
+    st = ctypes.c_int(0)
+    n = lib().sb_embed_grad_workspace_bytes(table.ref(), B, int(bool(accumulate)), ctypes.byref(st))
+    if st.value != SB_OK:
+        raise SbError(st.value, "sb_embed_grad_workspace_bytes")
+    return int(n)
+
+
+def embed_grad_workspace(table, B, accumulate=False, device=None):
+    """A workspace for sb_embed_grad on B rows (its contents on entry do not matter)."""
+    return torch.empty(max(sb_embed_grad_workspace_bytes(table, B, accumulate), 16), dtype=torch.uint8,
+                       device=_as_list(table.w)[0].device if device is None else device)
+
+
+def sb_embed_grad(table, ids, dout, scale=1.0, accumulate=False, ws=None, stream=None):
+    """The gradient of sum(dout * sb_embed(...)): written to the tensors of `table`
+    (a Table of the gradient), all of whose rows are overwritten; with
+    accumulate it is added to the rows that ids name.  dout (fp32 or bf16 [B, H])
+    is of any type.  Returns the table's tensor or tensors."""
+    device = table.device()
+    B = _count(ids, "ids", torch.int32)
+    code = _type_of(dout, "dout")
+    _matrix(dout, "dout", dout.dtype, B, table.H)
+    _vector(ws, "ws", torch.uint8, 0)
+    device = _one_device([ids, dout, ws], device)
+    _run("sb_embed_grad", device, stream, lambda: sb_embed_grad_workspace_bytes(table, B, accumulate), ws,
+         lambda p, n, s: lib().sb_embed_grad(table.ref(), ids.data_ptr(), B, scale, dout.data_ptr(), code,
+                                             _row_stride(dout), int(bool(accumulate)), p, n, s))
+    return table.w
 
 
 def to_device_bf16(bits, device="cuda"):

@@ -611,6 +611,88 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
                         const void *dout, int dout_type, int64_t lddo, int accumulate, void *ws,
                         size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Verification of drafted tokens: a draft model (or a lookup) proposes tokens
+ * for a sequence, the head computes the logits of all their positions in one
+ * batch, and given random numbers decide how many of them the target keeps.
+ * For sequence i with n drafts x_0 .. x_(n-1), target logits z_0 .. z_n, draft
+ * logits y_0 .. y_(n-1) and temperature t > 0:
+ *   p_j = softmax(z_j / t),  q_j = softmax(y_j / t)
+ *   draft j is accepted if every one before it is and u_j * q_j(x_j) < p_j(x_j)
+ *   the next token is drawn from max(p_j - q_j, 0) of the first rejected draft
+ *   j, or from p_n if all are accepted: the lowest column whose cumulative sum
+ *   passes u_next times the whole
+ * Accepted drafts and next token then follow the target's distribution exactly.
+ *  - Without draft logits a draft counts as certain: q_j(x_j) = 1.
+ *  - Where max(p_j - q_j, 0) is 0 everywhere the token is drawn from p_j.
+ *  - A temperature that is not > 0 (0, negative, NaN) is greedy: draft j is
+ *    accepted if it is the argmax of z_j, and the next token is the argmax (the
+ *    projection calls' order: NaN above every number, the lowest index among
+ *    equals).  Draft logits and random numbers are not used.
+ *  - A logit of -inf is a token that cannot be drawn.  A row that holds a NaN or
+ *    +inf logit, or nothing but -inf, has no distribution: as p_j its draft is
+ *    rejected and the next token is -1; as q_j its draft is rejected and the
+ *    next token is drawn from p_j.
+ *  - A drafted token outside 0 .. V - 1 is rejected (without draft logits the
+ *    next token is then drawn from p_j).  u_j of 0 accepts any draft with
+ *    p_j(x_j) > 0, NaN none; u_next below 0 or NaN counts as 0, and from 1 up
+ *    it draws the last token that can be drawn.
+ *  - Everything behind the logits is computed in 64 bits, in an order fixed by
+ *    V alone: the same logits and numbers give the same tokens in any batch.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ *   N        sequences; N == 0 is a valid no-op
+ *   K        the most drafts of a sequence, >= 0 (0: every call draws one token
+ *            per sequence)
+ *   V        vocabulary size, 1 .. 2^30 (SB_ERR_UNSUPPORTED beyond)
+ *   drafts   drafted tokens of all sequences together
+ *   offsets  DEVICE int32 [N + 1]: sequence i's drafts are offsets[i] ..
+ *            offsets[i + 1] - 1.  Drafts past the K-th of a sequence are ignored.
+ *            Offsets outside 0 .. drafts or falling ones are taken as the nearest
+ *            that fit: never read out of range.
+ *   tokens   DEVICE int32 [drafts]
+ *   target   DEVICE [drafts + N][ldt] logits, 16-byte aligned: sequence i's rows
+ *            are offsets[i] + i .. offsets[i + 1] + i, one for each draft and one
+ *            behind the last
+ *   ldt      row stride, >= V, a multiple of 4 (fp32) or 8 (bf16)
+ *   draft    DEVICE [drafts][ldd] logits, laid out as target, or NULL
+ *   type     sb_dtype of target and draft (anything else: SB_ERR_SHAPE)
+ *   temperature  DEVICE fp32 [N], or NULL (1)
+ * N * (2 K + 1) * ceil(V / 8192) is below 2^24, and every matrix spans less than
+ * 2^47 bytes (SB_ERR_UNSUPPORTED).
+ */
+typedef struct sb_drafts_desc {
+    int32_t N, K, V, drafts;
+    const int32_t *offsets;
+    const int32_t *tokens;
+    const void *target;
+    int64_t ldt;
+    const void *draft;
+    int64_t ldd;
+    int type;
+    const float *temperature;
+} sb_drafts_desc;
+
+/*
+ * Bytes of device workspace of sb_verify_drafts; 0 for N == 0.  On an invalid
+ * descriptor returns 0 and sets *status (if not NULL).
+ */
+size_t sb_verify_workspace_bytes(const sb_drafts_desc *desc, sb_status *status);
+
+/*
+ *   u         DEVICE fp32 [drafts], numbers drawn from [0, 1)
+ *   u_next    DEVICE fp32 [N], numbers drawn from [0, 1)
+ *   out       DEVICE int32 [N][ldo], ldo >= K + 1: the accepted drafts, the next
+ *             token, then -1 up to column K; columns past K are left as they were
+ *   accepted  DEVICE int32 [N]: how many drafts are accepted
+ *   ws        >= sb_verify_workspace_bytes(desc), 16-byte aligned
+ */
+sb_status sb_verify_drafts(const sb_drafts_desc *desc, const float *u, const float *u_next, int32_t *out,
+                           int64_t ldo, int32_t *accepted, void *ws, size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *sb_status_string(sb_status status);
 

@@ -8,7 +8,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsb.so")
 SOURCES = ["kernels.hip", "sb_api.cpp", "loss.hip", "sb_loss.cpp", "int8.hip",
            "sb_int8.cpp", "norm.hip", "sb_norm.cpp", "embed.hip",
-           "sb_embed.cpp"]
+           "sb_embed.cpp", "verify.hip", "sb_verify.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

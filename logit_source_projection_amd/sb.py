@@ -49,7 +49,7 @@ EXPORTS = ("sb_workspace_bytes", "sb_project_tokens", "sb_project_tokens_static"
            "sb_int8_workspace_bytes", "sb_int8_project_tokens", "sb_int8_logits",
            "sb_layer_norm", "sb_layer_norm_grad_workspace_bytes", "sb_layer_norm_grad",
            "sb_embed", "sb_embed_grad_workspace_bytes", "sb_embed_grad",
-           "sb_status_string")
+           "sb_verify_workspace_bytes", "sb_verify_drafts", "sb_status_string")
 
 
 class SbError(RuntimeError):
@@ -102,6 +102,16 @@ class sb_table_desc(ctypes.Structure):
         ("V", ctypes.c_int32), ("H", ctypes.c_int32), ("k", ctypes.c_int32),
         ("lane_off", ctypes.POINTER(ctypes.c_int32)),
         ("w", ctypes.POINTER(ctypes.c_void_p)), ("ldw", ctypes.c_int64), ("type", ctypes.c_int),
+    ]
+
+
+class sb_drafts_desc(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("drafts", ctypes.c_int32),
+        ("offsets", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+        ("target", ctypes.c_void_p), ("ldt", ctypes.c_int64),
+        ("draft", ctypes.c_void_p), ("ldd", ctypes.c_int64), ("type", ctypes.c_int),
+        ("temperature", ctypes.c_void_p),
     ]
 
 
@@ -169,6 +179,11 @@ def lib():
     L.sb_embed_grad_workspace_bytes.argtypes = [PT, i32, cint, ctypes.POINTER(cint)]
     L.sb_embed_grad.restype = cint
     L.sb_embed_grad.argtypes = [PT, vp, i32, f32, vp, cint, i64, cint, vp, sz, vp]
+    PD = ctypes.POINTER(sb_drafts_desc)
+    L.sb_verify_workspace_bytes.restype = sz
+    L.sb_verify_workspace_bytes.argtypes = [PD, ctypes.POINTER(cint)]
+    L.sb_verify_drafts.restype = cint
+    L.sb_verify_drafts.argtypes = [PD, vp, vp, vp, i64, vp, vp, sz, vp]
     L.sb_status_string.restype = ctypes.c_char_p
     L.sb_status_string.argtypes = [ctypes.c_int]
     _lib = L
@@ -1032,6 +1047,94 @@ def sb_embed_grad(table, ids, dout, scale=1.0, accumulate=False, ws=None, stream
          lambda p, n, s: lib().sb_embed_grad(table.ref(), ids.data_ptr(), B, scale, dout.data_ptr(), code,
                                              _row_stride(dout), int(bool(accumulate)), p, n, s))
     return table.w
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens.
+# ---------------------------------------------------------------------------
+class Drafts:
+    """Descriptor of N sequences' drafted tokens: tokens (int32, all sequences'
+    one after another), offsets (int32 [N + 1], on the device: sequence i has
+    tokens[offsets[i]:offsets[i + 1]], at most max_drafts of them), the target's
+    logits [len(tokens) + N, V] (fp32 or bf16; a sequence's rows are those of its
+    drafts and one behind the last), and optionally the draft model's logits
+    [len(tokens), V] of the same type and temperatures (fp32 [N]; 1 where there
+    are none)."""
+
+    def __init__(self, target, tokens, offsets, max_drafts, draft=None, temperature=None):
+        self.target, self.tokens, self.offsets = target, tokens, offsets
+        self.draft, self.temperature = draft, temperature
+        self._device = None
+        self.desc = sb_drafts_desc(
+            N=max(0, offsets.numel() - 1), K=int(max_drafts), V=target.shape[1], drafts=tokens.numel(),
+            offsets=offsets.data_ptr(), tokens=tokens.data_ptr(), target=target.data_ptr(),
+            ldt=_row_stride(target), draft=None if draft is None else draft.data_ptr(),
+            ldd=0 if draft is None else _row_stride(draft), type=_TYPES.get(target.dtype, -1),
+            temperature=None if temperature is None else temperature.data_ptr())
+
+    @property
+    def N(self):
+        return self.desc.N
+
+    @property
+    def K(self):
+        return self.desc.K
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+    def device(self):
+        """The one device of the operands.  The descriptor holds their addresses,
+        so they are checked once."""
+        if self._device is None:
+            d = self.desc
+            _type_of(self.target, "target")
+            drafts = _count(self.tokens, "tokens", torch.int32)
+            if _count(self.offsets, "offsets", torch.int32) < 1:
+                raise ValueError("offsets must hold one number more than there are sequences")
+            _matrix(self.target, "target", self.target.dtype, drafts + d.N, d.V)
+            _matrix(self.draft, "draft", self.target.dtype, drafts, d.V)
+            _vector(self.temperature, "temperature", torch.float32, d.N)
+            # (no drafts: torch gives an empty tensor no address)
+            if self.draft is not None and drafts == 0:
+                d.draft = None
+            self._device = _one_device([self.target, self.tokens, self.offsets, self.draft, self.temperature])
+        return self._device
+
+
+def sb_verify_workspace_bytes(drafts):
+    st = ctypes.c_int(0)
+    n = lib().sb_verify_workspace_bytes(drafts.ref(), ctypes.byref(st))
+    if st.value != SB_OK:
+        raise SbError(st.value, "sb_verify_workspace_bytes")
+    return int(n)
+
+
+def verify_workspace(drafts, device=None):
+    """A workspace for sb_verify_drafts (its contents on entry do not matter)."""
+    return torch.empty(max(sb_verify_workspace_bytes(drafts), 16), dtype=torch.uint8,
+                       device=drafts.target.device if device is None else device)
+
+
+def sb_verify_drafts(drafts, u, u_next, out, accepted, ws=None, stream=None):
+    """out (int32 [N, max_drafts + 1]) <- every sequence's accepted drafts, the
+    token behind them, and -1 up to the end; accepted (int32 [N]) <- how many
+    are accepted.  u (fp32, one per drafted token) and u_next (fp32 [N]) are
+    random numbers from [0, 1).  Returns (out, accepted)."""
+    device = drafts.device()
+    N, K = drafts.N, drafts.K
+    _vector(u, "u", torch.float32, drafts.desc.drafts)
+    _vector(u_next, "u_next", torch.float32, N)
+    _matrix(out, "out", torch.int32, N, K + 1)
+    _vector(accepted, "accepted", torch.int32, N)
+    _vector(ws, "ws", torch.uint8, 0)
+    device = _one_device([u, u_next, out, accepted, ws], device)
+    ldo = 0 if out is None else out.stride(0) if out.shape[0] > 1 else out.shape[1]
+    _run("sb_verify_drafts", device, stream, lambda: sb_verify_workspace_bytes(drafts), ws,
+         lambda p, n, s: lib().sb_verify_drafts(drafts.ref(), _ptr(u), _ptr(u_next), _ptr(out),
+                                                ldo,
+                                                _ptr(accepted), p, n, s))
+    return out, accepted
 
 
 def to_device_bf16(bits, device="cuda"):

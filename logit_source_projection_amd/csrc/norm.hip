@@ -7,6 +7,12 @@
 //
 // Sums are fp32; the variance is that of the differences from the mean, not a
 // difference of two large sums.  y, dx, dw and db are rounded once.
+//
+// Both are bound by the bytes of their rows, so a row is read once: the team of
+// lanes that has it keeps it in registers (UNITS units of 8 values per lane)
+// across its sums, with the next row's loads already under way.  A team is 8 to 64
+// lanes of a wave for rows that fit (no barrier), else a workgroup of as many
+// waves as the row needs.  Longer rows (kMostUnits) are read again for every sum.
 #include "norm.h"
 
 #include <algorithm>
@@ -18,22 +24,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int64_t kMostRows = 1 << 20;  // workgroups that rows are dealt to
-
-// The sum over the workgroup; every thread has it.  `scratch` holds a float per
-// wave and is free again after the next barrier.
-__device__ __forceinline__ float group_sum(float v, float *scratch)
-{
-    v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0)
-        scratch[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = scratch[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w)
-        v += scratch[w];
-    return v;
-}
+constexpr int kMostWaves = 16;              // of a team
+constexpr int64_t kMostRows = 1 << 20;      // workgroups that rows are dealt to
+constexpr int kCus = 256;
 
 // Values c .. of a parameter, `other` where there is none.
 __device__ __forceinline__ void load_param(const void *p, bool bf16, int c, int n, float other, float (&v)[8])
@@ -50,10 +43,281 @@ __device__ __forceinline__ void load_param(const void *p, bool bf16, int c, int 
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup per row, reading it once per sum.
+// Teams.  TEAM lanes of a wave, or with TEAM 0 the whole workgroup.
 // ---------------------------------------------------------------------------
+template <int TEAM, int UNITS>
+struct Team {
+    int at, lanes;   // this lane in its team, and the team's lanes
+    int64_t row;     // the team's first row and the distance to its next
+    int64_t step;
+    __device__ __forceinline__ Team()
+    {
+        if (TEAM == 0) {
+            at = threadIdx.x;
+            lanes = blockDim.x;
+            row = blockIdx.x;
+            step = gridDim.x;
+        } else {
+            constexpr int kTeams = kThreads / (TEAM ? TEAM : 1);
+            at = threadIdx.x & (TEAM - 1);
+            lanes = TEAM;
+            row = (int64_t)blockIdx.x * kTeams + threadIdx.x / (TEAM ? TEAM : 1);
+            step = (int64_t)gridDim.x * kTeams;
+        }
+    }
+    __device__ __forceinline__ int column(int k) const { return 8 * (k * lanes + at); }
+    // The sum over the team.  With TEAM 0 `scratch` holds a float per wave, and is free
+    // again behind the team's next barrier.
+    __device__ __forceinline__ float sum(float v, float *scratch) const
+    {
+        v = lanes_sum<TEAM ? TEAM : 64>(v);
+        if (TEAM == 0) {
+            if ((threadIdx.x & 63) == 0)
+                scratch[threadIdx.x >> 6] = v;
+            __syncthreads();
+            v = scratch[0];
+            for (int w = 1; w < (int)blockDim.x / 64; ++w)
+                v += scratch[w];
+        }
+        return v;
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, int H, Unit<T> (&v)[UNITS]) const
+    {
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const int c = column(k);
+            if (c < H)
+                v[k] = load_some(row + c, H - c);
+            else
+                clear(v[k]);
+        }
+    }
+};
+
+template <typename TX, typename TY, int TEAM, int UNITS, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_kernel(const NormArgs a)
+{
+    __shared__ float scratch[2][kMostWaves];
+    const Team<TEAM, UNITS> team;
+    const int H = a.H;
+    float w[UNITS][8], s[UNITS][8];
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+        const int c = team.column(k);
+        load_param(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
+        load_param(a.bias, a.params_bf16, c, H - c, 0.f, s[k]);
+    }
+    Unit<TX> next[UNITS];
+    if (team.row < a.B)
+        team.load(static_cast<const TX *>(a.x) + team.row * a.ldx, H, next);
+    for (int64_t b = team.row; b < a.B; b += team.step) {
+        float v[UNITS][8], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            values_of(next[k], v[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += v[k][e];
+        }
+        if (b + team.step < a.B)
+            team.load(static_cast<const TX *>(a.x) + (b + team.step) * a.ldx, H, next);
+        const float mean = team.sum(sum, scratch[0]) / H;
+        float squares = 0.f;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[k][e] -= mean;
+                squares += team.column(k) + e < H ? v[k][e] * v[k][e] : 0.f;
+            }
+        const float rstd = 1.f / sqrtf(team.sum(squares, scratch[1]) / H + a.eps);
+        if (team.at == 0) {
+            if (a.mean)
+                a.mean[b] = mean;
+            if (a.rstd)
+                a.rstd[b] = rstd;
+        }
+        TY *y = static_cast<TY *>(a.y) + b * a.ldy;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const int c = team.column(k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[k][e] = v[k][e] * rstd * w[k][e] + s[k][e];
+            if (c < H)
+                store_some(y + c, v[k], H - c);
+        }
+    }
+}
+
+// dx, and the parameters' sums over the rows of the workgroup.
+template <typename TX, typename TY, int TEAM, int UNITS, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
+{
+    __shared__ float scratch[2][2][kMostWaves];
+    const Team<TEAM, UNITS> team;
+    const int H = a.H;
+    float w[UNITS][8], dw[UNITS][8], db[UNITS][8];
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+        const int c = team.column(k);
+        load_param(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            dw[k][e] = db[k][e] = 0.f;
+    }
+    // (teams of more than 8 waves have no registers left for the next row)
+    constexpr bool kAhead = THREADS <= 512;
+    Unit<TX> nx[UNITS];
+    Unit<TY> ng[UNITS];
+    float nmean = 0.f, nrstd = 0.f;
+    if (kAhead && team.row < a.B) {
+        team.load(static_cast<const TX *>(a.x) + team.row * a.ldx, H, nx);
+        team.load(static_cast<const TY *>(a.dy) + team.row * a.lddy, H, ng);
+        nmean = a.mean_in[team.row];
+        nrstd = a.rstd_in[team.row];
+    }
+    int parity = 0;
+    for (int64_t b = team.row; b < a.B; b += team.step, parity ^= 1) {
+        Unit<TX> x[UNITS];
+        Unit<TY> g[UNITS];
+        if (!kAhead) {
+            team.load(static_cast<const TX *>(a.x) + b * a.ldx, H, x);
+            team.load(static_cast<const TY *>(a.dy) + b * a.lddy, H, g);
+            nmean = a.mean_in[b];
+            nrstd = a.rstd_in[b];
+        } else {
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                x[k] = nx[k];
+                g[k] = ng[k];
+            }
+        }
+        const float mean = nmean, rstd = nrstd;
+        if (kAhead && b + team.step < a.B) {
+            team.load(static_cast<const TX *>(a.x) + (b + team.step) * a.ldx, H, nx);
+            team.load(static_cast<const TY *>(a.dy) + (b + team.step) * a.lddy, H, ng);
+            nmean = a.mean_in[b + team.step];
+            nrstd = a.rstd_in[b + team.step];
+        }
+        float sum = 0.f, cross = 0.f;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            float xv[8], gv[8];
+            values_of(x[k], xv);
+            values_of(g[k], gv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (xv[e] - mean) * rstd;
+                dw[k][e] += gv[e] * xh;
+                db[k][e] += gv[e];
+                sum += gv[e] * w[k][e];
+                cross += gv[e] * w[k][e] * xh;
+            }
+        }
+        if (!a.dx)
+            continue;
+        float m, c2;
+        if (TEAM == 0) {
+            // one barrier a row: the rows' scratch alternates
+            sum = wave_sum(sum);
+            cross = wave_sum(cross);
+            if ((threadIdx.x & 63) == 0) {
+                scratch[parity][0][threadIdx.x >> 6] = sum;
+                scratch[parity][1][threadIdx.x >> 6] = cross;
+            }
+            __syncthreads();
+            m = scratch[parity][0][0];
+            c2 = scratch[parity][1][0];
+            for (int i = 1; i < (int)blockDim.x / 64; ++i) {
+                m += scratch[parity][0][i];
+                c2 += scratch[parity][1][i];
+            }
+        } else {
+            m = lanes_sum<TEAM ? TEAM : 64>(sum);
+            c2 = lanes_sum<TEAM ? TEAM : 64>(cross);
+        }
+        m /= H;
+        c2 /= H;
+        TX *dx = static_cast<TX *>(a.dx) + b * a.lddx;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k) {
+            const int c = team.column(k);
+            float xv[8], gv[8];
+            values_of(x[k], xv);
+            values_of(g[k], gv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                xv[e] = rstd * (gv[e] * w[k][e] - m - (xv[e] - mean) * rstd * c2);
+            if (c < H)
+                store_some(dx + c, xv, H - c);
+        }
+    }
+    if (!a.part)
+        return;
+    if (TEAM != 0) {
+        // the workgroup's teams: those of a wave, then the waves in order
+        __shared__ float joined[kWaves][2][TEAM ? 8 * TEAM * UNITS : 1];
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int k = 0; k < UNITS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int d = TEAM; d < 64; d <<= 1) {
+                    dw[k][e] += __shfl_xor(dw[k][e], d);
+                    db[k][e] += __shfl_xor(db[k][e], d);
+                }
+        if ((threadIdx.x & 63) < TEAM)
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                store_some(&joined[wave][0][team.column(k)], dw[k], 8);
+                store_some(&joined[wave][1][team.column(k)], db[k], 8);
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * 8 * TEAM * UNITS; i += kThreads) {
+            const int which = i / (8 * TEAM * UNITS), c = i % (8 * TEAM * UNITS);
+            float v = joined[0][which][c];
+#pragma unroll
+            for (int u = 1; u < kWaves; ++u)
+                v += joined[u][which][c];
+            if (c < a.ldpart)
+                a.part[((int64_t)blockIdx.x * 2 + which) * a.ldpart + c] = v;
+        }
+        return;
+    }
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.ldpart;
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+        const int c = team.column(k);
+        if (c < H) {
+            store_some(part + c, dw[k], 8);
+            store_some(part + a.ldpart + c, db[k], 8);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows that no team holds: one workgroup per row, reading it once per sum.
+// ---------------------------------------------------------------------------
+// The sum over the workgroup; every thread has it.  `scratch` holds a float per
+// wave and is free again after the next barrier.
+__device__ __forceinline__ float group_sum(float v, float *scratch)
+{
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0)
+        scratch[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = scratch[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+        v += scratch[w];
+    return v;
+}
+
 template <typename TX, typename TY>
-__global__ __launch_bounds__(kThreads) void norm_rows_kernel(const NormArgs a)
+__global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a)
 {
     __shared__ float scratch[2][kWaves];
     const int H = a.H, units = (H + 7) / 8;
@@ -161,43 +425,137 @@ __global__ __launch_bounds__(kThreads) void norm_grad_columns_kernel(const NormA
     store_some(part + a.ldpart, db, 8);
 }
 
-// dw and db: the runs' sums added in order.
+// ---------------------------------------------------------------------------
+// dw and db: the runs' sums added in order.  A workgroup has kJoinColumns columns of
+// one of them; each of its kJoinRuns groups of threads adds an equal share of the
+// runs in order, and the shares are added in order.
+// ---------------------------------------------------------------------------
+constexpr int kJoinColumns = 64, kJoinQuads = kJoinColumns / 4, kJoinRuns = kThreads / kJoinQuads;
+
 __global__ __launch_bounds__(kThreads) void norm_params_kernel(const NormArgs a)
 {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= a.H)
+    __shared__ float shares[kJoinRuns][kJoinColumns];
+    const bool bias = blockIdx.y != 0;
+    void *to = bias ? a.dbias : a.dweight;
+    if (!to)
         return;
-    float dw = 0.f, db = 0.f;
-    for (int p = 0; p < a.parts; ++p) {
-        dw += a.part[(int64_t)2 * p * a.ldpart + c];
-        db += a.part[((int64_t)2 * p + 1) * a.ldpart + c];
+    const int quad = threadIdx.x % kJoinQuads, share = threadIdx.x / kJoinQuads;
+    const int c = blockIdx.x * kJoinColumns + 4 * quad;
+    const int each = (a.parts + kJoinRuns - 1) / kJoinRuns, last = min(a.parts, (share + 1) * each);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.H) {
+        const float *part = a.part + bias * a.ldpart + c;
+#pragma unroll 8
+        for (int p = share * each; p < last; ++p) {
+            const float4 o = *reinterpret_cast<const float4 *>(part + (int64_t)2 * p * a.ldpart);
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+        }
     }
-    if (a.dweight)
-        a.params_bf16 ? put(static_cast<bf16_t *>(a.dweight) + c, dw) : put(static_cast<float *>(a.dweight) + c, dw);
-    if (a.dbias)
-        a.params_bf16 ? put(static_cast<bf16_t *>(a.dbias) + c, db) : put(static_cast<float *>(a.dbias) + c, db);
+    *reinterpret_cast<float4 *>(&shares[share][4 * quad]) = v;
+    __syncthreads();
+    const int at = blockIdx.x * kJoinColumns + threadIdx.x;
+    if (threadIdx.x >= kJoinColumns || at >= a.H)
+        return;
+    float sum = shares[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kJoinRuns; ++i)
+        sum += shares[i][threadIdx.x];
+    if (a.params_bf16)
+        put(static_cast<bf16_t *>(to) + at, sum);
+    else
+        put(static_cast<float *>(to) + at, sum);
 }
+
+// ---------------------------------------------------------------------------
+// Launches.
+// ---------------------------------------------------------------------------
+struct Shape {
+    int team, units, threads, teams;  // teams per workgroup
+};
+
+constexpr int kMostUnits = 64 * kMostWaves * 2;  // of a row that a team holds
+
+Shape shape_of(int H)
+{
+    const int units = (H + 7) / 8;
+    for (int team = 8; team <= 64; team <<= 1)
+        if (units <= team)
+            return {team, 1, kThreads, kThreads / team};
+    if (units <= 128)
+        return {64, 2, kThreads, kWaves};
+    return {0, 2, (units + 127) / 128 * 64, 1};
+}
+
+// Workgroups that rows are dealt to: as many as put `waves` waves on every CU (one
+// workgroup on each at least).  The loads of the next row are under way while one is
+// summed, so few waves suffice and more only add ends: forward of 8192 rows of H 5120
+// in bf16 31 us with 16 waves per CU, 36 with 32, 57 with 8; gradient 59 us with 8,
+// 63 with 10, 68 with 16 (each workgroup leaves a row of partial sums).
+constexpr int kForwardWaves = 16, kGradWaves = 8;
+
+int groups_of(const Shape &t, int64_t B, int waves)
+{
+    const int64_t all = (B + t.teams - 1) / t.teams;
+    const int64_t resident = kCus * (int64_t)std::max(1, waves * 64 / t.threads);
+    return (int)std::min(all, resident);
+}
+
+// RUN(team, units, most threads) of the shape t.
+#define SHAPES \
+    if (t.team == 8) \
+        RUN(8, 1, kThreads); \
+    else if (t.team == 16) \
+        RUN(16, 1, kThreads); \
+    else if (t.team == 32) \
+        RUN(32, 1, kThreads); \
+    else if (t.team == 64 && t.units == 1) \
+        RUN(64, 1, kThreads); \
+    else if (t.team == 64) \
+        RUN(64, 2, kThreads); \
+    else if (t.threads <= 512) \
+        RUN(0, 2, 512); \
+    else \
+        RUN(0, 2, 64 * kMostWaves);
 
 template <typename TX, typename TY>
 hipError_t forward(const NormArgs &a, hipStream_t s)
 {
-    const unsigned rows = (unsigned)std::min<int64_t>(a.B, kMostRows);
-    hipLaunchKernelGGL((norm_rows_kernel<TX, TY>), dim3(rows), dim3(kThreads), 0, s, a);
+    if ((a.H + 7) / 8 > kMostUnits) {
+        hipLaunchKernelGGL((norm_long_kernel<TX, TY>), dim3((unsigned)std::min<int64_t>(a.B, kMostRows)), dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    const Shape t = shape_of(a.H);
+    const dim3 grid((unsigned)groups_of(t, a.B, kForwardWaves)), threads(t.threads);
+#define RUN(TEAM, UNITS, MOST) hipLaunchKernelGGL((norm_kernel<TX, TY, TEAM, UNITS, MOST>), grid, threads, 0, s, a)
+    SHAPES
+#undef RUN
     return hipGetLastError();
 }
 
 template <typename TX, typename TY>
 hipError_t gradient(const NormArgs &a, hipStream_t s)
 {
+    if ((a.H + 7) / 8 <= kMostUnits) {
+        const Shape t = shape_of(a.H);
+        const dim3 grid((unsigned)norm_parts(a.B, a.H)), threads(t.threads);
+#define RUN(TEAM, UNITS, MOST) \
+    hipLaunchKernelGGL((norm_grad_kernel<TX, TY, TEAM, UNITS, MOST>), grid, threads, 0, s, a)
+        SHAPES
+#undef RUN
+        return hipGetLastError();
+    }
     if (a.dx) {
-        const unsigned rows = (unsigned)std::min<int64_t>(a.B, kMostRows);
-        hipLaunchKernelGGL((norm_grad_rows_kernel<TX, TY>), dim3(rows), dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((norm_grad_rows_kernel<TX, TY>), dim3((unsigned)std::min<int64_t>(a.B, kMostRows)), dim3(kThreads), 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !a.part)
             return e;
     }
     const unsigned chunks = (unsigned)(((a.H + 7) / 8 + kThreads - 1) / kThreads);
-    hipLaunchKernelGGL((norm_grad_columns_kernel<TX, TY>), dim3(chunks, (unsigned)a.parts), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((norm_grad_columns_kernel<TX, TY>), dim3(chunks, (unsigned)norm_parts(a.B, a.H)),
+                       dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -205,7 +563,9 @@ hipError_t gradient(const NormArgs &a, hipStream_t s)
 
 int norm_parts(int32_t B, int32_t H)
 {
-    return std::min(B, 256);
+    if ((H + 7) / 8 > kMostUnits)
+        return std::min(B, 256);
+    return groups_of(shape_of(H), B, kGradWaves);
 }
 
 hipError_t launch_norm(const NormArgs &a, hipStream_t s)
@@ -224,7 +584,8 @@ hipError_t launch_norm_grad(const NormArgs &a, hipStream_t s)
 
 hipError_t launch_norm_params(const NormArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(norm_params_kernel, dim3((unsigned)((a.H + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(norm_params_kernel, dim3((unsigned)((a.H + kJoinColumns - 1) / kJoinColumns), 2),
+                       dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 

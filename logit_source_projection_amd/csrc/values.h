@@ -126,13 +126,31 @@ __device__ __forceinline__ void store_some(bf16_t *p, const float (&v)[8], int n
             put(p + e, v[e]);
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// The value of another lane of the 16 that a DPP control reaches.
+template <int CONTROL>
+__device__ __forceinline__ float dpp(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v += __shfl_xor(v, d);
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CONTROL, 0xF, 0xF, true));
+}
+
+// The sum over LANES neighbouring lanes (8, 16, 32 or 64), in each of them.  Lanes add
+// what lies across the middle of ever larger groups, so that all find the same bits.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    v += dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+    v += dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+    v += dpp<0x141>(v);  // row_half_mirror
+    if (LANES >= 16)
+        v += dpp<0x140>(v);  // row_mirror
+    if (LANES >= 32)
+        v += __shfl_xor(v, 16);
+    if (LANES >= 64)
+        v += __shfl_xor(v, 32);
     return v;
 }
+
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
 }  // namespace
 }  // namespace sbk

@@ -568,8 +568,9 @@ sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_ty
  *            allocation is passed as w[i] = base + off_i * ldw.
  *   ldw      row stride, >= H, a multiple of 4 (fp32) or 8 (bf16)
  *   type     sb_dtype of the table (anything else: SB_ERR_SHAPE, as for every type)
- * H <= 2^24 and V <= 2^30, in the gradient V <= 2^24 and B <= 2^24; every matrix
- * of these calls spans less than 2^47 bytes (SB_ERR_UNSUPPORTED).
+ * H <= 2^24 and V <= 2^30; in the gradient H < 2^24 - 256, V <= 2^24, B <= 2^24 and
+ * about B * H < 2^38; every matrix of these calls spans less than 2^47 bytes
+ * (SB_ERR_UNSUPPORTED).
  */
 typedef struct sb_table_desc {
     int32_t V, H, k;

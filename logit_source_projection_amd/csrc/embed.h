@@ -24,16 +24,31 @@ struct EmbedArgs {
     const void *dout;             // [B][lddo]
     int64_t lddo;
     bool add;                     // added to the table's rows instead of replacing all of them
-    int32_t *start;               // [V + 1]: where each ID's positions start in `order`
-    int32_t *order;               // [B] positions sorted by their IDs, equal ones ascending
+    int32_t shift;                // 2^shift groups of IDs: ID v is number v >> shift of group
+                                  // v % 2^shift
+    int32_t range;                // IDs of a group
+    int32_t *start;               // [range * 2^shift + 1]: where each ID's positions start in
+                                  // `order`, group by group (embed_slot); behind the last
+                                  // ID, how many there are
+    int32_t *order;               // [B] positions sorted by their IDs' places in `start`,
+                                  // those of an ID ascending
     int32_t *sorted;              // [B] their IDs
-    float *part;                  // fp32 [runs][2][ldpart]
+    float *part;                  // fp32 [pieces][2][ldpart]
     int64_t ldpart;
     int32_t runs;
 };
 
-// Sorted positions per run: the rows of a run are summed by one workgroup.
-constexpr int kEmbedRun = 64;
+// IDs of up to kEmbedLong positions are summed whole, by the workgroup of the run of
+// kEmbedRun sorted positions that they start in; those of more in pieces of kEmbedPiece
+// sorted positions, whose sums (`part`) are joined.
+constexpr int kEmbedRun = 16, kEmbedLong = 32, kEmbedPiece = 32;
+
+// Whether the gradient's launches fit a grid.
+bool embed_grad_fits(int32_t B, int32_t H);
+
+// The groups that a table's IDs are sorted in (2 to this), and the IDs of each.
+int embed_shift(int32_t V);
+inline int embed_range(int32_t V) { return (int)(((int64_t)V + (1 << embed_shift(V)) - 1) >> embed_shift(V)); }
 
 hipError_t launch_embed(const EmbedArgs &a, hipStream_t s);
 hipError_t launch_embed_sort(const EmbedArgs &a, hipStream_t s);

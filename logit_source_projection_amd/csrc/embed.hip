@@ -9,14 +9,22 @@
 
 #include <algorithm>
 
+#include "tile_gemm.h"
 #include "values.h"
 
 namespace sbk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnitColumns = 8 * kThreads;  // columns that a workgroup takes at a time
-constexpr int64_t kMostGroups = 1 << 20;    // workgroups along x
+constexpr int64_t kMostGroups = 1 << 20; // workgroups along x
+
+// Threads for rows of H columns, 8 to each: a row in equal parts of up to kThreads
+// threads, so that few are idle.
+inline int row_threads(int H)
+{
+    const int units = std::max(1, (H + 7) / 8), parts = (units + kThreads - 1) / kThreads;
+    return std::max(64, ((units + parts - 1) / parts + 63) / 64 * 64);
+}
 
 // The row of a table that ID v (0 .. V - 1) names.
 template <typename T>
@@ -30,143 +38,234 @@ __device__ __forceinline__ T *table_row(const EmbedArgs &a, int v)
         else
             hi = mid;
     }
-    return static_cast<T *>(a.w[lo]) + (int64_t)(v - a.off[lo]) * a.ldw;
+    return in_memory(static_cast<T *>(a.w[lo])) + (int64_t)(v - a.off[lo]) * a.ldw;
 }
 
 // ---------------------------------------------------------------------------
-// Lookup: one workgroup per row.
+// Lookup: `team` threads per row (a power of two up to 32, or the workgroup).
 // ---------------------------------------------------------------------------
+constexpr int kLookupUnits = 4;  // loads of a thread under way
+
 template <typename TT, typename TO>
-__global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedArgs a)
+__global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedArgs a, int team)
 {
-    const int H = a.H;
-    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int id = __builtin_amdgcn_readfirstlane(a.ids[b]);
+    const int H = a.H, at = threadIdx.x % team, teams = blockDim.x / team;
+    for (int64_t b = (int64_t)blockIdx.x * teams + threadIdx.x / team; b < a.B; b += (int64_t)gridDim.x * teams) {
+        int id = a.ids[b];
+        if (teams == 1)
+            id = __builtin_amdgcn_readfirstlane(id);
         TO *out = static_cast<TO *>(a.out) + b * a.ldo;
         const bool there = (uint32_t)id < (uint32_t)a.V;
-        const TT *row = there ? table_row<TT>(a, id) : nullptr;
+        const TT *row = table_row<const TT>(a, there ? id : 0);
         const float other = id < 0 ? 0.f : NAN;
-        for (int c = 8 * threadIdx.x; c < H; c += kUnitColumns) {
-            float v[8];
-            if (there)
-                values_of(load_some(row + c, H - c), v);
+        for (int c0 = 8 * at; c0 < H; c0 += 8 * kLookupUnits * team) {
+            Unit<TT> raw[kLookupUnits];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = there ? v[e] * a.scale : other;
-            store_some(out + c, v, H - c);
+            for (int k = 0; k < kLookupUnits; ++k)
+                raw[k] = load_at(row, c0 + 8 * k * team, H);
+#pragma unroll
+            for (int k = 0; k < kLookupUnits; ++k) {
+                const int c = c0 + 8 * k * team;
+                float v[8];
+                values_of(raw[k], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = there ? v[e] * a.scale : other;
+                if (c < H)
+                    store_some(out + c, v, H - c);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Positions sorted by their IDs, equal ones ascending, in one launch without a
-// word between workgroups: each takes a range of IDs and reads all of `ids`
-// twice (from the L2; 64 KB for 16384 tokens).  The first pass counts the IDs
-// below its range, which is where its own positions start, and those of every ID
-// in it; the second compacts the range's positions in order, a chunk at a time,
-// and places them behind the earlier ones of their ID.  In a chunk wave w places
-// the IDs that are w modulo 16, 64 entries at a time, all equal ones at once: a
-// token that fills the batch is as quick as one that comes once.
+// Positions sorted by ID, equal ones ascending, in one launch without a word
+// between workgroups.  Workgroup g takes the IDs that are g modulo the number of groups (so that
+// neighbouring IDs, which often come together, are spread) and reads all of `ids`
+// (from the L2; 64 KB for 16384 tokens).  A first pass counts the IDs of the groups
+// before, which is where its own positions start, and those of every ID of its own; a
+// second compacts its positions in order, a chunk at a time, and places them behind
+// the earlier ones of their ID.  Up to a chunk of IDs stay in registers between the
+// passes.  In a chunk wave w places the IDs whose number in the group is w modulo 16,
+// 64 entries at a time, all equal ones at once.  An ID of a 32nd of all tokens or
+// more (padding that is not negative, say) is placed by the whole workgroup instead,
+// straight from the registers: 16384 equal tokens took 70 us in one wave's hands.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortEach = 4;                              // IDs per thread and chunk
-constexpr int kSortChunk = kSortThreads * kSortEach;
+constexpr int kSortEach = 16;                             // IDs per thread and chunk
+constexpr int kSortChunk = kSortThreads * kSortEach;      // 2^14
 constexpr int kSortRange = 4096;                          // IDs per workgroup at most
-constexpr int kSortGroups = 256;                          // workgroups where ranges allow
+constexpr int kSortNeighbours = kSortRange / kSortThreads;
+constexpr int kSortLds = kSortRange * 4 + kSortChunk * 4;
+constexpr int kSortHot = 32;                              // IDs that may be this share of all
 
-inline int sort_range(int V)
+// The place of an ID in `start`.
+__device__ __forceinline__ int embed_slot(const EmbedArgs &a, uint32_t v)
 {
-    return std::min(kSortRange, (V + kSortGroups - 1) / kSortGroups);
+    return (int)(v & ((1u << a.shift) - 1)) * a.range + (int)(v >> a.shift);
 }
 
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArgs a, int range)
+// The IDs of a chunk, 64 neighbours to a wave's load: their number in the group, or
+// kSortOther of another group's; `before` counts those of groups before this one.
+constexpr uint32_t kSortOther = 0xFFFFFFFFu;
+
+__device__ __forceinline__ int sort_place(int b0, int k)
 {
-    __shared__ int32_t next[kSortRange];        // counts, then where an ID's next position goes
-    __shared__ int2 list[kSortChunk];           // {ID - lo, position} of the chunk
-    __shared__ int32_t sums[kSortWaves];
-    const int lo = blockIdx.x * range, n = min(range, a.V - lo);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int i = threadIdx.x; i < n; i += kSortThreads)
+    return b0 + ((threadIdx.x >> 6) * kSortEach + k) * 64 + (threadIdx.x & 63);
+}
+
+__device__ __forceinline__ void sort_load(const EmbedArgs &a, int b0, uint32_t (&id)[kSortEach], int &before)
+{
+#pragma unroll
+    for (int k = 0; k < kSortEach; ++k) {
+        const int b = sort_place(b0, k);
+        id[k] = b < a.B ? (uint32_t)a.ids[b] : kSortOther;
+    }
+#pragma unroll
+    for (int k = 0; k < kSortEach; ++k) {
+        const uint32_t group = id[k] & ((1u << a.shift) - 1);
+        const bool there = id[k] < (uint32_t)a.V;
+        before += there && group < blockIdx.x;
+        id[k] = there && group == blockIdx.x ? id[k] >> a.shift : kSortOther;
+    }
+}
+
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArgs a)
+{
+    extern __shared__ int32_t smem[];
+    int32_t *next = smem;                     // counts, then where an ID's next position goes
+    uint32_t *list = reinterpret_cast<uint32_t *>(smem + kSortRange);  // number << 14 | place in the chunk
+    __shared__ int32_t sums[kSortWaves], hot[kSortHot], hots;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, range = a.range;
+    int before = 0, none = 0;
+    uint32_t id[kSortEach];
+    sort_load(a, 0, id, before);
+    for (int i = threadIdx.x; i < range; i += kSortThreads)
         next[i] = 0;
+    if (threadIdx.x == 0)
+        hots = 0;
     __syncthreads();
-    int below = 0;
-    for (int b = threadIdx.x; b < a.B; b += kSortThreads) {
-        const int id = a.ids[b];
-        below += (uint32_t)id < (uint32_t)lo;
-        const uint32_t at = (uint32_t)id - (uint32_t)lo;
-        if (at < (uint32_t)n)
-            atomicAdd(&next[at], 1);
+    for (int b0 = 0; b0 < a.B; b0 += kSortChunk) {
+        if (b0 > 0)
+            sort_load(a, b0, id, before);
+#pragma unroll
+        for (int k = 0; k < kSortEach; ++k)
+            if (id[k] != kSortOther)
+                atomicAdd(&next[id[k]], 1);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1)
-        below += __shfl_xor(below, d);
+        before += __shfl_xor(before, d);
     if (lane == 0)
-        sums[wave] = below;
+        sums[wave] = before;
     __syncthreads();
     int base = 0;
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w)
         base += sums[w];
-    // counts to starting places, 64 IDs at a time by the first wave
-    if (wave == 0) {
-        for (int i0 = 0; i0 < n; i0 += 64) {
-            const int i = i0 + lane, count = i < n ? next[i] : 0;
-            int upto = count;
+    // counts to starting places, kSortNeighbours neighbours per thread
+    const int most = max(kSortThreads, a.B / kSortHot);
+    int count[kSortNeighbours], upto = 0;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int v = __shfl_up(upto, d);
-                upto += lane >= d ? v : 0;
-            }
-            if (i < n) {
-                next[i] = base + upto - count;
-                if (!a.add)
-                    a.start[lo + i] = base + upto - count;
-            }
-            base += __shfl(upto, 63);
-        }
-        if (lane == 0 && lo + n == a.V)
-            a.start[a.add ? 0 : a.V] = base;
+    for (int e = 0; e < kSortNeighbours; ++e) {
+        const int i = kSortNeighbours * threadIdx.x + e;
+        count[e] = i < range ? next[i] : 0;
+        upto += count[e];
+        if (count[e] > most)  // (fewer than kSortHot IDs have so many)
+            hot[atomicAdd(&hots, 1)] = i;
     }
-    for (int b0 = 0; b0 < a.B; b0 += kSortChunk) {
-        // wave w compacts the chunk's IDs [256 w, 256 w + 256)
-        int id[kSortEach], mine = 0;
-        uint64_t hit[kSortEach];
+    const int own = upto;
 #pragma unroll
-        for (int i = 0; i < kSortEach; ++i) {
-            const int b = b0 + (wave * kSortEach + i) * 64 + lane;
-            id[i] = b < a.B ? (int)((uint32_t)a.ids[b] - (uint32_t)lo) : -1;
-            hit[i] = __ballot((uint32_t)id[i] < (uint32_t)n);
-            mine += __popcll(hit[i]);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        upto += lane >= d ? v : 0;
+    }
+    __syncthreads();  // `sums` has been read
+    if (lane == 63)
+        sums[wave] = upto;
+    __syncthreads();
+    base += upto - own;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w)
+        base += w < wave ? sums[w] : 0;
+#pragma unroll
+    for (int e = 0; e < kSortNeighbours; ++e) {
+        const int i = kSortNeighbours * threadIdx.x + e;
+        if (i < range) {
+            next[i] = a.start[blockIdx.x * range + i] = base;
+            base += count[e];
+            if (i == range - 1 && blockIdx.x + 1 == gridDim.x)
+                a.start[range << a.shift] = base;
         }
-        __syncthreads();  // `sums` and the list are free, `next` is whole
+    }
+    // Where this wave's hits of a chunk start among the workgroup's, and all of them.
+    // (The first barrier also makes `next` whole, and the second the list free.)
+    auto places = [&](int mine, int &all) {
+        __syncthreads();
         if (lane == 0)
             sums[wave] = mine;
         __syncthreads();
-        int at = 0, entries = 0;
+        int at = 0;
+        all = 0;
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
             at += w < wave ? sums[w] : 0;
-            entries += sums[w];
+            all += sums[w];
         }
+        return at;
+    };
+    const uint64_t earlier = ((uint64_t)1 << lane) - 1;
+    for (int b0 = 0; b0 < a.B; b0 += kSortChunk) {
+        if (a.B > kSortChunk)
+            sort_load(a, b0, id, none);
+        for (int h = 0; h < hots; ++h) {
+            const int one = hot[h];
+            int mine = 0, all;
 #pragma unroll
-        for (int i = 0; i < kSortEach; ++i) {
-            if (hit[i] >> lane & 1)
-                list[at + __popcll(hit[i] & (((uint64_t)1 << lane) - 1))] =
-                    make_int2(id[i], b0 + (wave * kSortEach + i) * 64 + lane);
-            at += __popcll(hit[i]);
+            for (int k = 0; k < kSortEach; ++k)
+                mine += __popcll(__ballot(id[k] == (uint32_t)one));
+            int p = places(mine, all) + next[one];
+#pragma unroll
+            for (int k = 0; k < kSortEach; ++k) {
+                const uint64_t hit = __ballot(id[k] == (uint32_t)one);
+                if (hit >> lane & 1) {
+                    const int to = p + __popcll(hit & earlier);
+                    a.order[to] = sort_place(b0, k);
+                    a.sorted[to] = (one << a.shift) + blockIdx.x;
+                    id[k] = kSortOther;
+                }
+                p += __popcll(hit);
+            }
+            __syncthreads();  // `next` has been read
+            if (threadIdx.x == 0)
+                next[one] += all;
+        }
+        int mine = 0, entries;
+#pragma unroll
+        for (int k = 0; k < kSortEach; ++k)
+            mine += __popcll(__ballot(id[k] != kSortOther));
+        int at = places(mine, entries);
+#pragma unroll
+        for (int k = 0; k < kSortEach; ++k) {
+            const uint64_t hit = __ballot(id[k] != kSortOther);
+            if (hit >> lane & 1)
+                list[at + __popcll(hit & earlier)] = id[k] << 14 | (uint32_t)sort_place(0, k);
+            at += __popcll(hit);
         }
         __syncthreads();
         for (int e0 = 0; e0 < entries; e0 += 64) {
-            const int2 entry = e0 + lane < entries ? list[e0 + lane] : make_int2(-1, 0);
-            uint64_t todo = __ballot(entry.x >= 0 && entry.x % kSortWaves == wave);
+            const bool there = e0 + lane < entries;
+            const uint32_t entry = there ? list[e0 + lane] : 0u;
+            const int which = there ? (int)(entry >> 14) : -1;
+            uint64_t todo = __ballot(there && which % kSortWaves == wave);
             while (todo) {
-                const int one = __builtin_amdgcn_readlane(entry.x, __builtin_ctzll(todo));
-                const uint64_t same = __ballot(entry.x == one);
+                const int one = __builtin_amdgcn_readlane(which, __builtin_ctzll(todo));
+                const uint64_t same = __ballot(which == one);
                 const int place = next[one];
-                if (entry.x == one) {
-                    const int p = place + __popcll(same & (((uint64_t)1 << lane) - 1));
-                    a.order[p] = entry.y;
-                    a.sorted[p] = lo + one;
+                if (which == one) {
+                    const int p = place + __popcll(same & earlier);
+                    a.order[p] = b0 + (int)(entry & (kSortChunk - 1));
+                    a.sorted[p] = (one << a.shift) + blockIdx.x;
                 }
                 next[one] = place + __popcll(same);  // (by every lane: the next read is its own)
                 todo &= ~same;
@@ -174,28 +273,14 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArg
         }
     }
 }
+static_assert(kSortChunk == 1 << 14 && kSortRange <= 1 << 18, "an entry of the list is 32 bits");
 
-// Rows without a position are zeros.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void embed_zero_kernel(const EmbedArgs a)
+// n values of a row of the gradient from their sums.
+template <bool ADD, typename T>
+__device__ __forceinline__ void store_row(const EmbedArgs &a, T *to, int n, const float (&sum)[8])
 {
-    const float zeros[8] = {};
-    for (int v = blockIdx.x; v < a.V; v += gridDim.x) {
-        if (a.start[v] != a.start[v + 1])
-            continue;
-        T *row = table_row<T>(a, v);
-        for (int c = 8 * threadIdx.x; c < a.H; c += kUnitColumns)
-            store_some(row + c, zeros, a.H - c);
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_row(const EmbedArgs &a, int id, int c, const float (&sum)[8])
-{
-    T *to = table_row<T>(a, id) + c;
-    const int n = a.H - c;
     float v[8];
-    if (a.add) {
+    if (ADD) {
         values_of(load_some(to, n), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -209,91 +294,271 @@ __device__ __forceinline__ void store_row(const EmbedArgs &a, int id, int c, con
 }
 
 // ---------------------------------------------------------------------------
-// Sums of runs of kEmbedRun sorted positions, a unit of columns per thread.  An
-// ID whose positions all lie in the run is done here; the sums of one that came
-// from the run before go to the run's first partial row, of one that starts here
-// and goes on to its second.
+// Sums of runs of kEmbedRun sorted positions, a unit of columns per thread: of the IDs
+// of up to kEmbedLong positions that start in the run, all of them.  The workgroup of
+// a piece's first run also has those of the longer IDs in the piece: the sum of one
+// that goes on behind it goes to the piece's second partial row, of one that came from
+// before to its first.  Rows are loaded kRunLoads at a time.
 // ---------------------------------------------------------------------------
-template <typename TT, typename TO>
-__global__ __launch_bounds__(kThreads) void embed_runs_kernel(const EmbedArgs a)
+constexpr int kRunLoads = 8;
+static_assert(kEmbedRun + kEmbedLong <= 64 && kEmbedPiece <= 64 && kEmbedPiece % kEmbedRun == 0,
+              "the positions of a run and of a piece are a wave's lanes");
+
+template <typename TT, typename TO, bool ADD>
+__device__ __forceinline__ void sum_run(const EmbedArgs &a, int run, int c)
 {
-    const int c = blockIdx.y * kUnitColumns + 8 * threadIdx.x;
-    const int total = a.start[a.add ? 0 : a.V];
-    const int run = blockIdx.x, p0 = run * kEmbedRun, p1 = min(p0 + kEmbedRun, total);
-    if (c >= a.H || p0 >= p1)
+    const int total = a.start[a.range << a.shift], lane = threadIdx.x & 63;
+    const int p0 = run * kEmbedRun, p = p0 + lane;
+    if (p0 >= total)
         return;
+    // lane l: position p0 + l, its ID, and the ID's first position and the one behind
+    const int id = a.sorted[min(p, total - 1)];
+    const int row = a.order[min(p, total - 1)];
+    const int32_t *start = a.start + embed_slot(a, (uint32_t)id);
+    const int first = start[0], behind = start[1];
+    const bool many = behind - first > kEmbedLong;
+    const bool mine = p < total && (many ? p0 % kEmbedPiece == 0 && lane < kEmbedPiece : first >= p0 && first < p0 + kEmbedRun);
+    const bool whole = !many || (first >= p0 && behind <= p0 + kEmbedPiece);
+    const uint64_t stores = __ballot(mine && (p + 1 == behind || (many && lane == kEmbedPiece - 1)));
+    const uint64_t wholes = __ballot(whole);
+    char *to = whole ? reinterpret_cast<char *>(table_row<TT>(a, id))
+                     : reinterpret_cast<char *>(a.part + (2 * (int64_t)(p0 / kEmbedPiece) + (first >= p0)) * a.ldpart);
+    const int to_low = (int)reinterpret_cast<uint64_t>(to), to_high = (int)(reinterpret_cast<uint64_t>(to) >> 32);
     float sum[8] = {};
-    bool begins = p0 == 0 || a.sorted[p0 - 1] != a.sorted[p0];
-    for (int p = p0; p < p1; ++p) {
-        const int id = a.sorted[p];
-        float v[8];
-        values_of(load_some(static_cast<const TO *>(a.dout) + (int64_t)a.order[p] * a.lddo + c, a.H - c), v);
+    uint64_t todo = __ballot(mine);
+    while (todo) {
+        // the next kRunLoads of them; the last one again where there are no more, which
+        // is added behind its own store and lost
+        int at[kRunLoads];
+        uint64_t now = 0;
+        Unit<TO> raw[kRunLoads];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum[e] += v[e];
-        const bool ends = p + 1 == total || a.sorted[p + 1] != id;
-        if (!ends && p + 1 < p1)
-            continue;
-        if (begins && ends)
-            store_row<TT>(a, id, c, sum);
-        else
-            store_some(a.part + (2 * (int64_t)run + begins) * a.ldpart + c, sum, 8);
+        for (int q = 0; q < kRunLoads; ++q) {
+            at[q] = todo ? __builtin_ctzll(todo) : at[q > 0 ? q - 1 : 0];
+            now |= todo & -todo;
+            todo &= todo - 1;
+            raw[q] = load_at(static_cast<const TO *>(a.dout) + (int64_t)__builtin_amdgcn_readlane(row, at[q]) * a.lddo,
+                             c, a.H);
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum[e] = 0.f;
-        begins = true;
+        for (int q = 0; q < kRunLoads; ++q) {
+            float v[8];
+            values_of(raw[q], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] += v[e];
+            if (stores & now & (uint64_t)1 << at[q]) {
+                now ^= (uint64_t)1 << at[q];
+                const uint64_t row_at = (uint32_t)__builtin_amdgcn_readlane(to_low, at[q]) |
+                                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane(to_high, at[q]) << 32;
+                if (c < a.H) {
+                    if (wholes >> at[q] & 1)
+                        store_row<ADD>(a, in_memory(reinterpret_cast<TT *>(row_at)) + c, a.H - c, sum);
+                    else
+                        store_some(in_memory(reinterpret_cast<float *>(row_at)) + c, sum, 8);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] = 0.f;
+            }
+        }
     }
 }
 
-// IDs whose positions span runs: the workgroup of the run that they start in adds
-// the partial rows in order.
+// ---------------------------------------------------------------------------
+// Zeros for the rows that no ID names, nearly all of the call's bytes.  A thread has one
+// 16-byte chunk and workgroups follow each other through the table: in that order
+// 151936 rows of 10 KB take 235 us with the sort (227 us as a plain fill); workgroups
+// with a row or two each took 297.  What there is to save is the time up to the store:
+// chunks are numbered within 31 bits and divided by multiplication (245 us and more
+// otherwise), and the row's lane is looked for, by the scalar unit where a wave is in
+// one row, while the flags are under way.  They share a launch with the sums, whose
+// loads run beside them (3333 rows, V 50257, H 1111: 62 us, 75 in two launches).
+// ---------------------------------------------------------------------------
+struct ZeroRows {
+    int32_t first, rows;   // of the table, rows * chunks < 2^31
+    int32_t chunks;        // of a row, the last one possibly short
+    uint32_t factor;       // chunk k is in row (k * factor) >> shift
+    int32_t shift;
+};
+
+ZeroRows zero_rows(int first, int V, int64_t row_bytes)
+{
+    ZeroRows z;
+    z.chunks = (int32_t)((row_bytes + 15) / 16);
+    z.first = first;
+    z.rows = (int32_t)std::min<int64_t>(V - first, (((int64_t)1 << 31) - 1) / z.chunks);
+    // 2^(shift - 31) >= chunks, factor = 2^shift / chunks rounded up: off by less than
+    // chunks / 2^shift of it, so that k < 2^31 chunks never reach the next row
+    z.shift = 31;
+    while ((int64_t)1 << (z.shift - 31) < z.chunks)
+        ++z.shift;
+    z.factor = (uint32_t)((((uint64_t)1 << z.shift) + z.chunks - 1) / z.chunks);
+    return z;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_zero(const EmbedArgs &a, const ZeroRows &z, uint32_t k)
+{
+    if (k >= (uint32_t)z.rows * (uint32_t)z.chunks)
+        return;
+    const int row = (int)((uint64_t)k * z.factor >> z.shift), v = z.first + row;
+    const int32_t *start = a.start + embed_slot(a, (uint32_t)v);
+    const int first = start[0], behind = start[1];
+    const int one = __builtin_amdgcn_readfirstlane(v);
+    constexpr int kEach = 16 / sizeof(T);
+    const int c = kEach * (int)(k - (uint32_t)row * (uint32_t)z.chunks);
+    T *to = (__all(v == one) ? table_row<T>(a, one) : table_row<T>(a, v)) + c;
+    __builtin_amdgcn_sched_barrier(0);
+    if (first != behind)
+        return;
+    const int n = a.H - c;
+    if (n >= kEach) {
+        *reinterpret_cast<raw4 *>(to) = raw4{0u, 0u, 0u, 0u};
+        return;
+    }
+    for (int e = 0; e < n; ++e)
+        to[e] = 0;
+}
+
+// Sums, and behind their `groups` workgroups zeros, which run beside them.  A
+// workgroup has a run's columns, or where few threads do, several runs'.
+template <typename TT, typename TO, bool ADD>
+__global__ __launch_bounds__(kThreads) void embed_sums_kernel(const EmbedArgs a, const ZeroRows z, int threads,
+                                                              int parts, uint32_t groups)
+{
+    if (blockIdx.x >= groups) {
+        write_zero<TT>(a, z, (blockIdx.x - groups) * kThreads + threadIdx.x);
+        return;
+    }
+    const int per = kThreads / threads, team = threadIdx.x / threads, part = blockIdx.x % parts;
+    const int run = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / parts) * per + team);
+    if (team < per)
+        sum_run<TT, TO, ADD>(a, run, 8 * (part * threads + (int)threadIdx.x % threads));
+}
+
+// ---------------------------------------------------------------------------
+// IDs whose positions span pieces: their partial rows added, by the workgroup of the
+// piece that they start in.  It looks at a piece per wave and has kJoinColumns columns
+// of them.  A wave adds up to kJoinAlone rows by itself, in order; of more each of the
+// waves adds an equal share, and the shares are added in order.
+// ---------------------------------------------------------------------------
+constexpr int kJoinColumns = 256, kJoinWaves = kThreads / 64, kJoinAlone = 16, kJoinLoads = 8;
+
+// The partial rows [i0, i1) of the ID that starts in `piece`: the piece's second row, then
+// the first of each piece behind.
+__device__ __forceinline__ float4 add_parts(const EmbedArgs &a, int piece, int i0, int i1, int c)
+{
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *part = a.part + min((int64_t)c, a.ldpart - 4);
+    for (; i0 < i1; i0 += kJoinLoads) {
+        float4 v[kJoinLoads];
+#pragma unroll
+        for (int k = 0; k < kJoinLoads; ++k) {
+            const int i = min(i0 + k, i1 - 1);
+            v[k] = *reinterpret_cast<const float4 *>(part + (2 * (int64_t)(piece + i) + (i == 0)) * a.ldpart);
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinLoads; ++k) {
+            const bool there = i0 + k < i1;
+            sum.x += there ? v[k].x : 0.f;
+            sum.y += there ? v[k].y : 0.f;
+            sum.z += there ? v[k].z : 0.f;
+            sum.w += there ? v[k].w : 0.f;
+        }
+    }
+    return sum;
+}
+
+// Four columns per lane to the eight that a store takes: even lanes store.
+template <typename T>
+__device__ __forceinline__ void store_joined(const EmbedArgs &a, int id, int c, const float4 &sum)
+{
+    const float v[8] = {sum.x, sum.y, sum.z, sum.w, __shfl_down(sum.x, 1), __shfl_down(sum.y, 1),
+                        __shfl_down(sum.z, 1), __shfl_down(sum.w, 1)};
+    if ((threadIdx.x & 1) == 0 && c < a.H) {
+        T *row = table_row<T>(a, id) + c;
+        a.add ? store_row<true>(a, row, a.H - c, v) : store_row<false>(a, row, a.H - c, v);
+    }
+}
+
 template <typename TT>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(const EmbedArgs a)
 {
-    const int c = blockIdx.y * kUnitColumns + 8 * threadIdx.x;
-    const int total = a.start[a.add ? 0 : a.V];
-    const int run = blockIdx.x;
-    int p1 = (run + 1) * kEmbedRun;
-    if (c >= a.H || p1 >= total)
-        return;
-    const int id = a.sorted[p1];
-    // it goes on behind this run, and did not come from the one before
-    if (a.sorted[p1 - 1] != id || (run > 0 && a.sorted[p1 - kEmbedRun - 1] == id))
-        return;
-    float sum[8], v[8];
-    values_of(load_unit(a.part + (2 * (int64_t)run + 1) * a.ldpart + c), sum);
-    for (int r = run + 1; p1 < total && a.sorted[p1] == id; ++r, p1 += kEmbedRun) {
-        values_of(load_unit(a.part + 2 * (int64_t)r * a.ldpart + c), v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum[e] += v[e];
+    __shared__ float4 shares[kJoinWaves][64];
+    const int total = a.start[a.range << a.shift];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    // lane l: the ID that starts in piece kJoinWaves * x + l and goes on behind it
+    const int piece0 = blockIdx.x * kJoinWaves, p0 = (piece0 + lane) * kEmbedPiece, last = p0 + kEmbedPiece - 1;
+    int id = 0, rows = 0;
+    if (lane < kJoinWaves && last < total) {
+        id = a.sorted[last];
+        const int32_t *start = a.start + embed_slot(a, (uint32_t)id);
+        const int first = start[0], behind = start[1];
+        if (first >= p0 && behind > last + 1 && behind - first > kEmbedLong)
+            rows = (behind - 1) / kEmbedPiece - (piece0 + lane) + 1;
     }
-    store_row<TT>(a, id, c, sum);
+    const int c = blockIdx.y * kJoinColumns + 4 * lane;
+    const int mine = __builtin_amdgcn_readlane(rows, wave);
+    if (mine > 0 && mine <= kJoinAlone)
+        store_joined<TT>(a, __builtin_amdgcn_readlane(id, wave), c, add_parts(a, piece0 + wave, 0, mine, c));
+    for (uint64_t todo = __ballot(rows > kJoinAlone); todo; todo &= todo - 1) {
+        const int l = __builtin_ctzll(todo), n = __builtin_amdgcn_readlane(rows, l);
+        const int each = (n + kJoinWaves - 1) / kJoinWaves;
+        const float4 share = add_parts(a, piece0 + l, wave * each, min(n, (wave + 1) * each), c);
+        __syncthreads();  // the shares are free
+        shares[wave][lane] = share;
+        __syncthreads();
+        if (wave == 0) {
+            float4 sum = shares[0][lane];
+#pragma unroll
+            for (int w = 1; w < kJoinWaves; ++w) {
+                const float4 v = shares[w][lane];
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            store_joined<TT>(a, __builtin_amdgcn_readlane(id, l), c, sum);
+        }
+    }
 }
 
 template <typename TT, typename TO>
 hipError_t lookup(const EmbedArgs &a, hipStream_t s)
 {
-    const unsigned rows = (unsigned)std::min<int64_t>(a.B, kMostGroups);
-    hipLaunchKernelGGL((embed_kernel<TT, TO>), dim3(rows), dim3(kThreads), 0, s, a);
+    const int units = (a.H + 7) / 8;
+    int threads = kThreads, team = 8;
+    while (team < units && team < 64)
+        team <<= 1;
+    if (team == 64)
+        team = threads = row_threads(a.H);
+    const int64_t groups = ((int64_t)a.B + threads / team - 1) / (threads / team);
+    hipLaunchKernelGGL((embed_kernel<TT, TO>), dim3((unsigned)std::min(groups, kMostGroups)), dim3(threads), 0, s, a, team);
     return hipGetLastError();
 }
 
 template <typename TT, typename TO>
 hipError_t sums(const EmbedArgs &a, hipStream_t s)
 {
-    hipError_t e;
-    if (!a.add) {
-        const unsigned rows = (unsigned)std::min<int64_t>(a.V, kMostGroups);
-        hipLaunchKernelGGL((embed_zero_kernel<TT>), dim3(rows), dim3(kThreads), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess || a.B == 0)
+    const int threads = row_threads(a.H), parts = (a.H + 8 * threads - 1) / (8 * threads), per = kThreads / threads;
+    unsigned groups = (unsigned)((a.runs + per - 1) / per * parts);
+    hipError_t e = hipSuccess;
+    if (a.add)
+        hipLaunchKernelGGL((embed_sums_kernel<TT, TO, true>), dim3(groups), dim3(kThreads), 0, s, a, ZeroRows{}, threads, parts, groups);
+    for (int first = 0; !a.add && first < a.V;) {
+        const ZeroRows z = zero_rows(first, a.V, a.H * (int64_t)sizeof(TT));
+        const unsigned zeros = ((unsigned)z.rows * (unsigned)z.chunks + kThreads - 1) / kThreads;
+        hipLaunchKernelGGL((embed_sums_kernel<TT, TO, false>), dim3(groups + zeros), dim3(kThreads), 0, s, a, z, threads, parts, groups);
+        if ((e = hipGetLastError()) != hipSuccess)
             return e;
+        first += z.rows;
+        groups = 0;
     }
-    const dim3 grid((unsigned)a.runs, (unsigned)((a.H + kUnitColumns - 1) / kUnitColumns));
-    hipLaunchKernelGGL((embed_runs_kernel<TT, TO>), grid, dim3(kThreads), 0, s, a);
-    if ((e = hipGetLastError()) != hipSuccess || a.runs < 2)
+    if ((e = hipGetLastError()) != hipSuccess || a.B <= std::max(kEmbedPiece, kEmbedLong))
         return e;
-    hipLaunchKernelGGL((embed_join_kernel<TT>), dim3(grid.x - 1, grid.y), dim3(kThreads), 0, s, a);
+    const dim3 grid((unsigned)((a.B + kEmbedPiece * kJoinWaves - 1) / (kEmbedPiece * kJoinWaves)), (unsigned)((a.H + kJoinColumns - 1) / kJoinColumns));
+    hipLaunchKernelGGL((embed_join_kernel<TT>), grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -306,10 +571,30 @@ hipError_t launch_embed(const EmbedArgs &a, hipStream_t s)
     return a.rows_bf16 ? lookup<float, bf16_t>(a, s) : lookup<float, float>(a, s);
 }
 
+// 256 groups, one for every CU, or as many as leave no more IDs in one than it counts.
+int embed_shift(int32_t V)
+{
+    int shift = 8;
+    while ((int64_t)kSortRange << shift < V)
+        ++shift;
+    return shift;
+}
+
+bool embed_grad_fits(int32_t B, int32_t H)
+{
+    const int64_t threads = row_threads(H), parts = ((int64_t)H + 8 * threads - 1) / (8 * threads);
+    const int64_t runs = ((int64_t)B + kEmbedRun - 1) / kEmbedRun;
+    return runs * parts * kThreads < (int64_t)1 << 32 &&
+           ((int64_t)H + kJoinColumns - 1) / kJoinColumns <= 65535;
+}
+
 hipError_t launch_embed_sort(const EmbedArgs &a, hipStream_t s)
 {
-    const int range = sort_range(a.V);
-    hipLaunchKernelGGL(embed_sort_kernel, dim3((unsigned)((a.V + range - 1) / range)), dim3(kSortThreads), 0, s, a, range);
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(embed_sort_kernel), kSortLds, allowed);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(embed_sort_kernel, dim3(1u << a.shift), dim3(kSortThreads), kSortLds, s, a);
     return hipGetLastError();
 }
 

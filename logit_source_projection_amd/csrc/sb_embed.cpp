@@ -78,7 +78,7 @@ Layout layout(const sb_table_desc *d, int32_t B, bool add)
     Layout L;
     if (d->H == 0 || (B == 0 && add))
         return L;
-    size_t at = up(((size_t)(add ? 0 : d->V) + 1) * sizeof(int32_t), kRegionAlign);
+    size_t at = up((((size_t)sbk::embed_range(d->V) << sbk::embed_shift(d->V)) + 1) * sizeof(int32_t), kRegionAlign);
     L.order = at;
     at = up(at + (size_t)B * sizeof(int32_t), kRegionAlign);
     L.sorted = at;
@@ -86,8 +86,9 @@ Layout layout(const sb_table_desc *d, int32_t B, bool add)
     L.runs = (B + sbk::kEmbedRun - 1) / sbk::kEmbedRun;
     L.ldpart = ((int64_t)d->H + 7) & ~(int64_t)7;
     L.part = at;
-    // (one run has no partial rows)
-    L.total = up(at + (L.runs > 1 ? (size_t)L.runs * 2 * (size_t)L.ldpart * sizeof(float) : 0), kRegionAlign);
+    const size_t pieces = ((size_t)B + sbk::kEmbedPiece - 1) / sbk::kEmbedPiece;
+    // (one piece has no partial rows)
+    L.total = up(at + (pieces > 1 ? pieces * 2 * (size_t)L.ldpart * sizeof(float) : 0), kRegionAlign);
     return L;
 }
 
@@ -98,7 +99,8 @@ sb_status check_grad(const sb_table_desc *d, int32_t B)
         return st;
     if (B < 0)
         return SB_ERR_SHAPE;
-    return d->V > kMostGradVocab || B > kMostGradRows ? SB_ERR_UNSUPPORTED : SB_OK;
+    return d->V > kMostGradVocab || B > kMostGradRows || !sbk::embed_grad_fits(B, d->H) ? SB_ERR_UNSUPPORTED
+                                                                                     : SB_OK;
 }
 
 sbk::EmbedArgs args_of(const sb_table_desc *d, const int32_t *ids, int32_t B, float scale, int rows_type)
@@ -170,6 +172,8 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
     a.dout = dout;
     a.lddo = lddo;
     a.add = add;
+    a.range = sbk::embed_range(desc->V);
+    a.shift = sbk::embed_shift(desc->V);
     a.start = reinterpret_cast<int32_t *>(base + L.start);
     a.order = reinterpret_cast<int32_t *>(base + L.order);
     a.sorted = reinterpret_cast<int32_t *>(base + L.sorted);

@@ -28,6 +28,14 @@ __device__ __forceinline__ float value_of(bf16_t bits) { return __uint_as_float(
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t *p, float v) { *p = __builtin_bit_cast(bf16_t, (__bf16)v); }
 
+// A pointer that the compiler would not know to be to device memory (one taken out of
+// a table, say): flat accesses count as LDS ones too, and loads would wait for stores.
+template <typename T>
+__device__ __forceinline__ T *in_memory(T *p)
+{
+    return (T *)(__attribute__((address_space(1))) T *)p;
+}
+
 // Eight values as they lie in memory.
 template <typename T>
 struct Unit;
@@ -68,17 +76,33 @@ __device__ __forceinline__ void values_of(const Unit<bf16_t> &u, float (&v)[8])
     }
 }
 
-// A unit whose first n values are there; the others are 0 and not read.
+// A unit whose first n values are there; the others are 0 and not read.  (By 16, 8,
+// 4 and 2 bytes, whose places are as aligned as they are long.)
+__device__ __forceinline__ raw4 load_words(const uint32_t *p, int n)
+{
+    raw4 w = {0u, 0u, 0u, 0u};
+    if (n >= 4)
+        return *reinterpret_cast<const raw4 *>(p);
+    if (n >= 2) {
+        const uint2 two = *reinterpret_cast<const uint2 *>(p);
+        w[0] = two.x;
+        w[1] = two.y;
+    }
+    if (n & 1) {
+        const uint32_t one = p[n - 1];
+        w[0] = n == 1 ? one : w[0];
+        w[2] = n == 3 ? one : 0u;
+    }
+    return w;
+}
 __device__ __forceinline__ Unit<float> load_some(const float *p, int n)
 {
     if (n >= 8)
         return load_unit(p);
     Unit<float> u;
-    clear(u);
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n)
-            (e < 4 ? u.a : u.b)[e & 3] = __float_as_uint(p[e]);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(p);
+    u.a = load_words(words, max(n, 0));
+    u.b = load_words(words + 4, max(n - 4, 0));
     return u;
 }
 __device__ __forceinline__ Unit<bf16_t> load_some(const bf16_t *p, int n)
@@ -86,44 +110,68 @@ __device__ __forceinline__ Unit<bf16_t> load_some(const bf16_t *p, int n)
     if (n >= 8)
         return load_unit(p);
     Unit<bf16_t> u;
-    clear(u);
+    u.a = load_words(reinterpret_cast<const uint32_t *>(p), max(n, 0) >> 1);
+    if (n > 0 && n & 1) {
+        const uint32_t one = p[n - 1];
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n)
-            u.a[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        for (int e = 0; e < 4; ++e)
+            u.a[e] = n >> 1 == e ? one : u.a[e];
+    }
     return u;
 }
 
-// The first n of eight values, rounded to the type.
-__device__ __forceinline__ void store_some(float *p, const float (&v)[8], int n)
+// The unit at column c of a row of H (>= 1) columns, in whole 16-byte loads without a
+// branch: what lies behind the row's last 16 bytes is not read (the row's first ones are
+// instead), and columns behind H hold anything.
+__device__ __forceinline__ Unit<float> load_at(const float *row, int c, int H)
 {
-    if (n >= 8) {
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        reinterpret_cast<f4 *>(p)[0] = f4{v[0], v[1], v[2], v[3]};
-        reinterpret_cast<f4 *>(p)[1] = f4{v[4], v[5], v[6], v[7]};
+    return {*reinterpret_cast<const raw4 *>(row + (c < H ? c : 0)),
+            *reinterpret_cast<const raw4 *>(row + (c + 4 < H ? c + 4 : 0))};
+}
+__device__ __forceinline__ Unit<bf16_t> load_at(const bf16_t *row, int c, int H)
+{
+    return {*reinterpret_cast<const raw4 *>(row + (c < H ? c : 0))};
+}
+// The first n of eight values, rounded to the type.
+__device__ __forceinline__ void store_words(uint32_t *p, const raw4 &w, int n)
+{
+    if (n >= 4) {
+        *reinterpret_cast<raw4 *>(p) = w;
         return;
     }
+    if (n >= 2)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    if (n > 0 && n & 1)
+        p[n - 1] = n == 1 ? w[0] : w[2];
+}
+__device__ __forceinline__ void store_some(float *p, const float (&v)[8], int n)
+{
+    raw4 a, b;
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n)
-            p[e] = v[e];
+    for (int e = 0; e < 4; ++e) {
+        a[e] = __float_as_uint(v[e]);
+        b[e] = __float_as_uint(v[4 + e]);
+    }
+    uint32_t *words = reinterpret_cast<uint32_t *>(p);
+    store_words(words, a, n);
+    if (n > 4)
+        store_words(words + 4, b, n - 4);
 }
 __device__ __forceinline__ void store_some(bf16_t *p, const float (&v)[8], int n)
 {
-    if (n >= 8) {
-        half8 h;
+    half8 h;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            h[e] = (__bf16)v[e];
-        *reinterpret_cast<half8 *>(p) = h;
-        return;
+    for (int e = 0; e < 8; ++e)
+        h[e] = (__bf16)v[e];
+    const raw4 w = __builtin_bit_cast(raw4, h);
+    store_words(reinterpret_cast<uint32_t *>(p), w, n >> 1);
+    if (n < 8 && n & 1) {
+        uint32_t one = w[0];
+#pragma unroll
+        for (int e = 1; e < 4; ++e)
+            one = n >> 1 == e ? w[e] : one;
+        p[n - 1] = (bf16_t)one;
     }
-    // (each value converted by itself: values taken out of a converted vector came
-    // out as their neighbour)
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n)
-            put(p + e, v[e]);
 }
 
 // The value of another lane of the 16 that a DPP control reaches.

@@ -96,3 +96,11 @@ def test_host_tensors_are_refused():
         sb.sb_embed_grad(sb.Table(w), ids, torch.zeros(2, 8))
     with pytest.raises(ValueError, match="one tensor per lane, 2"):
         sb.Table([w], [0, 8, 16])
+
+
+def test_gradients_that_pass_a_grid():
+    wide = dict(ldw=1 << 24, type=sb.SB_BF16)
+    assert ws_status(table(H=(1 << 24) - 512, **wide), B=1 << 10) == sb.SB_OK
+    assert ws_status(table(H=(1 << 24) - 8, **wide)) == sb.SB_ERR_UNSUPPORTED
+    assert ws_status(table(H=1 << 16, ldw=1 << 16), B=1 << 24) == sb.SB_ERR_UNSUPPORTED
+    assert ws_status(table(H=1 << 12, ldw=1 << 12), B=1 << 24) == sb.SB_OK

@@ -132,6 +132,27 @@ __device__ __forceinline__ Unit<bf16_t> load_at(const bf16_t *row, int c, int H)
 {
     return {*reinterpret_cast<const raw4 *>(row + (c < H ? c : 0))};
 }
+// Eight values, rounded to the type.
+__device__ __forceinline__ void store_unit(float *p, const float (&v)[8])
+{
+    raw4 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = __float_as_uint(v[e]);
+        b[e] = __float_as_uint(v[4 + e]);
+    }
+    reinterpret_cast<raw4 *>(p)[0] = a;
+    reinterpret_cast<raw4 *>(p)[1] = b;
+}
+__device__ __forceinline__ void store_unit(bf16_t *p, const float (&v)[8])
+{
+    half8 h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[e] = (__bf16)v[e];
+    *reinterpret_cast<half8 *>(p) = h;
+}
+
 // The first n of eight values, rounded to the type.
 __device__ __forceinline__ void store_words(uint32_t *p, const raw4 &w, int n)
 {

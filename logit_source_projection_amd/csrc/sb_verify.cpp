@@ -16,7 +16,7 @@ constexpr int64_t kMostGroups = 1 << 24;  // workgroups that a launch stays belo
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int64_t chunks_of(int32_t V) { return ((int64_t)V + sbk::kVerifyChunk - 1) / sbk::kVerifyChunk; }
+int64_t chunks_of(int32_t V, int columns = sbk::kVerifyChunk) { return ((int64_t)V + columns - 1) / columns; }
 
 sb_status check(const sb_drafts_desc *d)
 {
@@ -39,25 +39,30 @@ sb_status check(const sb_drafts_desc *d)
         (d->draft && sbk::spans_addresses(d->drafts, d->ldd, bytes)))
         return SB_ERR_UNSUPPORTED;
     // (each factor below 2^32, and the first two together below 2^24)
-    if ((int64_t)d->N * (2 * (int64_t)d->K + 1) >= kMostGroups ||
+    if ((int64_t)d->N * chunks_of(d->V, sbk::kVerifyDraw) >= kMostGroups ||
+        (int64_t)d->N * (2 * (int64_t)d->K + 1) >= kMostGroups ||
         (int64_t)d->N * (2 * (int64_t)d->K + 1) * chunks_of(d->V) >= kMostGroups)
         return SB_ERR_UNSUPPORTED;
     return SB_OK;
 }
 
+int64_t slots_of(const sb_drafts_desc *d) { return (d->draft ? 2 : 1) * (int64_t)d->K + 1; }
+
 struct Layout {
-    size_t parts = 0, rest = 0, made = 0, total = 0;
+    size_t parts = 0, made = 0, rest = 0, done = 0, total = 0;
 };
 
 Layout layout(const sb_drafts_desc *d)
 {
     Layout L;
     const size_t rows = (size_t)d->N * chunks_of(d->V);
-    size_t at = up(rows * (2 * (size_t)d->K + 1) * sizeof(sbk::RowPart), kRegionAlign);
-    L.rest = at;
-    at = up(at + rows * sizeof(double), kRegionAlign);
+    size_t at = up(rows * (size_t)slots_of(d) * sizeof(sbk::RowPart), kRegionAlign);
     L.made = at;
-    L.total = up(at + (size_t)d->N * sizeof(sbk::Decision), kRegionAlign);
+    at = up(at + (size_t)d->N * sizeof(sbk::Verdict), kRegionAlign);
+    L.rest = at;
+    at = up(at + (size_t)d->N * chunks_of(d->V, sbk::kVerifyDraw) * 2 * sizeof(double), kRegionAlign);
+    L.done = at;
+    L.total = up(at + (size_t)d->N * sbk::kVerifyDone * sizeof(uint32_t), kRegionAlign);
     return L;
 }
 
@@ -112,11 +117,14 @@ sb_status sb_verify_drafts(const sb_drafts_desc *desc, const float *u, const flo
     a.K = desc->K;
     a.V = desc->V;
     a.drafts = desc->drafts;
+    a.slots = (int32_t)slots_of(desc);
     a.chunks = (int32_t)chunks_of(desc->V);
+    a.draws = (int32_t)chunks_of(desc->V, sbk::kVerifyDraw);
     a.bf16 = desc->type == SB_BF16;
     a.parts = reinterpret_cast<sbk::RowPart *>(base + L.parts);
+    a.made = reinterpret_cast<sbk::Verdict *>(base + L.made);
     a.rest = reinterpret_cast<double *>(base + L.rest);
-    a.made = reinterpret_cast<sbk::Decision *>(base + L.made);
+    a.done = reinterpret_cast<uint32_t *>(base + L.done);
     a.out = out;
     a.ldo = ldo;
     a.accepted = accepted;

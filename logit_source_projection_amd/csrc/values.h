@@ -221,5 +221,36 @@ __device__ __forceinline__ float lanes_sum(float v)
 
 __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
+template <int CONTROL>
+__device__ __forceinline__ double dpp(double v)
+{
+    return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), CONTROL, 0xF, 0xF, true),
+                            __builtin_amdgcn_mov_dpp(__double2loint(v), CONTROL, 0xF, 0xF, true));
+}
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// The larger, NaN where one is.
+__device__ __forceinline__ float most_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+__device__ __forceinline__ float wave_most(float v)
+{
+    v = most_of(v, dpp<0xB1>(v));
+    v = most_of(v, dpp<0x4E>(v));
+    v = most_of(v, dpp<0x141>(v));
+    v = most_of(v, dpp<0x140>(v));
+    v = most_of(v, __shfl_xor(v, 16));
+    return most_of(v, __shfl_xor(v, 32));
+}
+
 }  // namespace
 }  // namespace sbk

@@ -17,6 +17,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "values.h"
 #include "verify_place.h"
 
@@ -24,38 +26,76 @@ namespace sbk {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kUnits = kVerifyChunk / (8 * kThreads);  // units of 8 columns per thread
+constexpr int kMostJudges = 16;  // waves of a sequence's verdict
 
 // How the token behind the accepted ones is found.
 enum How : int {
-    kDone = 0,      // written already (greedy, or no distribution)
+    kDone = 0,      // greedy, or no distribution
     kRow = 1,       // drawn from p
     kLess = 2,      // drawn from max(p - q, 0)
     kWithout = 3    // drawn from p without the rejected token (no draft logits)
 };
 
-// exp of x <= 0 (0 of -inf and NaN): x = k ln 2 + r, exp(r) by its Taylor series to
-// r^11 / 11!, whose rest is below 0.3466^12 / 12! = 6e-15 of the value.
-__device__ __forceinline__ double exp_of(double x)
+// 2^f of -1/2 <= f <= 1/2, exactly 1 of 0: 1 + f g(f), g through (2^f - 1) / f at the 9
+// Chebyshev nodes; off by 3.7e-14 of it.
+__device__ __forceinline__ double power_within(double f)
 {
-    x = fmax(x, -800.0);
-    const double k = rint(x * 1.4426950408889634074);
-    double r = fma(k, -0.693147180559945286227, x);
-    r = fma(k, -2.319046813846299558e-17, r);
-    double e = 1.0 / 39916800;
-    e = fma(e, r, 1.0 / 3628800);
-    e = fma(e, r, 1.0 / 362880);
-    e = fma(e, r, 1.0 / 40320);
-    e = fma(e, r, 1.0 / 5040);
-    e = fma(e, r, 1.0 / 720);
-    e = fma(e, r, 1.0 / 120);
-    e = fma(e, r, 1.0 / 24);
-    e = fma(e, r, 1.0 / 6);
-    e = fma(e, r, 0.5);
-    e = fma(e, r, 1.0);
-    e = fma(e, r, 1.0);
-    return ldexp(e, (int)k);
+    double e = 1.02031210633917290e-07;
+    e = fma(e, f, 1.32552248786688168e-06);
+    e = fma(e, f, 1.52526868462677196e-05);
+    e = fma(e, f, 1.54034558524538382e-04);
+    e = fma(e, f, 1.33335581790431116e-03);
+    e = fma(e, f, 9.61812915940255843e-03);
+    e = fma(e, f, 5.55041086647604237e-02);
+    e = fma(e, f, 2.40226506958129887e-01);
+    e = fma(e, f, 6.93147180559945286e-01);
+    return fma(e, f, 1.0);
 }
+
+// 2^t of t <= 1, 0 of -inf and NaN.
+__device__ __forceinline__ double power_of(double t)
+{
+    t = fmax(t, -1100.0);
+    const double k = rint(t);
+    return ldexp(power_within(t - k), (int)k);
+}
+
+// The powers 2^(z rate - C) of a row's or a chunk's logits, whose largest is `most`, with C
+// the whole number next to most rate: then a logit takes 16 64-bit instructions.  Its
+// product with the rate, less C and rounded to a whole number k by the size of 3 2^51, and
+// the rest after k, are one fused multiply-add each, and k is the low word.  Logits whose
+// power is 0 anyway are raised to one that still is (so is -inf).  Far out, where k would
+// not fit, the powers are 2^((z - most) rate).
+struct Powers {
+    double rate, back, off;  // off: by how much the exponent is more than (z - most) rate
+    float most, low;
+    bool far;
+    __device__ __forceinline__ Powers(float largest, double r)
+    {
+        most = largest;
+        rate = r;
+        const double at = (double)most * rate;
+        far = !(fabs(at) < 1073741824.0 && rate > 1e-30);
+        const double C = far ? 0.0 : rint(at);
+        back = 6755399441055744.0 - C;
+        off = far ? 0.0 : fma((double)most, rate, -C);
+        low = (float)fmax((double)most - 1200.0 / rate, -3.4028234663852886e38);
+    }
+    template <bool FAR>
+    __device__ __forceinline__ double of(float z) const
+    {
+        if (FAR)
+            return power_of(((double)z - (double)most) * rate);
+        const double x = (double)most_of(z, low), k = fma(x, rate, back);
+        return ldexp(power_within(fma(x, rate, back - k)), __double2loint(k));
+    }
+    __device__ __forceinline__ double of(float z) const { return far ? of<true>(z) : of<false>(z); }
+    // the factor from the powers of another largest logit to these
+    __device__ __forceinline__ double from(const Powers &o) const
+    {
+        return power_of(((double)o.most - (double)most) * rate + (off - o.off));
+    }
+};
 
 // The order of the argmax: NaN above every number, then larger values, then lower
 // columns (the projection calls' order).
@@ -75,28 +115,6 @@ __device__ __forceinline__ void take_better(float &v, int &i, float v2, int i2)
     }
 }
 
-// The larger, NaN where one is.
-__device__ __forceinline__ float most_of(float a, float b)
-{
-    return a != a ? a : b != b ? b : fmaxf(a, b);
-}
-
-__device__ __forceinline__ float wave_most(float v)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v = most_of(v, __shfl_xor(v, d));
-    return v;
-}
-
-__device__ __forceinline__ double wave_sum(double v)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
 __device__ __forceinline__ void wave_best(float &v, int &i)
 {
 #pragma unroll
@@ -104,11 +122,11 @@ __device__ __forceinline__ void wave_best(float &v, int &i)
         take_better(v, i, __shfl_xor(v, d), __shfl_xor(i, d));
 }
 
-// A sequence's place and temperature.
+// A sequence's place and temperature: exp(z / t) is 2^(z rate).
 struct Sequence {
     int first, count;
     bool greedy;
-    double scale;  // 1 / temperature
+    double rate;
     __device__ __forceinline__ Sequence(const VerifyArgs &a, int i)
     {
         const Place place = place_of(a.offsets[i], a.offsets[i + 1], a.drafts, a.K);
@@ -116,7 +134,7 @@ struct Sequence {
         count = place.count;
         const float t = a.temperature ? a.temperature[i] : 1.f;
         greedy = !(t > 0.f);
-        scale = greedy ? 1.0 : 1.0 / (double)t;
+        rate = 1.4426950408889634074 / (greedy ? 1.0 : (double)t);
     }
     // rows of the matrices
     __device__ __forceinline__ int64_t target(int i, int j) const { return (int64_t)first + i + j; }
@@ -125,152 +143,214 @@ struct Sequence {
 
 __device__ __forceinline__ RowPart *parts_of(const VerifyArgs &a, int i, int slot)
 {
-    return a.parts + ((int64_t)i * (2 * a.K + 1) + slot) * a.chunks;
+    return a.parts + ((int64_t)i * a.slots + slot) * a.chunks;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_chunk(const void *rows, int64_t ld, int64_t row, int c0, int V,
-                                           Unit<T> (&v)[kUnits])
-{
-    const T *p = static_cast<const T *>(rows) + row * ld;
+// COLUMNS of a row, 8 to a thread at a time and neighbours in neighbouring threads.
+// Those behind the last are -inf, which no sum and no draw sees.
+template <typename T, int COLUMNS>
+struct Chunk {
+    static constexpr int kUnits = COLUMNS / (8 * kThreads);
+    Unit<T> raw[kUnits];
+    __device__ __forceinline__ static int column(int k) { return 8 * (k * kThreads + (int)threadIdx.x); }
+    // from p, which `left` columns are there of
+    __device__ __forceinline__ void load(const T *p, int left)
+    {
+        if (left >= COLUMNS) {
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int c = c0 + 8 * (i * kThreads + (int)threadIdx.x);
-        if (c < V)
-            v[i] = load_some(p + c, V - c);
-        else
-            clear(v[i]);
+            for (int k = 0; k < kUnits; ++k)
+                raw[k] = load_unit(p + column(k));
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k)
+            raw[k] = load_at(p, column(k), left);
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k)
+            fill(raw[k], left - column(k));
     }
+    __device__ __forceinline__ static void fill(Unit<float> &u, int n)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            (e < 4 ? u.a : u.b)[e & 3] = e < n ? (e < 4 ? u.a : u.b)[e & 3] : 0xFF800000u;
+    }
+    __device__ __forceinline__ static void fill(Unit<bf16_t> &u, int n)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u.a[e] = 2 * e + 1 < n ? u.a[e] : 2 * e < n ? (u.a[e] & 0xFFFFu) | 0xFF800000u : 0xFF80FF80u;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const T *row_at(const void *rows, int64_t ld, int64_t row, int c0)
+{
+    return static_cast<const T *>(rows) + row * ld + c0;
 }
 
 // ---------------------------------------------------------------------------
-// Every chunk of every row that a sequence may need.
+// Every chunk of every row that a sequence may need: the largest logit, and the sum of
+// the powers or, of a greedy sequence, the largest logit's column.  As many workgroups
+// as are resident take one chunk after the other, the next one's loads under way while
+// the powers of one are summed: the 64-bit instructions for a logit take two
+// thirds of the time that its 4 bytes take.
 // ---------------------------------------------------------------------------
+constexpr uint32_t kRowGroups = 1024;
+
+// A chunk to take: workgroup's items number, ... (none: to is NULL)
 template <typename T>
-__global__ __launch_bounds__(kThreads) void verify_rows_kernel(const VerifyArgs a)
+struct Item {
+    RowPart *to;
+    const T *from;
+    int left, c0;
+    bool greedy;
+    double rate;
+};
+
+// The first item from `at` on, in steps, that a sequence may need; `at` moves to it.
+template <typename T>
+__device__ __forceinline__ Item<T> next_item(const VerifyArgs &a, uint32_t &at, uint32_t items)
+{
+    const uint32_t each = (uint32_t)a.slots * (uint32_t)a.chunks;
+    Item<T> item = {};
+    for (; at < items; at += gridDim.x) {
+        const int i = (int)(at / each), rest = (int)(at % each);
+        const int slot = rest / a.chunks, chunk = rest % a.chunks;
+        const Sequence s(a, i);
+        const bool is_draft = slot > a.K;
+        // rows that are not there, and draft rows that nothing asks for
+        if (is_draft ? slot - a.K - 1 >= s.count || s.greedy : slot > s.count)
+            continue;
+        item.to = parts_of(a, i, slot) + chunk;
+        item.c0 = chunk * kVerifyChunk;
+        item.left = a.V - item.c0;
+        item.from = is_draft ? row_at<T>(a.draft, a.ldd, s.draft(slot - a.K - 1), item.c0)
+                             : row_at<T>(a.target, a.ldt, s.target(i, slot), item.c0);
+        item.greedy = s.greedy;
+        item.rate = s.rate;
+        break;
+    }
+    return item;
+}
+
+template <bool FAR, typename PART>
+__device__ __forceinline__ double sum_of_powers(const PART &part, const Powers &powers)
+{
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < PART::kUnits; ++k) {
+        float v[8];
+        values_of(part.raw[k], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum += powers.of<FAR>(v[e]);
+    }
+    return sum;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads, 4) void verify_rows_kernel(const VerifyArgs a, uint32_t items)
 {
     __shared__ float mosts[kWaves];
     __shared__ double sums[kWaves];
     __shared__ int ats[kWaves];
-    const int chunk = blockIdx.x % a.chunks;
-    const int slots = 2 * a.K + 1;
-    const int i = blockIdx.x / a.chunks / slots, slot = blockIdx.x / a.chunks % slots;
-    const Sequence s(a, i);
-    const bool is_draft = slot > a.K;
-    // rows that are not there, and draft rows that nothing asks for
-    if (is_draft ? slot - a.K - 1 >= s.count || !a.draft || s.greedy : slot > s.count)
-        return;
-    const int c0 = chunk * kVerifyChunk, V = a.V;
+    typedef Chunk<T, kVerifyChunk> Part;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    Unit<T> raw[kUnits];
-    if (is_draft)
-        load_chunk<T>(a.draft, a.ldd, s.draft(slot - a.K - 1), c0, V, raw);
-    else
-        load_chunk<T>(a.target, a.ldt, s.target(i, slot), c0, V, raw);
-    RowPart &to = parts_of(a, i, slot)[chunk];
-    if (s.greedy) {
-        float best = -INFINITY;
-        int at = INT_MAX;
+    uint32_t at = blockIdx.x;
+    Item<T> item = next_item<T>(a, at, items);
+    Part next;
+    if (item.to)
+        next.load(item.from, item.left);
+    while (item.to) {
+        const Item<T> now = item;
+        const Part part = next;
+        at += gridDim.x;
+        item = next_item<T>(a, at, items);
+        float most = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
+        for (int k = 0; k < Part::kUnits; ++k) {
             float v[8];
-            values_of(raw[k], v);
-            const int c = c0 + 8 * (k * kThreads + (int)threadIdx.x);
+            values_of(part.raw[k], v);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (c + e < V)
-                    take_better(best, at, v[e], c + e);
+                most = most_of(most, v[e]);
         }
-        wave_best(best, at);
-        if (lane == 0) {
-            mosts[wave] = best;
-            ats[wave] = at;
+        if (item.to)
+            next.load(item.from, item.left);
+        most = wave_most(most);
+        if (lane == 0)
+            mosts[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            most = most_of(most, mosts[w]);
+        if (now.greedy) {
+            // the lowest column that is a NaN, or else equals the largest (columns behind
+            // the last come after those that are there)
+            int low = INT_MAX;
+#pragma unroll
+            for (int k = Part::kUnits - 1; k >= 0; --k) {
+                float v[8];
+                values_of(part.raw[k], v);
+#pragma unroll
+                for (int e = 7; e >= 0; --e)
+                    if (most != most ? v[e] != v[e] : v[e] == most)
+                        low = Part::column(k) + e;
+            }
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1)
+                low = min(low, __shfl_xor(low, d));
+            if (lane == 0)
+                ats[wave] = low;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    low = min(low, ats[w]);
+                now.to->most = most;
+                now.to->at = now.c0 + low;
+            }
+            continue;
         }
+        if (most == INFINITY)
+            most = NAN;
+        double sum = 0.0;
+        if (most > -INFINITY) {
+            const Powers powers(most, now.rate);
+            sum = powers.far ? sum_of_powers<true>(part, powers) : sum_of_powers<false>(part, powers);
+        }
+        sum = wave_sum(sum);
+        if (lane == 0)
+            sums[wave] = sum;
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int w = 1; w < kWaves; ++w)
-                take_better(best, at, mosts[w], ats[w]);
-            to.most = best;
-            to.at = at;
+                sum += sums[w];
+            now.to->sum = sum;
+            now.to->most = most;
         }
-        return;
-    }
-    float most = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        float v[8];
-        values_of(raw[k], v);
-        const int c = c0 + 8 * (k * kThreads + (int)threadIdx.x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < V)
-                most = v[e] < INFINITY ? most_of(most, v[e]) : NAN;
-    }
-    most = wave_most(most);
-    if (lane == 0)
-        mosts[wave] = most;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-        most = most_of(most, mosts[w]);
-    double sum = 0.0;
-    if (most > -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            float v[8];
-            values_of(raw[k], v);
-            const int c = c0 + 8 * (k * kThreads + (int)threadIdx.x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double x = exp_of(((double)v[e] - (double)most) * s.scale);
-                sum += c + e < V ? x : 0.0;
-            }
-        }
-    }
-    sum = wave_sum(sum);
-    if (lane == 0)
-        sums[wave] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWaves; ++w)
-            sum += sums[w];
-        to.sum = sum;
-        to.most = most;
     }
 }
 
-// A row's softmax: p(v) = exp((z - most) scale) / sum.  `there` is false where the row
-// has no distribution.
-struct Softmax {
-    float most;
-    double over;  // 1 / sum
-    bool there;
-    __device__ __forceinline__ double of(float z, double scale) const
-    {
-        return exp_of(((double)z - (double)most) * scale) * over;
-    }
-    // the part of a chunk
-    __device__ __forceinline__ double part(const RowPart &r, double scale) const
-    {
-        return r.most > -INFINITY ? r.sum * exp_of(((double)r.most - (double)most) * scale) * over : 0.0;
-    }
-};
-
+__device__ __forceinline__ bool there(const Softmax &s) { return s.most > -INFINITY; }
 // From the row's chunks, by one wave.
-__device__ __forceinline__ Softmax softmax_of(const RowPart *parts, int chunks, double scale)
+__device__ __forceinline__ Softmax softmax_of(const RowPart *parts, int chunks, double rate)
 {
     const int lane = threadIdx.x & 63;
-    float most = -INFINITY;
-    for (int c = lane; c < chunks; c += 64)
+    // (the first 64 chunks are read once)
+    const RowPart none = {0.0, -INFINITY, 0}, first = lane < chunks ? parts[lane] : none;
+    float most = first.most;
+    for (int c = lane + 64; c < chunks; c += 64)
         most = most_of(most, parts[c].most);
-    most = wave_most(most);
-    Softmax s{most, 0.0, most > -INFINITY};
-    if (!s.there)
+    Softmax s{0.0, wave_most(most)};
+    if (!there(s))
         return s;
-    double sum = 0.0;
-    for (int c = lane; c < chunks; c += 64)
+    const Powers powers(s.most, rate);
+    double sum = first.most > -INFINITY ? first.sum * powers.from(Powers(first.most, rate)) : 0.0;
+    for (int c = lane + 64; c < chunks; c += 64)
         if (parts[c].most > -INFINITY)
-            sum += parts[c].sum * exp_of(((double)parts[c].most - (double)most) * scale);
+            sum += parts[c].sum * powers.from(Powers(parts[c].most, rate));
     s.over = 1.0 / wave_sum(sum);
     return s;
 }
@@ -286,153 +366,79 @@ __device__ __forceinline__ int best_of(const RowPart *parts, int chunks)
     return at;
 }
 
+// ---------------------------------------------------------------------------
+// What becomes of a sequence, a workgroup each: the first row that rejects its draft (the
+// row behind the last draft always does), a row per wave at a time.
+// ---------------------------------------------------------------------------
+// What a wave finds about row j: `accepted` is whether its draft is, `how` and `next` tell
+// how the token is found where it is not.
 template <typename T>
-__device__ __forceinline__ float logit(const void *rows, int64_t ld, int64_t row, int v)
+__device__ __forceinline__ Verdict judge(const VerifyArgs &a, const Sequence &s, int i, int j, int &next)
 {
-    return value_of(static_cast<const T *>(rows)[row * ld + v]);
+    Verdict d = {{0.0, NAN}, {0.0, NAN}, 0, kDone};
+    next = -1;
+    const bool drafted = j < s.count;
+    const int x = drafted ? a.tokens[s.first + j] : -1;
+    const bool inside = (uint32_t)x < (uint32_t)a.V;
+    if (s.greedy) {
+        next = best_of(parts_of(a, i, j), a.chunks);
+        d.accepted = drafted && next == x;
+        return d;
+    }
+    const bool both = drafted && a.draft;
+    const float z = inside ? value_of(*row_at<T>(a.target, a.ldt, s.target(i, j), x)) : -INFINITY;
+    const float y = inside && both ? value_of(*row_at<T>(a.draft, a.ldd, s.draft(j), x)) : -INFINITY;
+    const float u = drafted ? a.u[s.first + j] : 0.f;
+    d.p = softmax_of(parts_of(a, i, j), a.chunks, s.rate);
+    if (both)
+        d.q = softmax_of(parts_of(a, i, a.K + 1 + j), a.chunks, s.rate);
+    if (!there(d.p))
+        return d;
+    d.how = kRow;
+    if (!drafted)
+        return d;
+    const bool comparable = inside && (!both || there(d.q));
+    const double qx = both && comparable ? Powers(d.q.most, s.rate).of(y) * d.q.over : 1.0;
+    d.accepted = comparable && (double)u * qx < Powers(d.p.most, s.rate).of(z) * d.p.over;
+    if (both && there(d.q))
+        d.how = kLess;
+    else if (!both && inside)
+        d.how = kWithout;
+    return d;
 }
 
-// Whether draft j of a sequence is accepted, by one wave.
 template <typename T>
-__device__ __forceinline__ bool accepts(const VerifyArgs &a, const Sequence &s, int i, int j)
+__global__ __launch_bounds__(64 * kMostJudges) void verify_judge_kernel(const VerifyArgs a)
 {
-    const int x = a.tokens[s.first + j];
-    if ((uint32_t)x >= (uint32_t)a.V)
-        return false;
-    if (s.greedy)
-        return best_of(parts_of(a, i, j), a.chunks) == x;
-    const Softmax p = softmax_of(parts_of(a, i, j), a.chunks, s.scale);
-    if (!p.there)
-        return false;
-    const double px = p.of(logit<T>(a.target, a.ldt, s.target(i, j), x), s.scale);
-    double qx = 1.0;
-    if (a.draft) {
-        const Softmax q = softmax_of(parts_of(a, i, a.K + 1 + j), a.chunks, s.scale);
-        if (!q.there)
-            return false;
-        qx = q.of(logit<T>(a.draft, a.ldd, s.draft(j), x), s.scale);
-    }
-    return (double)a.u[s.first + j] * qx < px;
-}
-
-// What is left of the columns of a unit of row j, to draw from.
-template <typename T>
-struct Rest {
-    Softmax p, q;
-    double scale;
-    int how, without;
-    __device__ __forceinline__ void of(const Unit<T> &zs, const Unit<T> &ys, int c, int V, double (&r)[8]) const
-    {
-        // p and q are rounded before their difference: fused, equal ones would leave
-        // what the rounding of one took
-#pragma clang fp contract(off)
-        float z[8], y[8];
-        values_of(zs, z);
-        values_of(ys, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            r[e] = p.of(z[e], scale);
-            if (how == kLess)
-                r[e] = fmax(r[e] - q.of(y[e], scale), 0.0);
-            if (c + e >= V || (how == kWithout && c + e == without))
-                r[e] = 0.0;
-        }
-    }
-};
-
-// ---------------------------------------------------------------------------
-// One workgroup per sequence and chunk: what is accepted (each workgroup finds
-// that for itself, from the parts, four drafts at a time), and the sum of what is
-// left in the chunk.  Where the next token is drawn from a whole row, the rows'
-// parts hold that sum already.
-// ---------------------------------------------------------------------------
-template <typename T>
-__global__ __launch_bounds__(kThreads) void verify_rest_kernel(const VerifyArgs a)
-{
-    __shared__ int firsts[kWaves];
-    __shared__ double sums[kWaves];
-    const int i = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+    __shared__ int firsts[kMostJudges];
+    const int i = blockIdx.x, waves = blockDim.x >> 6;
     const Sequence s(a, i);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    int rejected = s.count;
-    for (int j = wave; j < s.count; j += kWaves)
-        if (!accepts<T>(a, s, i, j)) {
-            rejected = j;
+    int mine = INT_MAX, next = -1;
+    Verdict verdict;
+    for (int j = wave; j <= s.count; j += waves) {
+        verdict = judge<T>(a, s, i, j, next);
+        if (!verdict.accepted) {
+            mine = j;
             break;
         }
+    }
     if (lane == 0)
-        firsts[wave] = rejected;
+        firsts[wave] = mine;
     __syncthreads();
-    int j = s.count;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    int j = INT_MAX;
+    for (int w = 0; w < waves; ++w)
         j = min(j, firsts[w]);
-    const RowPart *row = parts_of(a, i, j);
-    const int x = j < s.count ? a.tokens[s.first + j] : -1;
-    Rest<T> rest;
-    rest.how = kRow;
-    rest.scale = s.scale;
-    rest.without = x;
-    if (s.greedy) {
-        rest.how = kDone;
-    } else {
-        rest.p = softmax_of(row, a.chunks, s.scale);
-        if (!rest.p.there) {
-            rest.how = kDone;
-        } else if (j < s.count) {
-            if (a.draft) {
-                rest.q = softmax_of(parts_of(a, i, a.K + 1 + j), a.chunks, s.scale);
-                if (rest.q.there)
-                    rest.how = kLess;
-            } else if ((uint32_t)x < (uint32_t)a.V) {
-                rest.how = kWithout;
-            }
-        }
-    }
-    if (chunk == 0) {
-        const int next = s.greedy ? best_of(row, a.chunks) : -1;
-        for (int k = threadIdx.x; k <= a.K; k += kThreads)
-            a.out[i * a.ldo + k] = k < j ? a.tokens[s.first + k] : k == j && rest.how == kDone ? next : -1;
-        if (threadIdx.x == 0) {
-            a.accepted[i] = j;
-            a.made[i] = Decision{j, rest.how};
-        }
-    }
-    if (rest.how == kDone)
+    if (mine != j)
         return;
-    const int c0 = chunk * kVerifyChunk;
-    double *to = a.rest + (int64_t)i * a.chunks + chunk;
-    if (rest.how == kRow || (rest.how == kWithout && (uint32_t)(x - c0) >= (uint32_t)kVerifyChunk)) {
-        if (threadIdx.x == 0)
-            *to = rest.p.part(row[chunk], s.scale);
-        return;
-    }
-    Unit<T> z[kUnits], y[kUnits];
-    load_chunk<T>(a.target, a.ldt, s.target(i, j), c0, a.V, z);
-    if (rest.how == kLess) {
-        load_chunk<T>(a.draft, a.ldd, s.draft(j), c0, a.V, y);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-            clear(y[k]);
-    }
-    double sum = 0.0;
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        double r[8];
-        rest.of(z[k], y[k], c0 + 8 * (k * kThreads + (int)threadIdx.x), a.V, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum += r[e];
-    }
-    sum = wave_sum(sum);
-    if (lane == 0)
-        sums[wave] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWaves; ++w)
-            sum += sums[w];
-        *to = sum;
+    // the wave of that row writes the sequence's results
+    for (int k = lane; k <= a.K; k += 64)
+        a.out[i * a.ldo + k] = k < j ? a.tokens[s.first + k] : k == j ? next : -1;
+    if (lane == 0) {
+        verdict.accepted = j;
+        a.accepted[i] = j;
+        a.made[i] = verdict;
+        a.done[(int64_t)i * kVerifyDone] = 0;
     }
 }
 
@@ -449,138 +455,211 @@ __device__ __forceinline__ double wave_upto(double v)
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup per sequence: the chunk whose cumulative sum passes the random
-// number's share of the whole, then the column in it.
+// The draw: a workgroup per sequence and kVerifyDraw columns sums up what is left of
+// them.  The last of a sequence's workgroups to be done (none waits for another) finds
+// the one whose cumulative sum passes the random number's share of the whole, then the
+// column.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ __launch_bounds__(kThreads) void verify_pick_kernel(const VerifyArgs a)
+struct Rest {
+    typedef Chunk<T, kVerifyDraw> Part;
+    Part z, y;
+    __device__ __forceinline__ void load(const VerifyArgs &a, const Sequence &s, const Verdict &d, int i, int c0)
+    {
+        z.load(row_at<T>(a.target, a.ldt, s.target(i, d.accepted), c0), a.V - c0);
+        if (d.how == kLess)
+            y.load(row_at<T>(a.draft, a.ldd, s.draft(d.accepted), c0), a.V - c0);
+    }
+    // A unit's shares of p and what is left of them; x: the rejected token's column, from
+    // these columns' first on.  (Whether powers are far out is asked once: eight
+    // of them run side by side.)
+    __device__ __forceinline__ void find(const Verdict &d, const Powers &ps, const Powers &qs, int x, int k,
+                                         double (&p)[8], double (&r)[8]) const
+    {
+        if (ps.far || (d.how == kLess && qs.far))
+            find_as<true>(d, ps, qs, x, k, p, r);
+        else
+            find_as<false>(d, ps, qs, x, k, p, r);
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void find_as(const Verdict &d, const Powers &ps, const Powers &qs, int x, int k,
+                                            double (&p)[8], double (&r)[8]) const
+    {
+        // p and q are rounded before their difference: fused, equal ones would leave
+        // what the rounding of one took
+#pragma clang fp contract(off)
+        float v[8];
+        values_of(z.raw[k], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            p[e] = (FAR ? ps.of(v[e]) : ps.of<false>(v[e])) * d.p.over;
+        if (d.how == kLess) {
+            values_of(y.raw[k], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                r[e] = fmax(p[e] - (FAR ? qs.of(v[e]) : qs.of<false>(v[e])) * d.q.over, 0.0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                r[e] = d.how == kWithout && Part::column(k) + e == x ? 0.0 : p[e];
+        }
+    }
+};
+
+__device__ __forceinline__ double sum_of(const double (&v)[8])
 {
-    __shared__ double unit_sums[kUnits][kWaves];
-    __shared__ int found, last;
-    const int i = blockIdx.x;
-    const Decision d = a.made[i];
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs a)
+{
+    typedef typename Rest<T>::Part Part;
+    constexpr int kUnits = Part::kUnits;
+    __shared__ double sums[2][kUnits][kWaves];
+    __shared__ int token, last;
+    __shared__ bool draws;
+    const int i = blockIdx.x / a.draws, mine = blockIdx.x % a.draws;
+    const Verdict d = a.made[i];
+    const Sequence s(a, i);
     if (d.how == kDone)
         return;
-    const Sequence s(a, i);
-    const int j = d.accepted;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const RowPart *row = parts_of(a, i, j);
-    Rest<T> rest;
-    rest.how = d.how;
-    rest.scale = s.scale;
-    rest.without = d.how == kWithout ? a.tokens[s.first + j] : -1;
-    rest.p = softmax_of(row, a.chunks, s.scale);
-    if (d.how == kLess)
-        rest.q = softmax_of(parts_of(a, i, a.K + 1 + j), a.chunks, s.scale);
-    const double *sums = a.rest + (int64_t)i * a.chunks;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = d.accepted;
+    const int x = d.how == kWithout ? a.tokens[s.first + j] : -1;
     const float u = a.u_next[i];
-    // Every wave looks for the chunk by itself.  Where nothing is left, the row itself
-    // is drawn from.
-    int chunk = 0;
-    double before = 0.0, goal = 0.0;
-    for (int pass = 0; pass < 2; ++pass) {
-        const bool whole = pass == 1;
-        if (whole)
-            rest.how = kRow;
-        double total = 0.0;
-        for (int c0 = 0; c0 < a.chunks; c0 += 64) {
-            const int c = c0 + lane;
-            total += wave_sum(c < a.chunks ? whole ? rest.p.part(row[c], s.scale) : sums[c] : 0.0);
+    double *rests = a.rest + (int64_t)i * a.draws * 2;
+    const Powers ps(d.p.most, s.rate), qs(d.q.most, s.rate);
+    Rest<T> rest;
+    rest.load(a, s, d, i, mine * kVerifyDraw);
+    double left = 0.0, whole = 0.0, p[8], r[kUnits][8];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+        rest.find(d, ps, qs, x - mine * kVerifyDraw, k, p, r[k]);
+        left += sum_of(r[k]);
+        whole += sum_of(p);
+    }
+    left = wave_sum(left);
+    whole = wave_sum(whole);
+    if (lane == 0) {
+        sums[0][0][wave] = left;
+        sums[1][0][wave] = whole;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWaves; ++w) {
+            left += sums[0][0][w];
+            whole += sums[1][0][w];
         }
+        // Written through to memory, complete before they are counted, and read from memory
+        // (device-scope atomics): no workgroup needs a fence, which writes back and
+        // empties its XCD's L2 (4800 of them took 80 us).
+        __hip_atomic_store(&rests[2 * mine], left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&rests[2 * mine + 1], whole, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_waitcnt(0);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        draws = __hip_atomic_fetch_add(&a.done[(int64_t)i * kVerifyDone], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+                (uint32_t)a.draws;
+        token = INT_MAX;
+        last = -1;
+    }
+    __syncthreads();
+    if (!draws)
+        return;
+    // Every wave looks for the columns' workgroup by itself.  Where nothing is left, p is
+    // drawn from.
+    int from = 0, at = 0;
+    double before = 0.0, goal = 0.0;
+    for (; from < 2; ++from) {
+        auto weight = [&](int c) {
+            return c < a.draws ? __hip_atomic_load(&rests[2 * c + from], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                               : 0.0;
+        };
+        const double first = weight(lane);  // (read once)
+        double total = wave_sum(first);
+        for (int c0 = 64; c0 < a.draws; c0 += 64)
+            total += wave_sum(weight(c0 + lane));
         if (!(total > 0.0))
             continue;
         // (a number outside [0, 1) draws the first or the last column)
         goal = (u > 0.f ? (double)u : 0.0) * total;
         double upto = 0.0;
-        chunk = -1;
-        for (int c0 = 0; c0 < a.chunks; c0 += 64) {
-            const int c = c0 + lane;
-            const double v = c < a.chunks ? whole ? rest.p.part(row[c], s.scale) : sums[c] : 0.0;
-            const double mine = upto + wave_upto(v);
-            const uint64_t past = __ballot(v > 0.0 && mine > goal), some = __ballot(v > 0.0);
-            // the first chunk past the goal, else the last one with anything left
-            const int at = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
-            if (at >= 0) {
-                chunk = c0 + at;
-                before = __shfl(mine, at) - __shfl(v, at);
+        for (int c0 = 0; c0 < a.draws; c0 += 64) {
+            const double v = c0 == 0 ? first : weight(c0 + lane), to = upto + wave_upto(v);
+            const uint64_t past = __ballot(v > 0.0 && to > goal), some = __ballot(v > 0.0);
+            // the first past the goal, else the last with anything left
+            const int one = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
+            if (one >= 0) {
+                at = c0 + one;
+                before = __shfl(to, one) - __shfl(v, one);
             }
             if (past)
                 break;
-            upto = __shfl(mine, 63);
+            upto = __shfl(to, 63);
         }
         break;
     }
-    if (threadIdx.x == 0) {
-        found = INT_MAX;
-        last = -1;
-    }
-    const int c0 = chunk * kVerifyChunk;
-    Unit<T> z[kUnits], y[kUnits];
-    load_chunk<T>(a.target, a.ldt, s.target(i, j), c0, a.V, z);
-    if (rest.how == kLess) {
-        load_chunk<T>(a.draft, a.ldd, s.draft(j), c0, a.V, y);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-            clear(y[k]);
-    }
-    double r[kUnits][8], upto[kUnits];
+    rest.load(a, s, d, i, at * kVerifyDraw);
+    double upto[kUnits];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-        rest.of(z[k], y[k], c0 + 8 * (k * kThreads + (int)threadIdx.x), a.V, r[k]);
-        double sum = 0.0;
+        rest.find(d, ps, qs, x - at * kVerifyDraw, k, p, r[k]);
+        if (from > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sum += r[k][e];
+            for (int e = 0; e < 8; ++e)
+                r[k][e] = p[e];
+        }
+        const double sum = sum_of(r[k]);
         upto[k] = wave_upto(sum);
         if (lane == 63)
-            unit_sums[k][wave] = upto[k];
+            sums[0][k][wave] = upto[k];
         upto[k] -= sum;
     }
     __syncthreads();
-    int mine = INT_MAX, behind = -1;
+    int past = INT_MAX, behind = -1;
     double base = before;
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
+        double mass = base + upto[k];
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            if (w == wave) {
-                double sum = base + upto[k];
-                const int c = c0 + 8 * (k * kThreads + (int)threadIdx.x);
+            mass += w < wave ? sums[0][k][w] : 0.0;
+            base += sums[0][k][w];
+        }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sum += r[k][e];
-                    if (r[k][e] > 0.0) {
-                        behind = c + e;
-                        if (sum > goal && mine == INT_MAX)
-                            mine = c + e;
-                    }
-                }
+        for (int e = 0; e < 8; ++e) {
+            mass += r[k][e];
+            if (r[k][e] > 0.0) {
+                behind = Part::column(k) + e;
+                if (mass > goal && past == INT_MAX)
+                    past = behind;
             }
-            base += unit_sums[k][w];
         }
     }
-    if (mine != INT_MAX)
-        atomicMin(&found, mine);
+    if (past != INT_MAX)
+        atomicMin(&token, past);
     if (behind >= 0)
         atomicMax(&last, behind);
     __syncthreads();
     if (threadIdx.x == 0)
-        a.out[i * a.ldo + j] = found != INT_MAX ? found : last;
+        a.out[i * a.ldo + j] = at * kVerifyDraw + (token != INT_MAX ? token : last);
 }
 
 template <typename T>
 hipError_t verify(const VerifyArgs &a, hipStream_t s)
 {
-    const unsigned per = (unsigned)a.N * (unsigned)a.chunks;
-    hipLaunchKernelGGL((verify_rows_kernel<T>), dim3(per * (2 * a.K + 1)), dim3(kThreads), 0, s, a);
+    // as many items for each workgroup
+    const uint32_t items = (uint32_t)a.N * (uint32_t)a.chunks * (uint32_t)a.slots;
+    const uint32_t rounds = (items + kRowGroups - 1) / kRowGroups;
+    hipLaunchKernelGGL((verify_rows_kernel<T>), dim3((items + rounds - 1) / rounds), dim3(kThreads), 0, s, a, items);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((verify_rest_kernel<T>), dim3(per), dim3(kThreads), 0, s, a);
+    const int judges = std::min(a.K + 1, kMostJudges);
+    hipLaunchKernelGGL((verify_judge_kernel<T>), dim3((unsigned)a.N), dim3(64 * judges), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess)
         return e;
-    hipLaunchKernelGGL((verify_pick_kernel<T>), dim3((unsigned)a.N), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((verify_draw_kernel<T>), dim3((unsigned)a.N * (unsigned)a.draws), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -46,7 +46,8 @@ def ws_status(d):
     (dict(ldt=1 << 45), sb.SB_ERR_UNSUPPORTED), (dict(ldd=1 << 62), sb.SB_ERR_UNSUPPORTED),
     (dict(N=1 << 24), sb.SB_ERR_UNSUPPORTED), (dict(K=1 << 30), sb.SB_ERR_UNSUPPORTED),
     (dict(N=2 ** 31 - 1, K=2 ** 31 - 1, drafts=2 ** 31 - 1), sb.SB_ERR_UNSUPPORTED),
-    (dict(N=1 << 20, K=8), sb.SB_ERR_UNSUPPORTED), (dict(N=1 << 19, K=8), sb.SB_OK)])
+    (dict(N=1 << 20, K=8), sb.SB_ERR_UNSUPPORTED), (dict(N=1 << 24, K=0), sb.SB_ERR_UNSUPPORTED),
+    (dict(N=(1 << 22) + 5, K=1), sb.SB_OK), (dict(N=1 << 23, K=0, V=4097, ldt=8192, ldd=8192), sb.SB_ERR_UNSUPPORTED), (dict(N=1 << 19, K=8), sb.SB_OK)])
 def test_descriptor(kw, want):
     assert ws_status(desc(**kw)) == want
     if want != sb.SB_OK:

@@ -122,6 +122,46 @@ def test_gradient_of_whole_numbers(require_gpu, B, V, H, k, kind, add):
     assert bool((ws[n:] == 255).all()), "workspace"
 
 
+@pytest.mark.parametrize("B", [3000, 16384, 16385, 50000])
+@pytest.mark.parametrize("tokens", [[5, 261, 517], [5, 6, 261, 40000], list(range(3, 256 * 40, 256)), [0, 50256]])
+def test_tokens_that_fill_the_batch(require_gpu, tokens, B):
+    """A few tokens, some of them of one group of the sort, make most of the batch."""
+    V, H = 50257, 24
+    g = torch.Generator(device="cuda").manual_seed(B)
+    ids = torch.tensor(tokens, dtype=torch.int32, device="cuda")[torch.randint(0, len(tokens), (B,), device="cuda", generator=g)]
+    rare = torch.rand(B, device="cuda", generator=g) < 0.1
+    ids = torch.where(rare, make_ids("uniform", B, V, 1), ids)
+    dout = torch.randint(-8, 9, (B, H), device="cuda", generator=g).float()
+    dw = torch.empty(V, H, device="cuda")
+    sb.sb_embed_grad(sb.Table(dw, lanes(V, 5)), ids, dout)
+    assert torch.equal(dw, reference_grad(ids, dout, V, 1.0).float())
+
+
+@pytest.mark.parametrize("V", [256 * 4096, 256 * 4096 + 1, 3000017])
+def test_large_vocabularies(require_gpu, V):
+    ids = torch.cat([make_ids("uniform", 3000, V, 1), make_ids("padded", 500, V, 2), make_ids("one", 100, V, 3)])
+    dout = torch.randint(-8, 9, (len(ids), 16), device="cuda").float()
+    dw = torch.empty(V, 16, device="cuda")
+    sb.sb_embed_grad(sb.Table(dw, lanes(V, 3)), ids, dout)
+    assert torch.equal(dw, reference_grad(ids, dout, V, 1.0).float())
+
+
+def test_a_table_that_is_zeroed_in_turns(require_gpu):
+    """More than 2^31 16-byte chunks of zeros: a table of 33 GiB."""
+    V, H = 1 << 24, 528
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GiB of memory")
+    dw = torch.empty(V, H, device="cuda")
+    dw.fill_(1.0)
+    ids = torch.tensor([V - 1, 0, V - 2, V // 2, V - 1], dtype=torch.int32, device="cuda")
+    sb.sb_embed_grad(sb.Table(dw, [0, 5000000, V]), ids, torch.ones(5, H, device="cuda"))
+    rows = torch.cat([part.any(1) for part in dw.split(1 << 20)]).nonzero()[:, 0]
+    assert torch.equal(rows, ids.long().unique())
+    assert bool((dw[V - 1] == 2).all()) and bool((dw[[0, V - 2, V // 2]] == 1).all())
+    del dw
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("tt", [F, H16])
 @pytest.mark.parametrize("to", [F, H16])
 @pytest.mark.parametrize("B,V,H,k", [(700, 300, 264, 3), (5000, 20000, 40, 4), (300, 10, 5120, 2), (64, 4096, 8192, 1)])

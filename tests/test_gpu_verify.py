@@ -157,6 +157,23 @@ def test_flat_and_peaked_rows(require_gpu, spread, near):
     check(make([5, 5], 5, 151936, F, True, 32, spread, near, None))
 
 
+@pytest.mark.parametrize("dtype", [F, H16])
+def test_large_vocabularies_and_many_drafts(require_gpu, dtype):
+    """More chunks of a row than a wave has lanes, more rows than a verdict has waves."""
+    check(make([2, 0, 1], 2, 1000003, dtype, True, 51, temperature="mixed"))
+    check(make([1, 2], 2, 600000, dtype, False, 52, spread=0.0, temperature=None))
+    for near in (0.05, 0.5):
+        check(make([40, 33, 0, 17, 16, 15], 40, 3000, dtype, True, 53, near=near, temperature=0.9))
+    s = make([40, 33, 0, 17], 40, 9000, dtype, False, 54, temperature=0.0)
+    s["tokens"][60] = 5
+    assert check(s)[1][0] == 40
+
+
+def test_more_chunks_than_workgroups(require_gpu):
+    check(make([4] * 150, 4, 20000, H16, True, 55))
+    check(make([0] * 700, 0, 17000, F, False, 56))
+
+
 def test_more_drafts_than_allowed(require_gpu):
     check(make([6, 1, 9, 0], 4, 500, seed=3))
     check(make([3, 2], 0, 500, seed=4))

@@ -807,13 +807,14 @@ def sb_int8_logits(head, out, ws=None, stream=None):
 _TYPES = {torch.float32: SB_FP32, torch.bfloat16: SB_BF16}
 
 
-def _type_of(t, name):
-    """The sb_dtype code of a device tensor."""
+def _on_device(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dtype not in _TYPES:
-        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, not {t.dtype}")
-    return _TYPES[t.dtype]
+
+
+def _padded(n, size):
+    """n columns rounded up to whole 16-byte units."""
+    return -(-n * size // 16) * 16 // size
 
 
 def _row_stride(t):
@@ -821,9 +822,64 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), _padded(t.shape[1], t.element_size()))
 
 
-def _padded(n, size):
-    """n columns rounded up to whole 16-byte units."""
-    return -(-n * size // 16) * 16 // size
+# The checks below also give what the C ABI takes; `index` is the number of the device that
+# the call's other tensors are on, or None.  They are written out: at a few microseconds
+# a call, those of several tensors are what a small call waits for.
+def _rows(t, name, rows, cols, index=None, dtype=None):
+    """(type code, address, row stride) of a [>= rows, >= cols] matrix with unit column
+    stride, fp32 or bf16 or of the given type."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    code = _TYPES.get(t.dtype)
+    if code is None and dtype is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a [>= {rows}, >= {cols}] matrix with unit column stride")
+    (n, m), (s0, s1) = t.size(), t.stride()
+    if n < rows or m < cols or (m > 1 and s1 != 1):
+        raise ValueError(f"{name} must be a [>= {rows}, >= {cols}] matrix with unit column stride")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"tensors on different devices: cuda:{index} and {t.device}")
+    return code, t.data_ptr(), s0 if n > 1 else max(s0, _padded(m, t.element_size()))
+
+
+def _buffer(t, name, dtype, n, index=None):
+    """The address of a contiguous buffer of at least n elements (None of None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be contiguous with at least {n} elements")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"tensors on different devices: cuda:{index} and {t.device}")
+    return t.data_ptr()
+
+
+def _call(name, index, stream, fn, *args):
+    """fn(*args, stream) on device `index`, which is made current for it where it is not."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(name, index, stream, fn, *args)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        s = _stream_on(stream, torch.device("cuda", index))
+    _check(fn(*args, s), name)
+
+
+def _space(ws, nbytes_fn, index, stream):
+    """(address, bytes) of the caller's workspace or of one for this call, and the tensor
+    that holds it."""
+    if ws is None:
+        device = torch.device("cuda", index)
+        with _on(device):
+            ws = _workspace(nbytes_fn, None, device, stream)
+    return _buffer(ws, "ws", torch.uint8, 0, index), ws.numel(), ws
 
 
 class Norm:
@@ -835,7 +891,7 @@ class Norm:
                  x_ptr=None, weight_ptr=None, bias_ptr=None, param_type=None):
         self.x, self.weight, self.bias = x, weight, bias
         self.from_tensors = x_ptr is None
-        self._device = None
+        self._index = None
         one = weight if weight is not None else bias
         self.param_dtype = torch.float32 if one is None else one.dtype
         self.desc = sb_norm_desc(
@@ -858,34 +914,33 @@ class Norm:
     def ref(self):
         return ctypes.byref(self.desc)
 
-    def device(self):
-        """The one device of the operands (None for raw pointers).  The
+    def index(self):
+        """The number of the operands' one device (None for raw pointers).  The
         descriptor holds their addresses, so they are checked once."""
-        if self._device is None and self.from_tensors:
+        if self._index is None and self.from_tensors:
             d = self.desc
-            _type_of(self.x, "x")
-            _matrix(self.x, "x", self.x.dtype, d.B, d.H)
+            _rows(self.x, "x", d.B, d.H)
+            index = self.x.get_device()
             for t, name in ((self.weight, "weight"), (self.bias, "bias")):
                 if t is not None:
-                    _type_of(t, name)
-                    _vector(t, name, self.param_dtype, d.H)
-            self._device = _one_device([self.x, self.weight, self.bias])
-        return self._device
+                    _on_device(t, name)
+                    if t.dtype not in _TYPES:
+                        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, not {t.dtype}")
+                    _buffer(t, name, self.param_dtype, d.H, index)
+            self._index = index
+        return self._index
 
 
 def sb_layer_norm(norm, y, mean=None, rstd=None, stream=None):
     """y (fp32 or bf16 [B, H]) <- layer norm of the rows; mean and rstd (fp32
     [B], either optional) are what sb_layer_norm_grad takes.  Returns y."""
-    device = norm.device()
-    B, H = norm.B, norm.H
-    code = _type_of(y, "y")
-    _matrix(y, "y", y.dtype, B, H)
-    _vector(mean, "mean", torch.float32, B)
-    _vector(rstd, "rstd", torch.float32, B)
-    device = _one_device([y, mean, rstd], device)
-    with _on(device):
-        _check(lib().sb_layer_norm(norm.ref(), y.data_ptr(), code, _row_stride(y), _ptr(mean), _ptr(rstd),
-                                   _stream_on(stream, device)), "sb_layer_norm")
+    index = norm.index()
+    d = norm.desc
+    B = d.B
+    code, p, ld = _rows(y, "y", B, d.H, index)
+    mean = _buffer(mean, "mean", torch.float32, B, index)
+    rstd = _buffer(rstd, "rstd", torch.float32, B, index)
+    _call("sb_layer_norm", y.get_device(), stream, lib().sb_layer_norm, norm.ref(), p, code, ld, mean, rstd)
     return y
 
 
@@ -908,36 +963,31 @@ def sb_layer_norm_grad(norm, dy, mean, rstd, dx=None, dweight=None, dbias=None, 
     where there are none) <- the gradient of sum(dy * y), any of them optional.
     dy (fp32 or bf16 [B, H]) is of any type; mean and rstd are what
     sb_layer_norm returned.  Returns (dx, dweight, dbias)."""
-    device = norm.device()
-    B, H = norm.B, norm.H
-    code = _type_of(dy, "dy")
-    _matrix(dy, "dy", dy.dtype, B, H)
-    _vector(mean, "mean", torch.float32, B)
-    _vector(rstd, "rstd", torch.float32, B)
-    _matrix(dx, "dx", norm.x.dtype, B, H)
-    _vector(dweight, "dweight", norm.param_dtype, H)
-    _vector(dbias, "dbias", norm.param_dtype, H)
-    _vector(ws, "ws", torch.uint8, 0)
-    device = _one_device([dy, mean, rstd, dx, dweight, dbias, ws], device)
-
-    def call(p, n, s):
-        return lib().sb_layer_norm_grad(norm.ref(), dy.data_ptr(), code, _row_stride(dy), _ptr(mean),
-                                        _ptr(rstd), _ptr(dx), 0 if dx is None else _row_stride(dx),
-                                        _ptr(dweight), _ptr(dbias), p, n, s)
-
-    _run("sb_layer_norm_grad", device, stream, lambda: sb_layer_norm_grad_workspace_bytes(norm), ws, call)
+    index = norm.index()
+    d = norm.desc
+    B, H = d.B, d.H
+    code, pdy, lddy = _rows(dy, "dy", B, H, index)
+    index = dy.get_device()
+    mean = _buffer(mean, "mean", torch.float32, B, index)
+    rstd = _buffer(rstd, "rstd", torch.float32, B, index)
+    _, pdx, lddx = (None, None, 0) if dx is None else _rows(dx, "dx", B, H, index, norm.x.dtype)
+    pw = _buffer(dweight, "dweight", norm.param_dtype, H, index)
+    pb = _buffer(dbias, "dbias", norm.param_dtype, H, index)
+    pws, n, ws = _space(ws, lambda: sb_layer_norm_grad_workspace_bytes(norm), index, stream)
+    _call("sb_layer_norm_grad", index, stream, lib().sb_layer_norm_grad, norm.ref(), pdy, code, lddy, mean, rstd,
+          pdx, lddx, pw, pb, pws, n)
     return dx, dweight, dbias
 
 
 # ---------------------------------------------------------------------------
 # Embedding.
 # ---------------------------------------------------------------------------
-def _count(t, name, dtype):
-    """The elements of a contiguous device buffer, as the C ABI counts them."""
-    _vector(t, name, dtype, 0)
+def _counted(t, name, dtype, index=None):
+    """(elements, address) of a contiguous buffer, as the C ABI counts them."""
+    p = _buffer(t, name, dtype, 0, index)
     if t is None or t.numel() >= 1 << 31:
         raise ValueError(f"{name} must be a tensor of fewer than 2^31 elements")
-    return t.numel()
+    return t.numel(), p
 
 
 class Table:
@@ -950,7 +1000,7 @@ class Table:
     def __init__(self, w, lane_off=None, *, V=None, H=None, ldw=None, type=None, w_ptrs=None):
         self.w = w
         self.from_tensors = w_ptrs is None
-        self._device = None
+        self._index = None
         one = _as_list(w)[0]
         if lane_off is None:
             lane_off = [0]
@@ -987,34 +1037,32 @@ class Table:
     def ref(self):
         return ctypes.byref(self.desc)
 
-    def device(self):
-        """The one device of the table (None for raw pointers).  The descriptor
-        holds its addresses, so it is checked once."""
-        if self._device is None and self.from_tensors:
+    def index(self):
+        """The number of the table's one device (None for raw pointers).  The
+        descriptor holds its addresses, so it is checked once."""
+        if self._index is None and self.from_tensors:
             d, off, w = self.desc, self.lane_off, _as_list(self.w)
-            _type_of(w[0], "w")
             if isinstance(self.w, (list, tuple)):
                 for i, t in enumerate(w):
-                    _matrix(t, f"w[{i}]", w[0].dtype, off[i + 1] - off[i], d.H)
+                    if i == 0:
+                        _rows(t, "w[0]", off[1] - off[0], d.H)
+                    else:
+                        _rows(t, f"w[{i}]", off[i + 1] - off[i], d.H, w[0].get_device(), w[0].dtype)
                 if len({t.stride(0) for t in w if t.shape[0] > 1}) > 1:
                     raise ValueError("the tensors of w must have one row stride")
             else:
-                _matrix(self.w, "w", self.w.dtype, d.V, d.H)
-            self._device = _one_device(w)
-        return self._device
+                _rows(self.w, "w", d.V, d.H)
+            self._index = w[0].get_device()
+        return self._index
 
 
 def sb_embed(table, ids, out, scale=1.0, stream=None):
     """out (fp32 or bf16 [B, H]) <- scale times the table's rows that ids (int32
     [B]) name; zeros for a negative ID, NaN for one past the table.  Returns out."""
-    device = table.device()
-    B = _count(ids, "ids", torch.int32)
-    code = _type_of(out, "out")
-    _matrix(out, "out", out.dtype, B, table.H)
-    device = _one_device([ids, out], device)
-    with _on(device):
-        _check(lib().sb_embed(table.ref(), ids.data_ptr(), B, scale, out.data_ptr(), code, _row_stride(out),
-                              _stream_on(stream, device)), "sb_embed")
+    index = table.index()
+    B, pids = _counted(ids, "ids", torch.int32, index)
+    code, p, ld = _rows(out, "out", B, table.desc.H, index)
+    _call("sb_embed", out.get_device(), stream, lib().sb_embed, table.ref(), pids, B, scale, p, code, ld)
     return out
 
 
@@ -1037,15 +1085,13 @@ def sb_embed_grad(table, ids, dout, scale=1.0, accumulate=False, ws=None, stream
     (a Table of the gradient), all of whose rows are overwritten; with
     accumulate it is added to the rows that ids name.  dout (fp32 or bf16 [B, H])
     is of any type.  Returns the table's tensor or tensors."""
-    device = table.device()
-    B = _count(ids, "ids", torch.int32)
-    code = _type_of(dout, "dout")
-    _matrix(dout, "dout", dout.dtype, B, table.H)
-    _vector(ws, "ws", torch.uint8, 0)
-    device = _one_device([ids, dout, ws], device)
-    _run("sb_embed_grad", device, stream, lambda: sb_embed_grad_workspace_bytes(table, B, accumulate), ws,
-         lambda p, n, s: lib().sb_embed_grad(table.ref(), ids.data_ptr(), B, scale, dout.data_ptr(), code,
-                                             _row_stride(dout), int(bool(accumulate)), p, n, s))
+    index = table.index()
+    B, pids = _counted(ids, "ids", torch.int32, index)
+    code, p, ld = _rows(dout, "dout", B, table.desc.H, index)
+    index = dout.get_device()
+    add = int(bool(accumulate))
+    pws, n, ws = _space(ws, lambda: sb_embed_grad_workspace_bytes(table, B, accumulate), index, stream)
+    _call("sb_embed_grad", index, stream, lib().sb_embed_grad, table.ref(), pids, B, scale, p, code, ld, add, pws, n)
     return table.w
 
 
@@ -1064,7 +1110,7 @@ class Drafts:
     def __init__(self, target, tokens, offsets, max_drafts, draft=None, temperature=None):
         self.target, self.tokens, self.offsets = target, tokens, offsets
         self.draft, self.temperature = draft, temperature
-        self._device = None
+        self._index = None
         self.desc = sb_drafts_desc(
             N=max(0, offsets.numel() - 1), K=int(max_drafts), V=target.shape[1], drafts=tokens.numel(),
             offsets=offsets.data_ptr(), tokens=tokens.data_ptr(), target=target.data_ptr(),
@@ -1083,23 +1129,22 @@ class Drafts:
     def ref(self):
         return ctypes.byref(self.desc)
 
-    def device(self):
-        """The one device of the operands.  The descriptor holds their addresses,
-        so they are checked once."""
-        if self._device is None:
-            d = self.desc
-            _type_of(self.target, "target")
-            drafts = _count(self.tokens, "tokens", torch.int32)
-            if _count(self.offsets, "offsets", torch.int32) < 1:
+    def index(self):
+        """The number of the operands' one device.  The descriptor holds their
+        addresses, so they are checked once."""
+        if self._index is None:
+            d, t = self.desc, self.target
+            _rows(t, "target", 0, d.V)
+            index = t.get_device()
+            drafts, _ = _counted(self.tokens, "tokens", torch.int32, index)
+            if _counted(self.offsets, "offsets", torch.int32, index)[0] < 1:
                 raise ValueError("offsets must hold one number more than there are sequences")
-            _matrix(self.target, "target", self.target.dtype, drafts + d.N, d.V)
-            _matrix(self.draft, "draft", self.target.dtype, drafts, d.V)
-            _vector(self.temperature, "temperature", torch.float32, d.N)
-            # (no drafts: torch gives an empty tensor no address)
-            if self.draft is not None and drafts == 0:
-                d.draft = None
-            self._device = _one_device([self.target, self.tokens, self.offsets, self.draft, self.temperature])
-        return self._device
+            _rows(t, "target", drafts + d.N, d.V)
+            if self.draft is not None:
+                _rows(self.draft, "draft", drafts, d.V, index, t.dtype)
+            _buffer(self.temperature, "temperature", torch.float32, d.N, index)
+            self._index = index
+        return self._index
 
 
 def sb_verify_workspace_bytes(drafts):
@@ -1121,19 +1166,15 @@ def sb_verify_drafts(drafts, u, u_next, out, accepted, ws=None, stream=None):
     token behind them, and -1 up to the end; accepted (int32 [N]) <- how many
     are accepted.  u (fp32, one per drafted token) and u_next (fp32 [N]) are
     random numbers from [0, 1).  Returns (out, accepted)."""
-    device = drafts.device()
-    N, K = drafts.N, drafts.K
-    _vector(u, "u", torch.float32, drafts.desc.drafts)
-    _vector(u_next, "u_next", torch.float32, N)
-    _matrix(out, "out", torch.int32, N, K + 1)
-    _vector(accepted, "accepted", torch.int32, N)
-    _vector(ws, "ws", torch.uint8, 0)
-    device = _one_device([u, u_next, out, accepted, ws], device)
-    ldo = 0 if out is None else out.stride(0) if out.shape[0] > 1 else out.shape[1]
-    _run("sb_verify_drafts", device, stream, lambda: sb_verify_workspace_bytes(drafts), ws,
-         lambda p, n, s: lib().sb_verify_drafts(drafts.ref(), _ptr(u), _ptr(u_next), _ptr(out),
-                                                ldo,
-                                                _ptr(accepted), p, n, s))
+    index = drafts.index()
+    d = drafts.desc
+    N, K = d.N, d.K
+    u = _buffer(u, "u", torch.float32, d.drafts, index)
+    u_next = _buffer(u_next, "u_next", torch.float32, N, index)
+    _, p, ldo = _rows(out, "out", N, K + 1, index, torch.int32)
+    acc = _buffer(accepted, "accepted", torch.int32, N, index)
+    pws, n, ws = _space(ws, lambda: sb_verify_workspace_bytes(drafts), index, stream)
+    _call("sb_verify_drafts", index, stream, lib().sb_verify_drafts, drafts.ref(), u, u_next, p, ldo, acc, pws, n)
     return out, accepted
 
 

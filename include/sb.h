@@ -523,7 +523,7 @@ sb_status sb_layer_norm(const sb_norm_desc *desc, void *y, int y_type, int64_t l
 
 /*
  * Bytes of device workspace of sb_layer_norm_grad, for its parameter gradients
- * (a call without them needs none); 0 for B == 0.  On an invalid descriptor
+ * (a call without them needs none); 0 for few rows.  On an invalid descriptor
  * returns 0 and sets *status (if not NULL).
  */
 size_t sb_layer_norm_grad_workspace_bytes(const sb_norm_desc *desc, sb_status *status);
@@ -536,7 +536,7 @@ size_t sb_layer_norm_grad_workspace_bytes(const sb_norm_desc *desc, sb_status *s
  *   dweight, dbias  DEVICE [H] of param_type, 16-byte aligned, or NULL; also
  *            where the weight or bias itself is NULL
  *   ws       >= sb_layer_norm_grad_workspace_bytes(desc), 16-byte aligned;
- *            only with dweight or dbias
+ *            only with dweight or dbias, and where it is not 0
  * At least one of dx, dweight and dbias is required.  All are overwritten, not
  * added to.
  */

@@ -29,6 +29,9 @@ struct NormArgs {
     int32_t parts;
 };
 
+// Whether the whole gradient is one launch, without partial sums.
+bool norm_grad_few(int32_t B, int32_t H);
+
 // Runs of rows whose sums for the parameters' gradients are kept apart.
 int norm_parts(int32_t B, int32_t H);
 

@@ -308,6 +308,123 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
 }
 
 // ---------------------------------------------------------------------------
+// Few rows, in one launch: the parameters' gradients need no sum over a row, so their
+// workgroups (kFewColumns units of columns, a row per kFewColumns threads) run beside the
+// ones of dx, a row each.  What such a call costs is launches: 16 rows of H 5120 in bf16
+// take 3.8 us, 6.9 with teams and a second launch for the sums, and the host a launch
+// less.  The columns' threads walk the rows, so it is for few: 256 rows of H 5120 in
+// bf16 8.7 us against 11.4, of H 8192 in fp32 11.5 against 15.5; 512 rows 16.9 against
+// 12.8, and 9.0 against 6.4 at H 512.
+// ---------------------------------------------------------------------------
+constexpr int kFewMost = 256, kFewColumns = 16, kFewRows = kThreads / kFewColumns, kFewUnits = 4;
+
+template <typename TX, typename TY, bool WHOLE>
+__device__ __forceinline__ void few_dx(const NormArgs &a, int row, float (&scratch)[2][kMostWaves])
+{
+    const TX *x = static_cast<const TX *>(a.x) + row * a.ldx;
+    const TY *dy = static_cast<const TY *>(a.dy) + row * a.lddy;
+    TX *dx = static_cast<TX *>(a.dx) + row * a.lddx;
+    const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+    Unit<TX> xs[kFewUnits];
+    Unit<TY> gs[kFewUnits];
+    float g[kFewUnits][8], xh[kFewUnits][8], sum = 0.f, cross = 0.f;
+#pragma unroll
+    for (int k = 0; k < kFewUnits; ++k) {
+        const int c = 8 * (threadIdx.x + k * kThreads);
+        xs[k] = load_at(x, c, a.H);
+        gs[k] = load_at(dy, c, a.H);
+        load_param(a.weight, a.params_bf16, c, a.H - c, 1.f, g[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kFewUnits; ++k) {
+        const int left = a.H - 8 * (int)(threadIdx.x + k * kThreads);
+        float gv[8];
+        values_of(xs[k], xh[k]);
+        values_of(gs[k], gv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool in = (WHOLE ? 0 : e) < left;
+            g[k][e] = in ? g[k][e] * gv[e] : 0.f;
+            xh[k][e] = in ? (xh[k][e] - mean) * rstd : 0.f;
+            sum += g[k][e];
+            cross += g[k][e] * xh[k][e];
+        }
+    }
+    const int wave = threadIdx.x >> 6;
+    sum = wave_sum(sum);
+    cross = wave_sum(cross);
+    if ((threadIdx.x & 63) == 0) {
+        scratch[0][wave] = sum;
+        scratch[1][wave] = cross;
+    }
+    __syncthreads();
+    sum = cross = 0.f;
+    for (int w = 0; w < kThreads / 64; ++w) {
+        sum += scratch[0][w];
+        cross += scratch[1][w];
+    }
+    sum /= a.H;
+    cross /= a.H;
+#pragma unroll
+    for (int k = 0; k < kFewUnits; ++k) {
+        const int c = 8 * (threadIdx.x + k * kThreads);
+        float out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            out[e] = rstd * (g[k][e] - sum - xh[k][e] * cross);
+        if (c < a.H)
+            store_some(dx + c, out, a.H - c);
+    }
+}
+
+template <typename TX, typename TY, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void norm_grad_few_kernel(const NormArgs a)
+{
+    __shared__ float scratch[2][kMostWaves];
+    __shared__ float joined[kFewRows][2][8 * kFewColumns];
+    const int rows = a.dx ? a.B : 0;
+    if ((int)blockIdx.x < rows) {
+        few_dx<TX, TY, WHOLE>(a, blockIdx.x, scratch);
+        return;
+    }
+    const int first = 8 * kFewColumns * ((int)blockIdx.x - rows);
+    const int unit = threadIdx.x % kFewColumns, at = threadIdx.x / kFewColumns, c = first + 8 * unit;
+    float weight[8] = {}, bias[8] = {};
+    if (c < a.H) {
+        for (int row = at; row < a.B; row += kFewRows) {
+            float x[8], g[8];
+            values_of(load_at(static_cast<const TX *>(a.x) + row * a.ldx, c, a.H), x);
+            values_of(load_at(static_cast<const TY *>(a.dy) + row * a.lddy, c, a.H), g);
+            const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                weight[e] += g[e] * ((x[e] - mean) * rstd);
+                bias[e] += g[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        joined[at][0][8 * unit + e] = weight[e];
+        joined[at][1][8 * unit + e] = bias[e];
+    }
+    __syncthreads();
+    const int which = threadIdx.x / (8 * kFewColumns), column = threadIdx.x % (8 * kFewColumns);
+    void *param = which ? a.dbias : a.dweight;
+    if (!param || first + column >= a.H)
+        return;
+    float v = joined[0][which][column];
+#pragma unroll
+    for (int r = 1; r < kFewRows; ++r)
+        v += joined[r][which][column];
+    if (a.params_bf16)
+        put(static_cast<bf16_t *>(param) + first + column, v);
+    else
+        put(static_cast<float *>(param) + first + column, v);
+}
+static_assert(kThreads == 2 * 8 * kFewColumns, "a thread per value of the parameters' gradients");
+
+// ---------------------------------------------------------------------------
 // Rows that no team holds: one workgroup per row, reading it once per sum.
 // ---------------------------------------------------------------------------
 // The sum over the workgroup; every thread has it.  `scratch` holds a float per
@@ -437,9 +554,10 @@ __global__ __launch_bounds__(kThreads) void norm_grad_columns_kernel(const NormA
 // ---------------------------------------------------------------------------
 // dw and db: the runs' sums added in order.  A workgroup has kJoinColumns columns of
 // one of them; each of its kJoinRuns groups of threads adds an equal share of the
-// runs in order, and the shares are added in order.
+// runs in order, and the shares are added in order.  32 columns: 1333 rows of H 1111 in
+// fp32 15.0 us with the launch before, 8192 rows of H 2048 in bf16 26.3; 64: 16.1 and 27.9.
 // ---------------------------------------------------------------------------
-constexpr int kJoinColumns = 64, kJoinQuads = kJoinColumns / 4, kJoinRuns = kThreads / kJoinQuads;
+constexpr int kJoinColumns = 32, kJoinQuads = kJoinColumns / 4, kJoinRuns = kThreads / kJoinQuads;
 
 __global__ __launch_bounds__(kThreads) void norm_params_kernel(const NormArgs a)
 {
@@ -548,6 +666,12 @@ hipError_t forward(const NormArgs &a, hipStream_t s)
 template <typename TX, typename TY, bool WHOLE>
 hipError_t gradient(const NormArgs &a, hipStream_t s)
 {
+    if (norm_grad_few(a.B, a.H)) {
+        const int chunks = a.dweight || a.dbias ? (a.H + 8 * kFewColumns - 1) / (8 * kFewColumns) : 0;
+        hipLaunchKernelGGL((norm_grad_few_kernel<TX, TY, WHOLE>), dim3((unsigned)((a.dx ? a.B : 0) + chunks)),
+                           dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+    }
     if ((a.H + 7) / 8 <= kMostUnits) {
         const Shape t = shape_of(a.H);
         const dim3 grid((unsigned)norm_parts(a.B, a.H)), threads(t.threads);
@@ -571,8 +695,12 @@ hipError_t gradient(const NormArgs &a, hipStream_t s)
 
 }  // namespace
 
+bool norm_grad_few(int32_t B, int32_t H) { return B <= kFewMost && H <= 8 * kFewUnits * kThreads; }
+
 int norm_parts(int32_t B, int32_t H)
 {
+    if (norm_grad_few(B, H))
+        return 0;
     if ((H + 7) / 8 > kMostUnits)
         return std::min(B, 256);
     return groups_of(shape_of(H), B, kGradWaves);

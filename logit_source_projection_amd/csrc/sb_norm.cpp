@@ -114,7 +114,7 @@ sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_ty
         return SB_ERR_NULL;
     if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 16) || !aligned(dbias, 16))
         return SB_ERR_ALIGN;
-    if (params && desc->B > 0) {
+    if (params && grad_bytes(desc) > 0) {
         if (!ws)
             return SB_ERR_NULL;
         if (ws_bytes < grad_bytes(desc))
@@ -142,6 +142,8 @@ sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_ty
     }
     if (desc->B > 0 && sbk::launch_norm_grad(a, s) != hipSuccess)
         return SB_ERR_HIP;
+    if (desc->B > 0 && sbk::norm_grad_few(desc->B, desc->H))
+        return SB_OK;
     return !params || sbk::launch_norm_params(a, s) == hipSuccess ? SB_OK : SB_ERR_HIP;
 }
 

@@ -13,6 +13,8 @@ TYPES = [(F, F, F), (H16, H16, H16), (F, H16, F), (H16, F, F), (F, F, H16), (H16
 SIZES = [(1, 1), (3, 2), (5, 7), (2, 8), (4, 9), (7, 63), (17, 64), (9, 511), (6, 512), (33, 520), (5, 1024),
          (257, 1111), (3, 2048), (2, 2056), (19, 4096), (16, 5120), (1, 5120), (3, 6144), (2, 8192), (5, 8200),
          (2, 16384), (3, 16385), (2, 17408), (2, 32768), (2, 40001), (1100, 72), (4099, 24),
+         # a gradient of few rows and of one more
+         (255, 333), (256, 5120), (257, 5120), (256, 8192), (257, 8192), (256, 8193), (257, 36),
          # every kind of team through several rows each
          (40000, 40), (20000, 104), (10000, 200), (9000, 333), (5000, 520), (3000, 1200), (1600, 5120), (601, 12001)]
 

@@ -75,9 +75,19 @@ def test_gradient_arguments():
                      (dict(lddx=511), sb.SB_ERR_SHAPE), (dict(lddx=516), sb.SB_ERR_ALIGN),
                      (dict(dx=FAKE + 8), sb.SB_ERR_ALIGN), (dict(lddx=1 << 60), sb.SB_ERR_UNSUPPORTED),
                      (dict(dw=FAKE + 8), sb.SB_ERR_ALIGN), (dict(db=FAKE + 8), sb.SB_ERR_ALIGN),
-                     (dict(dx=0, dw=0, db=0), sb.SB_ERR_NULL),
-                     (dict(ws=0), sb.SB_ERR_NULL), (dict(ws=FAKE + 8), sb.SB_ERR_ALIGN), (dict(n=16), sb.SB_ERR_WORKSPACE)):
+                     (dict(dx=0, dw=0, db=0), sb.SB_ERR_NULL)):
         assert grad(desc(), **kw) == want, kw
+    for kw, want in ((dict(ws=0), sb.SB_ERR_NULL), (dict(ws=FAKE + 8), sb.SB_ERR_ALIGN), (dict(n=16), sb.SB_ERR_WORKSPACE)):
+        assert grad(desc(B=1000), **kw) == want, kw
+
+
+def test_gradient_workspace():
+    def n(**kw):
+        return sb.lib().sb_layer_norm_grad_workspace_bytes(ctypes.byref(desc(**kw)), None)
+
+    # one launch of few rows, partial sums of more or longer ones
+    assert n(B=1) == n(B=256) == n(B=256, H=8192, ldx=8192) == 0
+    assert n(B=257) > 0 and n(B=1, H=8193, ldx=8200) > 0
 
 
 def test_no_rows():

@@ -55,7 +55,10 @@
  *    call must be memory the stream's device can access (its own, or a
  *    peer's with peer access enabled); the library does not check this, as
  *    a per-call pointer query would cost more than a decode call's launch.
- *    Outputs must not overlap inputs, the workspace or each other.
+ *    Outputs must not overlap inputs, the workspace or each other.  A row of
+ *    an input may be read up to the end of the 16 bytes that hold its last
+ *    value (a row starts at, and its stride is, a multiple of 16); what is
+ *    read behind the last value has no effect.
  *  - The workspace is scratch owned by the call until its work completes on
  *    the stream: its contents on entry do not matter, and nothing in it is
  *    valid afterwards.  Every workspace starts with the same fixed region
@@ -486,7 +489,8 @@ sb_status sb_int8_logits(const sb_int8_desc *desc, void *out, int dtype, int64_t
  * once to its type.  NaN and infinities follow IEEE rules and stay in their
  * row (in the parameters' gradients in their column): a row that holds one is
  * NaN.  A row whose values are all the same has y = bias for eps > 0 (rounding
- * of the mean aside) and NaN for eps = 0.
+ * of the mean aside) and NaN for eps = 0.  Finite rows whose sums or squares
+ * overflow fp32 are outside the contract (values up to 10^15 are safe).
  * ---------------------------------------------------------------------------
  */
 
@@ -569,7 +573,7 @@ sb_status sb_layer_norm_grad(const sb_norm_desc *desc, const void *dy, int dy_ty
  *   ldw      row stride, >= H, a multiple of 4 (fp32) or 8 (bf16)
  *   type     sb_dtype of the table (anything else: SB_ERR_SHAPE, as for every type)
  * H <= 2^24 and V <= 2^30; in the gradient H < 2^24 - 256, V <= 2^24, B <= 2^24 and
- * about B * H < 2^38; every matrix of these calls spans less than 2^47 bytes
+ * about B * H < 2^37; every matrix of these calls spans less than 2^47 bytes
  * (SB_ERR_UNSUPPORTED).
  */
 typedef struct sb_table_desc {

@@ -584,7 +584,8 @@ bool embed_grad_fits(int32_t B, int32_t H)
 {
     const int64_t threads = row_threads(H), parts = ((int64_t)H + 8 * threads - 1) / (8 * threads);
     const int64_t runs = ((int64_t)B + kEmbedRun - 1) / kEmbedRun;
-    return runs * parts * kThreads < (int64_t)1 << 32 &&
+    // (the zeros behind the sums are below 2^31 threads, and a grid below 2^32)
+    return runs * parts * kThreads < (int64_t)1 << 31 &&
            ((int64_t)H + kJoinColumns - 1) / kJoinColumns <= 65535;
 }
 

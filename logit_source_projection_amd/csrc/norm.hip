@@ -619,8 +619,8 @@ Shape shape_of(int H)
 // Workgroups that rows are dealt to: as many as put `waves` waves on every CU (one
 // workgroup on each at least).  The loads of the next row are under way while one is
 // summed, so few waves suffice and more only add ends: forward of 8192 rows of H 5120
-// in bf16 31 us with 16 waves per CU, 36 with 32, 57 with 8; gradient 59 us with 8,
-// 63 with 10, 68 with 16 (each workgroup leaves a row of partial sums).
+// in bf16 30 us with 16 waves per CU, 36 with 32, 53 with 8; gradient 52 us with 8,
+// 58 with 10, 63 with 16 (each workgroup leaves a row of partial sums).
 constexpr int kForwardWaves = 16, kGradWaves = 8;
 
 int groups_of(const Shape &t, int64_t B, int waves)

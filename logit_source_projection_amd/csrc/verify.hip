@@ -193,8 +193,8 @@ __device__ __forceinline__ const T *row_at(const void *rows, int64_t ld, int64_t
 // Every chunk of every row that a sequence may need: the largest logit, and the sum of
 // the powers or, of a greedy sequence, the largest logit's column.  As many workgroups
 // as are resident take one chunk after the other, the next one's loads under way while
-// the powers of one are summed: the 64-bit instructions for a logit take two
-// thirds of the time that its 4 bytes take.
+// the powers of one are summed.  64 sequences of 7 drafts with draft logits, V 151936 in
+// fp32: 111 us, of which the 583 MB alone take 90 and the 64-bit instructions as long.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kRowGroups = 1024;
 

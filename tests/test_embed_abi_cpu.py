@@ -103,4 +103,6 @@ def test_gradients_that_pass_a_grid():
     assert ws_status(table(H=(1 << 24) - 512, **wide), B=1 << 10) == sb.SB_OK
     assert ws_status(table(H=(1 << 24) - 8, **wide)) == sb.SB_ERR_UNSUPPORTED
     assert ws_status(table(H=1 << 16, ldw=1 << 16), B=1 << 24) == sb.SB_ERR_UNSUPPORTED
+    # with the zeros' workgroups behind them
+    assert ws_status(table(H=1 << 14, ldw=1 << 14), B=1 << 24) == sb.SB_ERR_UNSUPPORTED
     assert ws_status(table(H=1 << 12, ldw=1 << 12), B=1 << 24) == sb.SB_OK

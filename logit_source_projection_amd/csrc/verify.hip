@@ -191,12 +191,14 @@ __device__ __forceinline__ const T *row_at(const void *rows, int64_t ld, int64_t
 
 // ---------------------------------------------------------------------------
 // Every chunk of every row that a sequence may need: the largest logit, and the sum of
-// the powers or, of a greedy sequence, the largest logit's column.  As many workgroups
-// as are resident take one chunk after the other, the next one's loads under way while
-// the powers of one are summed.  64 sequences of 7 drafts with draft logits, V 151936 in
-// fp32: 111 us, of which the 583 MB alone take 90 and the 64-bit instructions as long.
+// the powers or, of a greedy sequence, the largest logit's column.  Workgroups take one
+// chunk after the other, the next one's loads under way while the powers of one are
+// summed.  64 sequences of 7 drafts with draft logits, V 151936 in fp32: 111 us, of which
+// the 583 MB alone take 90 and the 64-bit instructions as long.  Twice as many workgroups
+// as are resident: those whose rows are not there leave room for others (17 ragged
+// sequences, V 50257: the call takes 23.4 us, with as many as are resident 25.6).
 // ---------------------------------------------------------------------------
-constexpr uint32_t kRowGroups = 1024;
+constexpr uint32_t kRowGroups = 2048;
 
 // A chunk to take: workgroup's items number, ... (none: to is NULL)
 template <typename T>
@@ -459,6 +461,8 @@ __device__ __forceinline__ double wave_upto(double v)
 // them.  The last of a sequence's workgroups to be done (none waits for another) finds
 // the one whose cumulative sum passes the random number's share of the whole, then the
 // column.
+// One sequence (V 151936, fp32) takes 10 us, of which 4 are the columns' sums; 64 of them
+// 28, for 78 MB, partly out of the last-level cache, and 10 us of 64-bit instructions.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Rest {
@@ -512,7 +516,7 @@ __device__ __forceinline__ double sum_of(const double (&v)[8])
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs a)
+__global__ __launch_bounds__(kThreads, 3) void verify_draw_kernel(const VerifyArgs a)
 {
     typedef typename Rest<T>::Part Part;
     constexpr int kUnits = Part::kUnits;
@@ -529,93 +533,93 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs 
     const float u = a.u_next[i];
     double *rests = a.rest + (int64_t)i * a.draws * 2;
     const Powers ps(d.p.most, s.rate), qs(d.q.most, s.rate);
+    // First these columns' sums, then in the last workgroup the columns of the one that was
+    // found, by the same code: as code of its own, run by one workgroup and fetched
+    // from memory, that took it 3 us more.
     Rest<T> rest;
-    rest.load(a, s, d, i, mine * kVerifyDraw);
-    double left = 0.0, whole = 0.0, p[8], r[kUnits][8];
+    int from = 0, at = mine;
+    double before = 0.0, goal = 0.0, r[kUnits][8], upto[kUnits];
+    for (bool found = false;; found = true) {
+        rest.load(a, s, d, i, at * kVerifyDraw);
+        double whole = 0.0;
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        rest.find(d, ps, qs, x - mine * kVerifyDraw, k, p, r[k]);
-        left += sum_of(r[k]);
-        whole += sum_of(p);
-    }
-    left = wave_sum(left);
-    whole = wave_sum(whole);
-    if (lane == 0) {
-        sums[0][0][wave] = left;
-        sums[1][0][wave] = whole;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWaves; ++w) {
-            left += sums[0][0][w];
-            whole += sums[1][0][w];
-        }
-        // Written through to memory, complete before they are counted, and read from memory
-        // (device-scope atomics): no workgroup needs a fence, which writes back and
-        // empties its XCD's L2 (4800 of them took 80 us).
-        __hip_atomic_store(&rests[2 * mine], left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(&rests[2 * mine + 1], whole, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        __builtin_amdgcn_s_waitcnt(0);
-        __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        draws = __hip_atomic_fetch_add(&a.done[(int64_t)i * kVerifyDone], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
-                (uint32_t)a.draws;
-        token = INT_MAX;
-        last = -1;
-    }
-    __syncthreads();
-    if (!draws)
-        return;
-    // Every wave looks for the columns' workgroup by itself.  Where nothing is left, p is
-    // drawn from.
-    int from = 0, at = 0;
-    double before = 0.0, goal = 0.0;
-    for (; from < 2; ++from) {
-        auto weight = [&](int c) {
-            return c < a.draws ? __hip_atomic_load(&rests[2 * c + from], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                               : 0.0;
-        };
-        const double first = weight(lane);  // (read once)
-        double total = wave_sum(first);
-        for (int c0 = 64; c0 < a.draws; c0 += 64)
-            total += wave_sum(weight(c0 + lane));
-        if (!(total > 0.0))
-            continue;
-        // (a number outside [0, 1) draws the first or the last column)
-        goal = (u > 0.f ? (double)u : 0.0) * total;
-        double upto = 0.0;
-        for (int c0 = 0; c0 < a.draws; c0 += 64) {
-            const double v = c0 == 0 ? first : weight(c0 + lane), to = upto + wave_upto(v);
-            const uint64_t past = __ballot(v > 0.0 && to > goal), some = __ballot(v > 0.0);
-            // the first past the goal, else the last with anything left
-            const int one = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
-            if (one >= 0) {
-                at = c0 + one;
-                before = __shfl(to, one) - __shfl(v, one);
-            }
-            if (past)
-                break;
-            upto = __shfl(to, 63);
-        }
-        break;
-    }
-    rest.load(a, s, d, i, at * kVerifyDraw);
-    double upto[kUnits];
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        rest.find(d, ps, qs, x - at * kVerifyDraw, k, p, r[k]);
-        if (from > 0) {
+        for (int k = 0; k < kUnits; ++k) {
+            double p[8];
+            rest.find(d, ps, qs, x - at * kVerifyDraw, k, p, r[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                r[k][e] = p[e];
+                r[k][e] = from > 0 ? p[e] : r[k][e];
+            const double sum = sum_of(r[k]);
+            whole += sum_of(p);
+            upto[k] = wave_upto(sum);
+            if (lane == 63)
+                sums[0][k][wave] = upto[k];
+            upto[k] -= sum;
         }
-        const double sum = sum_of(r[k]);
-        upto[k] = wave_upto(sum);
-        if (lane == 63)
-            sums[0][k][wave] = upto[k];
-        upto[k] -= sum;
+        whole = wave_sum(whole);
+        if (lane == 0)
+            sums[1][0][wave] = whole;
+        __syncthreads();
+        if (found)
+            break;
+        if (threadIdx.x == 0) {
+            double left = 0.0;
+            whole = 0.0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+#pragma unroll
+                for (int k = 0; k < kUnits; ++k)
+                    left += sums[0][k][w];
+                whole += sums[1][0][w];
+            }
+            // Written through to memory, complete before they are counted, and read from memory
+            // (device-scope atomics): no workgroup needs a fence, which writes back and
+            // empties its XCD's L2 (4800 of them took 80 us).
+            __hip_atomic_store(&rests[2 * mine], left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&rests[2 * mine + 1], whole, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            __builtin_amdgcn_s_waitcnt(0);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            draws = __hip_atomic_fetch_add(&a.done[(int64_t)i * kVerifyDone], 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)a.draws;
+            token = INT_MAX;
+            last = -1;
+        }
+        __syncthreads();
+        if (!draws)
+            return;
+        // Every wave looks for the columns' workgroup by itself.  Where nothing is left, p is
+        // drawn from.
+        for (; from < 2; ++from) {
+            auto weight = [&](int c) {
+                return c < a.draws ? __hip_atomic_load(&rests[2 * c + from], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                   : 0.0;
+            };
+            const double first = weight(lane);  // (read once)
+            double total = wave_sum(first);
+            for (int c0 = 64; c0 < a.draws; c0 += 64)
+                total += wave_sum(weight(c0 + lane));
+            if (!(total > 0.0))
+                continue;
+            // (a number outside [0, 1) draws the first or the last column)
+            goal = (u > 0.f ? (double)u : 0.0) * total;
+            double behind = 0.0;
+            for (int c0 = 0; c0 < a.draws; c0 += 64) {
+                const double v = c0 == 0 ? first : weight(c0 + lane), to = behind + wave_upto(v);
+                const uint64_t past = __ballot(v > 0.0 && to > goal), some = __ballot(v > 0.0);
+                // the first past the goal, else the last with anything left
+                const int one = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
+                if (one >= 0) {
+                    at = c0 + one;
+                    before = __shfl(to, one) - __shfl(v, one);
+                }
+                if (past)
+                    break;
+                behind = __shfl(to, 63);
+            }
+            break;
+        }
     }
-    __syncthreads();
     int past = INT_MAX, behind = -1;
     double base = before;
 #pragma unroll
@@ -636,10 +640,16 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs 
             }
         }
     }
-    if (past != INT_MAX)
+    // (by one lane of each wave: of 64 an atomic takes one at a time)
+#pragma unroll 1
+    for (int lanes = 1; lanes < 64; lanes <<= 1) {
+        past = min(past, __shfl_xor(past, lanes));
+        behind = max(behind, __shfl_xor(behind, lanes));
+    }
+    if (lane == 0) {
         atomicMin(&token, past);
-    if (behind >= 0)
         atomicMax(&last, behind);
+    }
     __syncthreads();
     if (threadIdx.x == 0)
         a.out[i * a.ldo + j] = at * kVerifyDraw + (token != INT_MAX ? token : last);

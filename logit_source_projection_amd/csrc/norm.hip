@@ -28,7 +28,26 @@ constexpr int kMostWaves = 16;              // of a team
 constexpr int64_t kMostRows = 1 << 20;      // workgroups that rows are dealt to
 constexpr int kCus = 256;
 
-// Values c .. of a parameter, `other` where there is none.
+// The values of a unit that n values are there of (more in whole ones), 0 behind them.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void values_in(const Unit<T> &u, int n, float (&v)[8])
+{
+    values_of(u, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = WHOLE || e < n ? v[e] : 0.f;
+}
+
+// Values c .. of a parameter, 0 behind its n last ones, `other` where there is none.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void load_param(const T *p, int c, int n, float (&v)[8])
+{
+    if (WHOLE)
+        values_of(load_some(p + c, n), v);
+    else
+        values_in<false>(load_at(p, c, c + n), n, v);
+}
+template <bool WHOLE>
 __device__ __forceinline__ void load_param(const void *p, bool bf16, int c, int n, float other, float (&v)[8])
 {
     if (!p) {
@@ -36,16 +55,18 @@ __device__ __forceinline__ void load_param(const void *p, bool bf16, int c, int 
         for (int e = 0; e < 8; ++e)
             v[e] = other;
     } else if (bf16) {
-        values_of(load_some(static_cast<const bf16_t *>(p) + c, n), v);
+        load_param<WHOLE>(static_cast<const bf16_t *>(p), c, n, v);
     } else {
-        values_of(load_some(static_cast<const float *>(p) + c, n), v);
+        load_param<WHOLE>(static_cast<const float *>(p), c, n, v);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Teams.  TEAM lanes of a wave, or with TEAM 0 the whole workgroup.  WHOLE: H is a
 // multiple of 8, and no unit is there in part (code for such units between the loads and
-// their use cost 8192 fp32 rows of H 5120 10 us of 52).
+// their use cost 8192 fp32 rows of H 5120 10 us of 52).  Others load whole 16 bytes and
+// clear what is behind the row where it is used: 8192 rows of H 5001 in bf16 take 35 us
+// and their gradient 72; with loads of 8, 4 and 2 bytes, each waited for, 39 and 100.
 // ---------------------------------------------------------------------------
 template <int TEAM, int UNITS, bool WHOLE>
 struct Team {
@@ -90,7 +111,7 @@ struct Team {
         for (int k = 0; k < UNITS; ++k) {
             const int c = column(k);
             if (c < H)
-                v[k] = WHOLE ? load_unit(row + c) : load_some(row + c, H - c);
+                v[k] = WHOLE ? load_unit(row + c) : load_at(row, c, H);
             else
                 clear(v[k]);
         }
@@ -118,8 +139,8 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(const NormArgs a)
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
         const int c = team.column(k);
-        load_param(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
-        load_param(a.bias, a.params_bf16, c, H - c, 0.f, s[k]);
+        load_param<WHOLE>(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
+        load_param<WHOLE>(a.bias, a.params_bf16, c, H - c, 0.f, s[k]);
     }
     Unit<TX> next[UNITS];
     if (team.row < a.B)
@@ -128,7 +149,7 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(const NormArgs a)
         float v[UNITS][8], sum = 0.f;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
-            values_of(next[k], v[k]);
+            values_in<WHOLE>(next[k], H - team.column(k), v[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 sum += v[k][e];
@@ -173,7 +194,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
         const int c = team.column(k);
-        load_param(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
+        load_param<WHOLE>(a.weight, a.params_bf16, c, H - c, 1.f, w[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             dw[k][e] = db[k][e] = 0.f;
@@ -216,8 +237,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             float xv[8], gv[8];
-            values_of(x[k], xv);
-            values_of(g[k], gv);
+            values_in<WHOLE>(x[k], H - team.column(k), xv);
+            values_in<WHOLE>(g[k], H - team.column(k), gv);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float xh = (xv[e] - mean) * rstd;
@@ -255,8 +276,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             float xv[8], gv[8];
-            values_of(x[k], xv);
-            values_of(g[k], gv);
+            values_in<WHOLE>(x[k], H - team.column(k), xv);
+            values_in<WHOLE>(g[k], H - team.column(k), gv);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 xv[e] = rstd * (gv[e] * w[k][e] - m - (xv[e] - mean) * rstd * c2);
@@ -333,7 +354,7 @@ __device__ __forceinline__ void few_dx(const NormArgs &a, int row, float (&scrat
         const int c = 8 * (threadIdx.x + k * kThreads);
         xs[k] = load_at(x, c, a.H);
         gs[k] = load_at(dy, c, a.H);
-        load_param(a.weight, a.params_bf16, c, a.H - c, 1.f, g[k]);
+        load_param<WHOLE>(a.weight, a.params_bf16, c, a.H - c, 1.f, g[k]);
     }
 #pragma unroll
     for (int k = 0; k < kFewUnits; ++k) {
@@ -477,8 +498,8 @@ __global__ __launch_bounds__(kThreads) void norm_long_kernel(const NormArgs a)
         for (int u = threadIdx.x; u < units; u += kThreads) {
             float w[8], s[8];
             values_of(load_some(x + 8 * u, H - 8 * u), v);
-            load_param(a.weight, a.params_bf16, 8 * u, H - 8 * u, 1.f, w);
-            load_param(a.bias, a.params_bf16, 8 * u, H - 8 * u, 0.f, s);
+            load_param<false>(a.weight, a.params_bf16, 8 * u, H - 8 * u, 1.f, w);
+            load_param<false>(a.bias, a.params_bf16, 8 * u, H - 8 * u, 0.f, s);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 v[e] = (v[e] - mean) * rstd * w[e] + s[e];
@@ -504,7 +525,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_rows_kernel(const NormArgs
             const int n = H - 8 * u;
             values_of(load_some(x + 8 * u, n), xv);
             values_of(load_some(dy + 8 * u, n), gv);
-            load_param(a.weight, a.params_bf16, 8 * u, n, 1.f, w);
+            load_param<false>(a.weight, a.params_bf16, 8 * u, n, 1.f, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float g = e < n ? gv[e] * w[e] : 0.f;
@@ -518,7 +539,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_rows_kernel(const NormArgs
             const int n = H - 8 * u;
             values_of(load_some(x + 8 * u, n), xv);
             values_of(load_some(dy + 8 * u, n), gv);
-            load_param(a.weight, a.params_bf16, 8 * u, n, 1.f, w);
+            load_param<false>(a.weight, a.params_bf16, 8 * u, n, 1.f, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 xv[e] = rstd * (gv[e] * w[e] - m - (xv[e] - mean) * rstd * k);

@@ -108,6 +108,13 @@ def operators():
     cases["layer norm gradient"] = (
         [x, dy], lambda stream, ws: sb.sb_layer_norm_grad(n, dy, m2, r2, dx, dw, db, ws=ws, stream=stream), [dx, dw, db],
         lambda: sb.layer_norm_grad_workspace(n))
+    # the same of more rows than one launch takes
+    x5, dy5 = randn(500, H, seed=9), randn(500, H, seed=10)
+    n5, m5, r5 = sb.Norm(x5, w, b), x5.mean(1), 1 / x5.std(1)
+    dx5, dw5, db5 = torch.empty_like(x5), torch.empty_like(w), torch.empty_like(b)
+    cases["layer norm gradient, more rows"] = (
+        [x5, dy5], lambda stream, ws: sb.sb_layer_norm_grad(n5, dy5, m5, r5, dx5, dw5, db5, ws=ws, stream=stream),
+        [dx5, dw5, db5], lambda: sb.layer_norm_grad_workspace(n5))
     table, ids = randn(V, H, seed=5), make_ids("ranks", 300, V, 6)
     t, out = sb.Table(table, [0, 1000, V]), torch.empty(300, H, device="cuda")
     cases["embedding"] = ([table, ids], lambda stream, ws: sb.sb_embed(t, ids, out, scale=2.0, stream=stream), [out], None)
@@ -126,7 +133,8 @@ def operators():
     return cases
 
 
-NAMES = ["layer norm", "layer norm gradient", "embedding", "embedding gradient", "verification"]
+NAMES = ["layer norm", "layer norm gradient", "layer norm gradient, more rows", "embedding", "embedding gradient",
+         "verification"]
 
 
 def change(inputs, seed):

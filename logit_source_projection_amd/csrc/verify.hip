@@ -515,6 +515,8 @@ __device__ __forceinline__ double sum_of(const double (&v)[8])
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
+// (Registers for three workgroups on a CU spill two values that are used once: 64
+// sequences' whole call takes 143 us, with two of them 147.)
 template <typename T>
 __global__ __launch_bounds__(kThreads, 3) void verify_draw_kernel(const VerifyArgs a)
 {

@@ -262,6 +262,21 @@ def test_far_rows_of_a_large_table(require_gpu):
     assert bool((w[V - 1] == 2).all()) and bool((w[V - 2] == 1).all()) and float(w.float().sum()) == 6 * H
 
 
+def test_rows_far_apart(require_gpu):
+    """Rows of out and dout whose offsets pass 32 bits."""
+    w = torch.randn(50, 264, device="cuda").to(H16)
+    ids = torch.tensor([7, 49, 7], dtype=torch.int32, device="cuda")
+    ld = 1 << 30
+    far = torch.empty(2 * ld + 264, dtype=H16, device="cuda").as_strided((3, 264), (ld, 1))
+    sb.sb_embed(sb.Table(w), ids, far)
+    assert torch.equal(far, w[ids.long()])
+    dw = torch.empty(50, 264, device="cuda")
+    sb.sb_embed_grad(sb.Table(dw), ids, far)
+    want = torch.zeros(50, 264, device="cuda")
+    want[7], want[49] = 2 * w[7].float(), w[49].float()
+    assert torch.equal(dw, want)
+
+
 def test_refusals_of_the_binding(require_gpu):
     w, ids = torch.zeros(16, 8, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
     t, out = sb.Table(w), torch.empty(4, 8, device="cuda")

@@ -163,6 +163,23 @@ def test_many_rows(require_gpu, B, H):
     ref.check_gradient(dx, dw, db, x, w, dy, mean, rstd)
 
 
+@pytest.mark.parametrize("B,H,ld", [(3, 520, 1 << 30), (300, 520, 1 << 23), (3, 20000, 1 << 30)])
+def test_rows_far_apart(require_gpu, B, H, ld):
+    """Offsets past 32 bits give what the same rows give side by side."""
+    x, dy, w, b = make(B, H, H16, H16, F, 18)
+    want = run(x, dy, w, b)
+
+    def far():
+        return torch.empty((B - 1) * ld + H, dtype=H16, device="cuda").as_strided((B, H), (ld, 1))
+
+    n, g, y, dx = sb.Norm(far().copy_(x), w, b), far().copy_(dy), far(), far()
+    mean, rstd, dw, db = (torch.empty_like(t) for t in (*want[1:3], *want[4:]))
+    sb.sb_layer_norm(n, y, mean, rstd)
+    sb.sb_layer_norm_grad(n, g, mean, rstd, dx, dw, db)
+    for got, ref_ in zip((y, mean, rstd, dx, dw, db), want):
+        assert torch.equal(got, ref_)
+
+
 def test_no_rows(require_gpu):
     w, b = torch.randn(24, device="cuda"), torch.randn(24, device="cuda")
     n = sb.Norm(torch.empty(0, 24, device="cuda"), w, b)

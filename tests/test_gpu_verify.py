@@ -174,6 +174,16 @@ def test_more_chunks_than_workgroups(require_gpu):
     check(make([0] * 700, 0, 17000, F, False, 56))
 
 
+def test_rows_far_apart(require_gpu):
+    """Offsets past 32 bits."""
+    s = make([2, 1], 2, 9001, H16, True, 57)
+    for name in ("target", "draft"):
+        t, ld = s[name], 1 << 30
+        far = torch.empty((len(t) - 1) * ld + 9001, dtype=H16, device="cuda").as_strided(t.shape, (ld, 1))
+        s[name] = far.copy_(t)
+    check(s)
+
+
 def test_more_drafts_than_allowed(require_gpu):
     check(make([6, 1, 9, 0], 4, 500, seed=3))
     check(make([3, 2], 0, 500, seed=4))

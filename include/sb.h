@@ -666,7 +666,7 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
  *   draft    DEVICE [drafts][ldd] logits, laid out as target, or NULL
  *   type     sb_dtype of target and draft (anything else: SB_ERR_SHAPE)
  *   temperature  DEVICE fp32 [N], or NULL (1)
- * N * ceil(V / 4096) and N * (2 K + 1) * ceil(V / 8192) are below 2^24, and every
+ * N * ceil(V / 2048) and N * (2 K + 1) * ceil(V / 8192) are below 2^24, and every
  * matrix spans less than 2^47 bytes (SB_ERR_UNSUPPORTED).
  */
 typedef struct sb_drafts_desc {

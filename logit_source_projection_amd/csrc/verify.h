@@ -8,7 +8,7 @@
 namespace sbk {
 
 // Columns of a row that one workgroup takes: for its maximum and sum, and in the draw.
-constexpr int kVerifyChunk = 8192, kVerifyDraw = 4096;
+constexpr int kVerifyChunk = 8192, kVerifyDraw = 2048;
 
 // Words between the sequences' counters: a cache line, as the atomics of a line take turns.
 constexpr int kVerifyDone = 32;

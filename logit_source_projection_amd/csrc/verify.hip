@@ -89,11 +89,29 @@ struct Powers {
         const double x = (double)most_of(z, low), k = fma(x, rate, back);
         return ldexp(power_within(fma(x, rate, back - k)), __double2loint(k));
     }
-    __device__ __forceinline__ double of(float z) const { return far ? of<true>(z) : of<false>(z); }
-    // the factor from the powers of another largest logit to these
-    __device__ __forceinline__ double from(const Powers &o) const
+    // the factor from these powers to a row's shares
+    __device__ __forceinline__ double to(float row_most) const
     {
-        return power_of(((double)o.most - (double)most) * rate + (off - o.off));
+        return power_of(((double)most - (double)row_most) * rate - off);
+    }
+};
+
+// 2^((z - most) rate) of single logits and where a sequence's row is drawn from: an
+// instruction more than a power above, and no other code for logits far out, so
+// that few registers and instructions do.
+struct Shares {
+    double rate, most, low;
+    __device__ __forceinline__ Shares(float largest, double r)
+    {
+        rate = fmax(r, 1e-290);  // (a temperature of +inf; -inf logits stay at 0)
+        most = largest;
+        low = -1100.0 / rate;
+    }
+    __device__ __forceinline__ double of(float z) const
+    {
+        constexpr double kRound = 6755399441055744.0;  // 3 2^51
+        const double d = fmax((double)z - most, low), k = fma(d, rate, kRound);
+        return ldexp(power_within(fma(d, rate, kRound - k)), __double2loint(k));
     }
 };
 
@@ -348,11 +366,10 @@ __device__ __forceinline__ Softmax softmax_of(const RowPart *parts, int chunks, 
     Softmax s{0.0, wave_most(most)};
     if (!there(s))
         return s;
-    const Powers powers(s.most, rate);
-    double sum = first.most > -INFINITY ? first.sum * powers.from(Powers(first.most, rate)) : 0.0;
+    double sum = first.most > -INFINITY ? first.sum * Powers(first.most, rate).to(s.most) : 0.0;
     for (int c = lane + 64; c < chunks; c += 64)
         if (parts[c].most > -INFINITY)
-            sum += parts[c].sum * powers.from(Powers(parts[c].most, rate));
+            sum += parts[c].sum * Powers(parts[c].most, rate).to(s.most);
     s.over = 1.0 / wave_sum(sum);
     return s;
 }
@@ -400,8 +417,8 @@ __device__ __forceinline__ Verdict judge(const VerifyArgs &a, const Sequence &s,
     if (!drafted)
         return d;
     const bool comparable = inside && (!both || there(d.q));
-    const double qx = both && comparable ? Powers(d.q.most, s.rate).of(y) * d.q.over : 1.0;
-    d.accepted = comparable && (double)u * qx < Powers(d.p.most, s.rate).of(z) * d.p.over;
+    const double qx = both && comparable ? Shares(d.q.most, s.rate).of(y) * d.q.over : 1.0;
+    d.accepted = comparable && (double)u * qx < Shares(d.p.most, s.rate).of(z) * d.p.over;
     if (both && there(d.q))
         d.how = kLess;
     else if (!both && inside)
@@ -461,8 +478,8 @@ __device__ __forceinline__ double wave_upto(double v)
 // them.  The last of a sequence's workgroups to be done (none waits for another) finds
 // the one whose cumulative sum passes the random number's share of the whole, then the
 // column.
-// One sequence (V 151936, fp32) takes 10 us, of which 4 are the columns' sums; 64 of them
-// 28, for 78 MB, partly out of the last-level cache, and 10 us of 64-bit instructions.
+// 2048 columns, one unit to a thread: a call on one sequence (V 151936, fp32) takes 16.9
+// us, on 64 of them 131.8; with 4096 18.0 and 135.0.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Rest {
@@ -475,19 +492,9 @@ struct Rest {
             y.load(row_at<T>(a.draft, a.ldd, s.draft(d.accepted), c0), a.V - c0);
     }
     // A unit's shares of p and what is left of them; x: the rejected token's column, from
-    // these columns' first on.  (Whether powers are far out is asked once: eight
-    // of them run side by side.)
-    __device__ __forceinline__ void find(const Verdict &d, const Powers &ps, const Powers &qs, int x, int k,
+    // these columns' first on.
+    __device__ __forceinline__ void find(const Verdict &d, const Shares &ps, const Shares &qs, int x, int k,
                                          double (&p)[8], double (&r)[8]) const
-    {
-        if (ps.far || (d.how == kLess && qs.far))
-            find_as<true>(d, ps, qs, x, k, p, r);
-        else
-            find_as<false>(d, ps, qs, x, k, p, r);
-    }
-    template <bool FAR>
-    __device__ __forceinline__ void find_as(const Verdict &d, const Powers &ps, const Powers &qs, int x, int k,
-                                            double (&p)[8], double (&r)[8]) const
     {
         // p and q are rounded before their difference: fused, equal ones would leave
         // what the rounding of one took
@@ -496,12 +503,12 @@ struct Rest {
         values_of(z.raw[k], v);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            p[e] = (FAR ? ps.of(v[e]) : ps.of<false>(v[e])) * d.p.over;
+            p[e] = ps.of(v[e]) * d.p.over;
         if (d.how == kLess) {
             values_of(y.raw[k], v);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                r[e] = fmax(p[e] - (FAR ? qs.of(v[e]) : qs.of<false>(v[e])) * d.q.over, 0.0);
+                r[e] = fmax(p[e] - qs.of(v[e]) * d.q.over, 0.0);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -515,10 +522,8 @@ __device__ __forceinline__ double sum_of(const double (&v)[8])
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
-// (Registers for three workgroups on a CU spill two values that are used once: 64
-// sequences' whole call takes 143 us, with two of them 147.)
 template <typename T>
-__global__ __launch_bounds__(kThreads, 3) void verify_draw_kernel(const VerifyArgs a)
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs a)
 {
     typedef typename Rest<T>::Part Part;
     constexpr int kUnits = Part::kUnits;
@@ -534,7 +539,7 @@ __global__ __launch_bounds__(kThreads, 3) void verify_draw_kernel(const VerifyAr
     const int x = d.how == kWithout ? a.tokens[s.first + j] : -1;
     const float u = a.u_next[i];
     double *rests = a.rest + (int64_t)i * a.draws * 2;
-    const Powers ps(d.p.most, s.rate), qs(d.q.most, s.rate);
+    const Shares ps(d.p.most, s.rate), qs(d.q.most, s.rate);
     // First these columns' sums, then in the last workgroup the columns of the one that was
     // found, by the same code: as code of its own, run by one workgroup and fetched
     // from memory, that took it 3 us more.

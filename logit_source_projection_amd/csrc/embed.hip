@@ -92,11 +92,10 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const EmbedArgs a, int 
 // straight from the registers: 16384 equal tokens took 70 us in one wave's hands.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortEach = 16;                             // IDs per thread and chunk
+constexpr int kSortEach = 16;                             // IDs per thread and chunk at most
 constexpr int kSortChunk = kSortThreads * kSortEach;      // 2^14
 constexpr int kSortRange = 4096;                          // IDs per workgroup at most
 constexpr int kSortNeighbours = kSortRange / kSortThreads;
-constexpr int kSortLds = kSortRange * 4 + kSortChunk * 4;
 constexpr int kSortHot = 32;                              // IDs that may be this share of all
 
 // The place of an ID in `start`.
@@ -109,20 +108,22 @@ __device__ __forceinline__ int embed_slot(const EmbedArgs &a, uint32_t v)
 // kSortOther of another group's; `before` counts those of groups before this one.
 constexpr uint32_t kSortOther = 0xFFFFFFFFu;
 
+template <int EACH>
 __device__ __forceinline__ int sort_place(int b0, int k)
 {
-    return b0 + ((threadIdx.x >> 6) * kSortEach + k) * 64 + (threadIdx.x & 63);
+    return b0 + ((threadIdx.x >> 6) * EACH + k) * 64 + (threadIdx.x & 63);
 }
 
-__device__ __forceinline__ void sort_load(const EmbedArgs &a, int b0, uint32_t (&id)[kSortEach], int &before)
+template <int EACH>
+__device__ __forceinline__ void sort_load(const EmbedArgs &a, int b0, uint32_t (&id)[EACH], int &before)
 {
 #pragma unroll
-    for (int k = 0; k < kSortEach; ++k) {
-        const int b = sort_place(b0, k);
+    for (int k = 0; k < EACH; ++k) {
+        const int b = sort_place<EACH>(b0, k);
         id[k] = b < a.B ? (uint32_t)a.ids[b] : kSortOther;
     }
 #pragma unroll
-    for (int k = 0; k < kSortEach; ++k) {
+    for (int k = 0; k < EACH; ++k) {
         const uint32_t group = id[k] & ((1u << a.shift) - 1);
         const bool there = id[k] < (uint32_t)a.V;
         before += there && group < blockIdx.x;
@@ -130,26 +131,29 @@ __device__ __forceinline__ void sort_load(const EmbedArgs &a, int b0, uint32_t (
     }
 }
 
+// EACH: IDs per thread and chunk.  One, for up to 1024 tokens, has no ID that is hot.
+template <int EACH>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArgs a)
 {
+    constexpr int kChunk = kSortThreads * EACH;
     extern __shared__ int32_t smem[];
     int32_t *next = smem;                     // counts, then where an ID's next position goes
     uint32_t *list = reinterpret_cast<uint32_t *>(smem + kSortRange);  // number << 14 | place in the chunk
     __shared__ int32_t sums[kSortWaves], hot[kSortHot], hots;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, range = a.range;
     int before = 0, none = 0;
-    uint32_t id[kSortEach];
+    uint32_t id[EACH];
     sort_load(a, 0, id, before);
     for (int i = threadIdx.x; i < range; i += kSortThreads)
         next[i] = 0;
     if (threadIdx.x == 0)
         hots = 0;
     __syncthreads();
-    for (int b0 = 0; b0 < a.B; b0 += kSortChunk) {
+    for (int b0 = 0; b0 < a.B; b0 += kChunk) {
         if (b0 > 0)
             sort_load(a, b0, id, before);
 #pragma unroll
-        for (int k = 0; k < kSortEach; ++k)
+        for (int k = 0; k < EACH; ++k)
             if (id[k] != kSortOther)
                 atomicAdd(&next[id[k]], 1);
     }
@@ -215,22 +219,22 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArg
         return at;
     };
     const uint64_t earlier = ((uint64_t)1 << lane) - 1;
-    for (int b0 = 0; b0 < a.B; b0 += kSortChunk) {
-        if (a.B > kSortChunk)
+    for (int b0 = 0; b0 < a.B; b0 += kChunk) {
+        if (a.B > kChunk)
             sort_load(a, b0, id, none);
-        for (int h = 0; h < hots; ++h) {
+        for (int h = 0; EACH > 1 && h < hots; ++h) {
             const int one = hot[h];
             int mine = 0, all;
 #pragma unroll
-            for (int k = 0; k < kSortEach; ++k)
+            for (int k = 0; k < EACH; ++k)
                 mine += __popcll(__ballot(id[k] == (uint32_t)one));
             int p = places(mine, all) + next[one];
 #pragma unroll
-            for (int k = 0; k < kSortEach; ++k) {
+            for (int k = 0; k < EACH; ++k) {
                 const uint64_t hit = __ballot(id[k] == (uint32_t)one);
                 if (hit >> lane & 1) {
                     const int to = p + __popcll(hit & earlier);
-                    a.order[to] = sort_place(b0, k);
+                    a.order[to] = sort_place<EACH>(b0, k);
                     a.sorted[to] = (one << a.shift) + blockIdx.x;
                     id[k] = kSortOther;
                 }
@@ -242,14 +246,14 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArg
         }
         int mine = 0, entries;
 #pragma unroll
-        for (int k = 0; k < kSortEach; ++k)
+        for (int k = 0; k < EACH; ++k)
             mine += __popcll(__ballot(id[k] != kSortOther));
         int at = places(mine, entries);
 #pragma unroll
-        for (int k = 0; k < kSortEach; ++k) {
+        for (int k = 0; k < EACH; ++k) {
             const uint64_t hit = __ballot(id[k] != kSortOther);
             if (hit >> lane & 1)
-                list[at + __popcll(hit & earlier)] = id[k] << 14 | (uint32_t)sort_place(0, k);
+                list[at + __popcll(hit & earlier)] = id[k] << 14 | (uint32_t)sort_place<EACH>(0, k);
             at += __popcll(hit);
         }
         __syncthreads();
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArg
                 const int place = next[one];
                 if (which == one) {
                     const int p = place + __popcll(same & earlier);
-                    a.order[p] = b0 + (int)(entry & (kSortChunk - 1));
+                    a.order[p] = b0 + (int)(entry & (kChunk - 1));
                     a.sorted[p] = (one << a.shift) + blockIdx.x;
                 }
                 next[one] = place + __popcll(same);  // (by every lane: the next read is its own)
@@ -373,7 +377,7 @@ __device__ __forceinline__ void sum_run(const EmbedArgs &a, int run, int c)
 // chunks are numbered within 31 bits and divided by multiplication (245 us and more
 // otherwise), and the row's lane is looked for, by the scalar unit where a wave is in
 // one row, while the flags are under way.  They share a launch with the sums, whose
-// loads run beside them (3333 rows, V 50257, H 1111: 62 us, 75 in two launches).
+// loads run beside them (3333 rows, V 50257, H 1111: 61 us, 75 in two launches).
 // ---------------------------------------------------------------------------
 struct ZeroRows {
     int32_t first, rows;   // of the table, rows * chunks < 2^31
@@ -562,6 +566,18 @@ hipError_t sums(const EmbedArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int EACH>
+hipError_t sort(const EmbedArgs &a, hipStream_t s)
+{
+    constexpr int kLds = kSortRange * 4 + kSortThreads * EACH * 4;
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(embed_sort_kernel<EACH>), kLds, allowed);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((embed_sort_kernel<EACH>), dim3(1u << a.shift), dim3(kSortThreads), kLds, s, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_embed(const EmbedArgs &a, hipStream_t s)
@@ -589,14 +605,11 @@ bool embed_grad_fits(int32_t B, int32_t H)
            ((int64_t)H + kJoinColumns - 1) / kJoinColumns <= 65535;
 }
 
+// As few IDs per thread as one chunk needs: 300 tokens' gradient (V 1500, H 300, bf16) takes
+// 14.4 us, 2000 tokens' 17.2; with 16 throughout 17.6 and 19.5.
 hipError_t launch_embed_sort(const EmbedArgs &a, hipStream_t s)
 {
-    static std::atomic<uint64_t> allowed{0};
-    const hipError_t e = allow_lds(reinterpret_cast<const void *>(embed_sort_kernel), kSortLds, allowed);
-    if (e != hipSuccess)
-        return e;
-    hipLaunchKernelGGL(embed_sort_kernel, dim3(1u << a.shift), dim3(kSortThreads), kSortLds, s, a);
-    return hipGetLastError();
+    return a.B <= kSortThreads ? sort<1>(a, s) : a.B <= 4 * kSortThreads ? sort<4>(a, s) : sort<kSortEach>(a, s);
 }
 
 hipError_t launch_embed_sums(const EmbedArgs &a, hipStream_t s)

@@ -608,8 +608,9 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(const VerifyArgs 
                 total += wave_sum(weight(c0 + lane));
             if (!(total > 0.0))
                 continue;
-            // (a number outside [0, 1) draws the first or the last column)
-            goal = (u > 0.f ? (double)u : 0.0) * total;
+            // (a number outside [0, 1) draws the first or the last column: no sum passes
+            // infinity, but those below may pass the total, which is added in another order)
+            goal = u >= 1.f ? (double)INFINITY : (u > 0.f ? (double)u : 0.0) * total;
             double behind = 0.0;
             for (int c0 = 0; c0 < a.draws; c0 += 64) {
                 const double v = c0 == 0 ? first : weight(c0 + lane), to = behind + wave_upto(v);

@@ -348,3 +348,30 @@ def test_refusals_of_the_binding(require_gpu):
             (call(ws=torch.empty(16, dtype=torch.uint8, device="cuda")), sb.SbError)):
         with pytest.raises(error):
             f()
+
+
+@pytest.mark.parametrize("dtype", [F, H16])
+@pytest.mark.parametrize("V", [1500, 40965, 151936])
+@pytest.mark.parametrize("u", [1.0, 1.0 + 2.0 ** -23, 7.0, float("inf")])
+def test_numbers_from_one_up_draw_the_last_token(require_gpu, u, V, dtype):
+    """The last columns have shares of about e^-60 of the whole, which no sum of it
+    shows: still the last of them that can be drawn is, not the one where a
+    cumulative sum first reaches the whole."""
+    N = 48
+    for how in ("row", "without", "less"):
+        n = 0 if how == "row" else 1
+        s = make([n] * N, n, V, dtype, how == "less", 61, near=0.5, temperature=None)
+        s["u"].fill_(float("nan"))  # accepts no draft
+        s["u_next"].fill_(u)
+        s["target"][:, -300:] -= 60
+        last = V - 1
+        if n:
+            s["tokens"].fill_(0)
+        if how == "less":
+            # q is below p in the tail by e^-19 or less, but for its last two columns
+            s["draft"][:, -300:] = s["target"][::2, -300:] - 20
+            s["draft"][:, -2:] += 40
+            last = V - 3
+        out, accepted = run(s)
+        off = np.nonzero(out[:, 0] != last)[0]
+        assert not len(off) and not accepted.any(), (how, off, out[off, 0])

@@ -228,7 +228,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const EmbedArg
 #pragma unroll
             for (int k = 0; k < EACH; ++k)
                 mine += __popcll(__ballot(id[k] == (uint32_t)one));
-            int p = places(mine, all) + next[one];
+            int p = places(mine, all);
+            p += next[one];  // (behind the barriers that make it whole)
 #pragma unroll
             for (int k = 0; k < EACH; ++k) {
                 const uint64_t hit = __ballot(id[k] == (uint32_t)one);

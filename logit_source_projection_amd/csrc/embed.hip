@@ -308,6 +308,7 @@ __device__ __forceinline__ void store_row(const EmbedArgs &a, T *to, int n, cons
 constexpr int kRunLoads = 8;
 static_assert(kEmbedRun + kEmbedLong <= 64 && kEmbedPiece <= 64 && kEmbedPiece % kEmbedRun == 0,
               "the positions of a run and of a piece are a wave's lanes");
+static_assert(kEmbedPiece <= kEmbedLong, "an ID that is summed in pieces spans two or more of them");
 
 template <typename TT, typename TO, bool ADD>
 __device__ __forceinline__ void sum_run(const EmbedArgs &a, int run, int c)
@@ -323,11 +324,10 @@ __device__ __forceinline__ void sum_run(const EmbedArgs &a, int run, int c)
     const int first = start[0], behind = start[1];
     const bool many = behind - first > kEmbedLong;
     const bool mine = p < total && (many ? p0 % kEmbedPiece == 0 && lane < kEmbedPiece : first >= p0 && first < p0 + kEmbedRun);
-    const bool whole = !many || (first >= p0 && behind <= p0 + kEmbedPiece);
     const uint64_t stores = __ballot(mine && (p + 1 == behind || (many && lane == kEmbedPiece - 1)));
-    const uint64_t wholes = __ballot(whole);
-    char *to = whole ? reinterpret_cast<char *>(table_row<TT>(a, id))
-                     : reinterpret_cast<char *>(a.part + (2 * (int64_t)(p0 / kEmbedPiece) + (first >= p0)) * a.ldpart);
+    const uint64_t wholes = __ballot(!many);
+    char *to = many ? reinterpret_cast<char *>(a.part + (2 * (int64_t)(p0 / kEmbedPiece) + (first >= p0)) * a.ldpart)
+                    : reinterpret_cast<char *>(table_row<TT>(a, id));
     const int to_low = (int)reinterpret_cast<uint64_t>(to), to_high = (int)(reinterpret_cast<uint64_t>(to) >> 32);
     float sum[8] = {};
     uint64_t todo = __ballot(mine);

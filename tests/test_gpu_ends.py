@@ -239,3 +239,42 @@ def test_tensors_of_several_devices_are_refused(require_gpu):
             else:
                 sb.sb_embed(sb.Table(other.cuda()), torch.zeros(40, dtype=torch.int32), other.cuda())
     assert cases
+
+
+def test_all_at_once_every_round(require_gpu):
+    """As above, but every round has other inputs, and its outputs are kept: copied on the
+    operator's own stream before the next round writes them, they equal those of the same
+    inputs alone."""
+    rounds = 12
+    cases = {name: operators()[name] for name in NAMES}  # (of one set, two read the same rows)
+    fresh = {name: [[t.clone() for t in inputs]] for name, (inputs, _, _, _) in cases.items()}
+    want = {name: [] for name in cases}
+    for name, (inputs, call, outputs, _) in cases.items():
+        for r in range(rounds):
+            if r:
+                change(inputs, 100 + r)
+                fresh[name].append([t.clone() for t in inputs])
+            for t in outputs:
+                t.fill_(-7)
+            call(None, None)
+            torch.cuda.synchronize()
+            want[name].append([t.clone() for t in outputs])
+        assert any(not torch.equal(a, b) for a, b in zip(want[name][0], want[name][1])), name
+    streams = {name: torch.cuda.Stream() for name in cases}
+    spaces = {name: case[3]() if case[3] else None for name, case in cases.items()}
+    got = {name: [] for name in cases}
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        for name, (inputs, call, outputs, _) in cases.items():
+            with torch.cuda.stream(streams[name]):
+                for t, value in zip(inputs, fresh[name][r]):
+                    t.copy_(value)
+                for t in outputs:
+                    t.fill_(-5)
+                call(None, spaces[name])
+                got[name].append([t.clone() for t in outputs])
+    torch.cuda.synchronize()
+    for name in cases:
+        for r in range(rounds):
+            for a, b in zip(want[name][r], got[name][r]):
+                assert torch.equal(a, b), (name, r)

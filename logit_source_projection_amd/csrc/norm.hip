@@ -288,7 +288,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormArgs a)
         return;
     if (TEAM != 0) {
         // the workgroup's teams: those of a wave, then the waves in order
-        __shared__ float joined[kWaves][2][TEAM ? 8 * TEAM * UNITS : 1];
+        __shared__ alignas(16) float joined[kWaves][2][TEAM ? 8 * TEAM * UNITS : 1];
         const int wave = threadIdx.x >> 6;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k)
@@ -582,7 +582,7 @@ constexpr int kJoinColumns = 32, kJoinQuads = kJoinColumns / 4, kJoinRuns = kThr
 
 __global__ __launch_bounds__(kThreads) void norm_params_kernel(const NormArgs a)
 {
-    __shared__ float shares[kJoinRuns][kJoinColumns];
+    __shared__ alignas(16) float shares[kJoinRuns][kJoinColumns];
     const bool bias = blockIdx.y != 0;
     void *to = bias ? a.dbias : a.dweight;
     if (!to)

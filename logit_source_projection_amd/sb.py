@@ -877,6 +877,8 @@ def _space(ws, nbytes_fn, index, stream):
     that holds it."""
     if ws is None:
         device = torch.device("cuda", index)
+        if stream is not None:
+            _stream_on(stream, device)  # (one of another device is refused here already)
         with _on(device):
             ws = _workspace(nbytes_fn, None, device, stream)
     return _buffer(ws, "ws", torch.uint8, 0, index), ws.numel(), ws

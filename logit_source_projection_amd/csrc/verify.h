@@ -14,7 +14,7 @@ constexpr int kVerifyChunk = 8192, kVerifyDraw = 2048;
 constexpr int kVerifyDone = 32;
 
 // What a chunk of a row holds.  Sampled rows: the largest logit (NaN where one is
-// NaN or +inf) and the sum of exp(z / temperature) against a power of two that goes by it.
+// NaN or +inf) and the sum of exp((z - that one) / temperature).
 // Greedy rows: the best logit and its column.
 struct RowPart {
     double sum;

@@ -375,3 +375,44 @@ def test_numbers_from_one_up_draw_the_last_token(require_gpu, u, V, dtype):
         out, accepted = run(s)
         off = np.nonzero(out[:, 0] != last)[0]
         assert not len(off) and not accepted.any(), (how, off, out[off, 0])
+
+
+@pytest.mark.parametrize("dtype", [F, H16])
+@pytest.mark.parametrize("t", [None, 0.7, 1e-12])
+def test_shares_of_equal_logits_are_exact(require_gpu, t, dtype):
+    """2^k equal logits and nothing else have shares of 2^-k exactly, whatever the logits
+    are: u q < p is false where both sides are equal, and true where u is the next lower
+    number."""
+    N, V = 240, 20000
+    z = torch.linspace(-40, 40, N, device="cuda").to(dtype)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for k, kq in ((0, None), (1, None), (2, None), (5, None), (9, None), (3, 1), (6, 2)):
+        s = make([1] * N, 1, V, dtype, kq is not None, 71, temperature=t)
+        s["target"].fill_(-float("inf"))
+        # (from chunk to chunk, the drafted token among them)
+        at = torch.randperm(V, device="cuda", generator=g)[:2 ** k]
+        s["target"][::2, at] = z[:, None]
+        s["target"][1::2, 0] = 0
+        s["tokens"].fill_(int(at[0]))
+        border = 2.0 ** -k
+        if kq is not None:
+            s["draft"].fill_(-float("inf"))
+            s["draft"][:, at[:2 ** kq]] = -z[:, None]
+            border = 2.0 ** (kq - k)
+        for u, want in ((border, 0), (float(np.nextafter(np.float32(border), np.float32(0))), 1)):
+            s["u"].fill_(u)
+            accepted = run(s)[1]
+            assert (accepted == want).all(), (k, kq, u, np.nonzero(accepted != want)[0])
+
+
+@pytest.mark.parametrize("z", [-17.3, 0.1, 1e6])
+def test_borders_of_a_flat_row_of_any_logit(require_gpu, z):
+    """Shares of 2^-14 exactly: a multiple k / V of the whole draws token k, the number
+    below it the one before."""
+    N, V = 512, 16384
+    s = make([0] * N, 0, V, F, False, 1, 0.0, 0.0, None)
+    s["target"].fill_(z)
+    k = torch.linspace(0, V - 1, N, device="cuda").round()
+    for u, token in ((k / V, k), (torch.nextafter(k / V, torch.tensor(-1.0, device="cuda")), (k - 1).clamp(min=0))):
+        s["u_next"] = u
+        assert np.array_equal(run(s)[0][:, 0], token.long().cpu().numpy())

@@ -61,9 +61,9 @@
  *    read behind the last value has no effect.
  *  - The workspace is scratch owned by the call until its work completes on
  *    the stream: its contents on entry do not matter, and nothing in it is
- *    valid afterwards.  Every workspace starts with the same fixed region
- *    (8,192 bytes) of per-tile counters for heads split into K slices (see
- *    below); a call on a split head clears the counters it uses on `stream`
+ *    valid afterwards.  The workspaces of calls on a head start with the same
+ *    fixed region (8,192 bytes) of per-tile counters for heads split into K
+ *    slices (see below); a call that counts clears its counters on `stream`
  *    before its head kernel runs (by a small clearing launch, or by the
  *    hidden-row copy for 33 <= B <= 64), so a workspace sized for the
  *    largest call serves calls of any shape, surface or entry point in any
@@ -486,11 +486,13 @@ sb_status sb_int8_logits(const sb_int8_desc *desc, void *out, int dtype, int64_t
  *   g = dy * weight,  dx = rstd * (g - sum_h g / H - xh * sum_h (g * xh) / H)
  *   dweight = sum_b dy * xh,   dbias = sum_b dy
  * Sums are fp32, in orders fixed by B, H and the types; every result is rounded
- * once to its type.  NaN and infinities follow IEEE rules and stay in their
- * row (in the parameters' gradients in their column): a row that holds one is
- * NaN.  A row whose values are all the same has y = bias for eps > 0 (rounding
- * of the mean aside) and NaN for eps = 0.  Finite rows whose sums or squares
- * overflow fp32 are outside the contract (values up to 10^15 are safe).
+ * once to its type.  NaN and infinities follow IEEE rules: a row of x that holds
+ * one is NaN in y, rstd and dx, and makes all of dweight NaN; one in dy leaves
+ * nothing finite in its row of dx, and in dweight and dbias stays in its column.
+ * Other rows of y and dx are not touched by either.  A row whose values are all
+ * the same has y = bias for eps > 0 (rounding of the mean aside) and NaN for
+ * eps = 0.  Finite rows whose sums or squares overflow fp32 are outside the
+ * contract (values up to 10^15 are safe).
  * ---------------------------------------------------------------------------
  */
 
@@ -628,7 +630,8 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
  *   the next token is drawn from max(p_j - q_j, 0) of the first rejected draft
  *   j, or from p_n if all are accepted: the lowest column whose cumulative sum
  *   passes u_next times the whole
- * Accepted drafts and next token then follow the target's distribution exactly.
+ * Over uniform random numbers accepted drafts and next token follow the target's
+ * distribution, whatever the draft's is.
  *  - Without draft logits a draft counts as certain: q_j(x_j) = 1.
  *  - Where max(p_j - q_j, 0) is 0 everywhere the token is drawn from p_j.
  *  - A temperature that is not > 0 (0, negative, NaN) is greedy: draft j is
@@ -644,7 +647,10 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
  *    p_j(x_j) > 0, NaN none; u_next below 0 or NaN counts as 0, and from 1 up
  *    it draws the last token that can be drawn.
  *  - Everything behind the logits is computed in 64 bits, in an order fixed by
- *    V alone: the same logits and numbers give the same tokens in any batch.
+ *    V alone: the same logits and numbers give the same tokens in any batch.  An
+ *    exponential is within 4 * 10^-14 of itself (of a share below 10^-100: 2 * 10^-13),
+ *    and exactly 1 of the largest logit: 2^n equal logits alone have shares of 2^-n.
+ *    One below 2^-1074 is 0, as that of -inf.
  * ---------------------------------------------------------------------------
  */
 

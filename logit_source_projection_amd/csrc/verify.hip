@@ -37,7 +37,10 @@ enum How : int {
 };
 
 // 2^f of -1/2 <= f <= 1/2, exactly 1 of 0: 1 + f g(f), g through (2^f - 1) / f at the 9
-// Chebyshev nodes; off by 3.7e-14 of it.
+// Chebyshev nodes; off by up to 3.7e-14 of it.  A logit is off by its own rounding, 2^-24
+// of itself in fp32, and a random number falls between a share and the one found once in
+// 10^7.  With 10 nodes (5.7e-16) 64 sequences of 7 drafts, V 151936 in fp32, take 148 us, 144
+// with 9.
 __device__ __forceinline__ double power_within(double f)
 {
     double e = 1.02031210633917290e-07;
@@ -185,10 +188,13 @@ __device__ __forceinline__ const T *row_at(const void *rows, int64_t ld, int64_t
 // Every chunk of every row that a sequence may need: the largest logit, and the sum of
 // the powers or, of a greedy sequence, the largest logit's column.  Workgroups take one
 // chunk after the other, the next one's loads under way while the powers of one are
-// summed.  64 sequences of 7 drafts with draft logits, V 151936 in fp32: 111 us, of which
-// the 583 MB alone take 90 and the 64-bit instructions as long.  Twice as many workgroups
-// as are resident: those whose rows are not there leave room for others (17 ragged
-// sequences, V 50257: the call takes 23.4 us, with as many as are resident 25.6).
+// summed.  64 sequences of 7 drafts with draft logits, 16 of them greedy, V 151936 in fp32:
+// 110 to 123 us.  The 515 MB that they read take 79 at 6.5 TB/s; 41.2 million wave
+// instructions, 23 for each logit whose power is summed (17 are the power and its sum),
+// keep the SIMDs busy for longer than that, and a third of the waves' cycles are waits.
+// Twice as many workgroups as are resident: those whose rows are not there leave room for
+// others (17 ragged sequences, V 50257: the call takes 22.1 us, with as many as are resident
+// 24.5; the 64 sequences 144.3 and 145.8).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kRowGroups = 2048;
 
@@ -450,8 +456,8 @@ __device__ __forceinline__ double wave_upto(double v)
 // them.  The last of a sequence's workgroups to be done (none waits for another) finds
 // the one whose cumulative sum passes the random number's share of the whole, then the
 // column.
-// 2048 columns, one unit to a thread: a call on one sequence (V 151936, fp32) takes 16.9
-// us, on 64 of them 131.8; with 4096 18.0 and 135.0.
+// 2048 columns, one unit to a thread: a call on one sequence (V 151936, fp32) takes 16.8
+// us, on 64 of them 144.3; with 4096 18.0 and 146.0.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Rest {

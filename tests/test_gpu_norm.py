@@ -218,3 +218,26 @@ def test_refusals_of_the_binding(require_gpu):
             (lambda: sb.sb_layer_norm_grad(n, dy.expand(4, 16)[:1].expand(4, 16), v, v, dx=y), sb.SbError)):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("B,H", [(40, 64), (40, 1111), (300, 1111), (300, 5120), (40, 20000)])
+def test_where_values_that_are_not_finite_go_in_the_gradient(require_gpu, B, H, bad):
+    x, dy, w, b = make(B, H, F, F, F, 12)
+    clean = run(x, dy, w, b)
+    rows = torch.arange(B, device="cuda") != 17
+    columns = torch.arange(H, device="cuda") != H // 2
+    # one in x: its rows of y, rstd and dx, and all of dweight
+    hit = matrix(B, H, F, 0.0)[1].copy_(x)
+    hit[17, H // 2] = bad
+    y, mean, rstd, dx, dw, db = run(hit, dy, w, b)
+    for t, c in ((y, clean[0]), (rstd, clean[2]), (dx, clean[3])):
+        assert bool(t[17].isnan().all()) and torch.equal(t[rows], c[rows])
+    assert bool(dw.isnan().all()) and torch.equal(db, clean[5])
+    # one in dy: its row of dx, and its column of dweight and dbias
+    hit = matrix(B, H, F, 0.0)[1].copy_(dy)
+    hit[17, H // 2] = bad
+    _, _, _, dx, dw, db = run(x, hit, w, b)
+    assert not dx[17].isfinite().any() and torch.equal(dx[rows], clean[3][rows])
+    for t, c in ((dw, clean[4]), (db, clean[5])):
+        assert not t[H // 2].isfinite() and torch.equal(t[columns], c[columns])

@@ -648,8 +648,8 @@ sb_status sb_embed_grad(const sb_table_desc *desc, const int32_t *ids, int32_t B
  *    it draws the last token that can be drawn.
  *  - Everything behind the logits is computed in 64 bits, in an order fixed by
  *    V alone: the same logits and numbers give the same tokens in any batch.  An
- *    exponential is within 4 * 10^-14 of itself (of a share below 10^-100: 2 * 10^-13),
- *    and exactly 1 of the largest logit: 2^n equal logits alone have shares of 2^-n.
+ *    exponential is within 5 * 10^-14 of itself (below 10^-20: 2 * 10^-13) and
+ *    exactly 1 of the largest logit: 2^n equal logits alone have shares of 2^-n.
  *    One below 2^-1074 is 0, as that of -inf.
  * ---------------------------------------------------------------------------
  */

@@ -191,7 +191,8 @@ __device__ __forceinline__ const T *row_at(const void *rows, int64_t ld, int64_t
 // summed.  64 sequences of 7 drafts with draft logits, 16 of them greedy, V 151936 in fp32:
 // 110 to 123 us.  The 515 MB that they read take 79 at 6.5 TB/s; 41.2 million wave
 // instructions, 23 for each logit whose power is summed (17 are the power and its sum),
-// keep the SIMDs busy for longer than that, and a third of the waves' cycles are waits.
+// take 90 at the 5.2 cycles each that a loop of powers alone takes, and a third of the
+// waves' cycles are waits.
 // Twice as many workgroups as are resident: those whose rows are not there leave room for
 // others (17 ragged sequences, V 50257: the call takes 22.1 us, with as many as are resident
 // 24.5; the 64 sequences 144.3 and 145.8).
